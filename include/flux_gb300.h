@@ -18,6 +18,10 @@
  * the experts (COMET's EP x TP ratio, same section):
  *     dispatch by expert + grouped GEMM                     flux_moe_ep_dispatch_gemm
  *     grouped GEMM + top-k weighted combine to the owners    flux_moe_ep_gemm_combine
+ * and what a transformer block needs next to these layers:
+ *     norms before and after a block, gate, residual         flux_block_norm(_bwd)
+ *     the router's losses, counts and score gradient         flux_moe_balance_loss, flux_moe_router_bwd
+ *     products of few rows with 4-bit weights                flux_w4_gemv, flux_moe_w4_layer0 / _layer1
  * plus the plain non-split GEMM that the effective-communication-time metric
  * ECT = OverallTime - GEMM_non-split is measured against (paper review,
  * section 三, "核心公式"): flux_gemm.  The operator list is the one the Flux
@@ -67,6 +71,8 @@ extern "C" {
 
 #define FLUX_MAX_RANKS 16
 #define FLUX_MAX_EXPERTS 1024
+#define FLUX_BLOCK_MAX_H 16384 /* widest row of flux_block_norm */
+#define FLUX_W4_MAX_ROWS 1024  /* most rows (tokens x topk) of a product with 4-bit weights */
 
 typedef enum {
   FLUX_OK = 0,
@@ -509,6 +515,178 @@ flux_status_t flux_moe_ep_gemm_combine(int R, int tp, int T, int H, int F, int E
                                        const int32_t* slot_to_row, const int32_t* row_to_slot,
                                        void* const* out, void* workspace, size_t workspace_bytes,
                                        const flux_opts_t* opts, void* stream);
+
+/* ---------------------------------------------------------------- norms around a block
+ *
+ * One pass over the residual stream between two blocks of a transformer: the
+ * finished block's output y is normalised, gated and added to the scaled
+ * residual stream x, and the sum x' is normalised for the next block.  Per
+ * token, with means over the H columns and everything in fp32:
+ *     z  = y r_y w_post,   r_y = 1 / sqrt(mean(y^2) + eps)   (post_norm; else z = y)
+ *     x' = rho x + g z
+ *     u  = x' r_x w_pre,   r_x = 1 / sqrt(mean(x'^2) + eps)
+ * x' and u are rounded once each; u is computed from the unrounded x'. */
+
+/*   x_shards[s]  device, [T/R x H]: the rows of the residual stream owned by rank s
+ *                (as flux_ag_gemm's x_shards and flux_gemm_rs's out)
+ *   y_shards     [T/R x H] each: the block's output; the array NULL = no block
+ *                before this norm (x' = x; then w_post, gate, res_scale, x_out
+ *                and rstd_y are NULL too)
+ *   post_norm    nonzero: y is normalised (ignored without y)
+ *   w_post       device [H] in dtype, or NULL = ones; only with post_norm
+ *   gate         device [gate_rows x gate_cols] in dtype, or NULL = 1.  Token t of
+ *                the T (over all shards) uses row t / (T / gate_rows); gate_cols
+ *                is H (a gate per channel) or 1.  gate_rows = 1: one gate for
+ *                all tokens; gate_rows = T: one per token.  T % gate_rows == 0.
+ *                Without a gate both sizes are ignored.
+ *   res_scale    device float: rho, or NULL = 1
+ *   w_pre        device [H] in dtype, or NULL = ones
+ *   x_out[s]     x' [T/R x H]; may be x_shards[s] or y_shards[s]
+ *   u_out[s]     u  [T/R x H], may be y_shards[s]; the array NULL = no next norm (then
+ *                w_pre and rstd_x are NULL too)
+ *   rstd_y, rstd_x  device float[T]: r_y and r_x for the backward pass, or NULL
+ * Requires T % R == 0, H % 8 == 0 and H <= FLUX_BLOCK_MAX_H (else
+ * FLUX_ERR_UNSUPPORTED), eps finite and >= 0.  A call with neither y nor u,
+ * or with an argument of a part that it leaves out, returns
+ * FLUX_ERR_INVALID_ARG.  Needs no workspace; deterministic. */
+flux_status_t flux_block_norm(int R, int T, int H, flux_dtype_t dtype, int post_norm, int gate_rows,
+                              int gate_cols, float eps, const void* const* x_shards,
+                              const void* const* y_shards, const void* w_post, const void* gate,
+                              const float* res_scale, const void* w_pre, void* const* x_out,
+                              void* const* u_out, float* rstd_y, float* rstd_x, void* stream);
+
+/* Bytes of workspace flux_block_norm_bwd needs; gate_rows, gate_cols 0 without a
+ * gate.  0 for invalid sizes. */
+size_t flux_block_norm_workspace_size(int T, int H, int gate_rows, int gate_cols);
+
+/* Gradients of flux_block_norm from those of x' and u.
+ *   x_shards .. w_pre  as the forward call had them (x and y unchanged)
+ *   rstd_y, rstd_x     device float[T] as the forward call wrote them (rstd_y
+ *                      with y and post_norm, rstd_x with du)
+ *   dx_out[s]    gradient of x' [T/R x H]; the array NULL = zeros
+ *   du[s]        gradient of u [T/R x H]; the array NULL = the call had no u
+ *   dx[s], dy[s] device [T/R x H] in dtype (dy NULL without y); each may be dx_out[s]
+ *                or du[s]
+ *   dw_post      device float[H]          dgate  device float[gate_rows x gate_cols]
+ *   dres_scale   device float             dw_pre device float[H]
+ *                written in fp32; NULL = not wanted
+ * The sums over tokens are taken in a fixed order: repeat calls give the same
+ * bits.  Workspace: flux_block_norm_workspace_size(). */
+flux_status_t flux_block_norm_bwd(int R, int T, int H, flux_dtype_t dtype, int post_norm,
+                                  int gate_rows, int gate_cols, const void* const* x_shards,
+                                  const void* const* y_shards, const void* w_post, const void* gate,
+                                  const float* res_scale, const void* w_pre, const float* rstd_y,
+                                  const float* rstd_x, const void* const* dx_out,
+                                  const void* const* du, void* const* dx, void* const* dy,
+                                  float* dw_post, float* dgate, float* dres_scale, float* dw_pre,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- the router in training */
+
+/* Balance and z losses of T tokens over E experts, with the counts they use.
+ * The tokens are `seqs` sequences of T / seqs tokens each; with p = softmax of
+ * a token's E scores, n_s the kept tokens of sequence s, n all kept tokens,
+ * c[s,e] the kept slots of sequence s that went to expert e:
+ *     P[s,e]  = sum of p over the kept tokens of s / n_s
+ *     loss[0] = balance_coef E / (topk seqs) sum_s sum_e (c[s,e] / n_s) P[s,e]
+ *     loss[1] = z_coef / n sum over kept tokens of lse^2,  lse = log sum_e exp(score)
+ * (a sequence with no kept token adds nothing; seqs = 1: one loss over the batch).
+ *   logits      device float32[T x E], as flux_moe_topk_gate takes them
+ *   topk_ids    device int32[T x topk] from that call; an id outside [0, E) is
+ *               counted nowhere and records FLUX_ERR_INVALID_ARG in the workspace
+ *   token_mask  device uint8[T]: 0 = padding, left out of everything; NULL = none
+ *   loss        device float[2]            counts  device int32[seqs x E]: c
+ *   probs       device float[seqs x E]: P (0 for an empty sequence)
+ *   tokens      device int32[seqs + 1]: n_s, then n
+ *   lse         device float[T], for every token
+ * Odd rows follow the gate: a NaN score counts as -inf; where the largest score
+ * is infinite, the scores equal to it share p equally, and the token has no z
+ * term.  Deterministic.  Requires 1 <= topk <= E <= FLUX_MAX_EXPERTS, seqs >= 1,
+ * T % seqs == 0, finite coefficients.
+ * Workspace: flux_moe_balance_workspace_size(). */
+flux_status_t flux_moe_balance_loss(int T, int E, int topk, int seqs, float balance_coef,
+                                    float z_coef, const float* logits, const int32_t* topk_ids,
+                                    const uint8_t* token_mask, float* loss, int32_t* counts,
+                                    float* probs, int32_t* tokens, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace flux_moe_balance_loss needs; 0 for invalid sizes. */
+size_t flux_moe_balance_workspace_size(int T, int E, int topk, int seqs);
+
+/* Gradient of the router scores from the two losses and from the gate weights:
+ *   dlogits[t,e] = dloss[0] d loss[0] / d score + dloss[1] d loss[1] / d score
+ *                + sum over the slots j of t that went to e of
+ *                  w_j (dweights[t,j] - sum_i w_i dweights[t,i])
+ * (the counts are constants; kept tokens only in the loss terms, every token in
+ * the gate's).  A token whose largest score is infinite gets zeros.
+ *   logits .. token_mask  as flux_moe_balance_loss had them
+ *   topk_ids, topk_weights  as flux_moe_topk_gate wrote them (no expert twice in a
+ *               token; needed with dweights only)
+ *   lse, counts, tokens  as flux_moe_balance_loss wrote them
+ *   dloss       device float[2], or NULL = ones
+ *   dweights    device float[T x topk]: gradient of topk_weights, or NULL = zeros
+ *   dlogits     device float[T x E] */
+flux_status_t flux_moe_router_bwd(int T, int E, int topk, int seqs, float balance_coef, float z_coef,
+                                  const float* logits, const int32_t* topk_ids,
+                                  const float* topk_weights, const uint8_t* token_mask,
+                                  const float* lse, const int32_t* counts, const int32_t* tokens,
+                                  const float* dloss, const float* dweights, float* dlogits,
+                                  void* stream);
+
+/* ---------------------------------------------------------------- few rows, 4-bit weights
+ *
+ * W[k,n] = scale[k / group, n] (code[n,k] - 8), codes 0..15: the decode step of an
+ * MLP or of an MoE layer with weights at a quarter of the bytes.
+ *   q        device bytes [E x N x ceil(K / 128) x 64]: the codes of column n in
+ *            input order, 128 inputs in 64 bytes: for each c of 0..3 sixteen
+ *            bytes, in them for each j of 0..3 a little-endian 32-bit word whose
+ *            nibble i (bits 4i..4i+3) is the input 32 j + 8 c + 2 i for i < 4
+ *            and 32 j + 8 c + 2 (i - 4) + 1 for i >= 4.  Codes past K are ignored.
+ *   scales   device [E x ceil(K / group) x N] in dtype
+ * Sums in fp32, the scale of a group applied to its exact sum of x (code - 8).
+ * Requires N % 8 == 0, K % 8 == 0, group % 32 == 0 (FLUX_ERR_UNSUPPORTED).  More
+ * than FLUX_W4_MAX_ROWS rows (M, or T topk) return FLUX_ERR_UNSUPPORTED: such
+ * products are bound by arithmetic and belong to the 16-bit GEMMs. */
+
+/* Bytes of q for E experts of K inputs and N outputs; 0 for invalid sizes. */
+size_t flux_w4_weight_bytes(int E, int K, int N);
+
+/* Bytes of workspace a product of `rows` rows (M, or T topk) needs; 0 for invalid sizes. */
+size_t flux_w4_workspace_size(int rows, int N, int K, int E);
+
+/* q and scales from 16-bit weights w, device [E x K x N] (one expert's matrix as the
+ * GEMMs take it): scale = largest magnitude of the group / 7, rounded to dtype;
+ * code = 8 + the nearest integer to w / scale, within 0..15 (8 where the scale is
+ * 0).  The weights have to be finite. */
+flux_status_t flux_w4_quantize(int E, int K, int N, int group, flux_dtype_t dtype, const void* w,
+                               void* q, void* scales, void* stream);
+
+/* out[M x N] = x[M x K] . W (E = 1).  K = 0 writes zeros. */
+flux_status_t flux_w4_gemv(int M, int N, int K, int group, flux_dtype_t dtype, const void* x,
+                           const void* q, const void* scales, void* out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* MoE layer0 of few tokens: h[t topk + j] = x[t] . W1[topk_ids[t,j]].
+ *   x device [T x H];  q1, scales1: E matrices of K = H, N = F
+ *   topk_ids device int32[T x topk] (flux_moe_topk_gate)
+ *   h device [T topk x F], rows in slot order (no routing call is needed)
+ * An id outside [0, E) gives a row of zeros and records FLUX_ERR_INVALID_ARG in
+ * the workspace. */
+flux_status_t flux_moe_w4_layer0(int T, int H, int F, int E, int topk, int group, flux_dtype_t dtype,
+                                 const void* x, const void* q1, const void* scales1,
+                                 const int32_t* topk_ids, void* h, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* MoE layer1 of few tokens: out[t] = sum_j topk_weights[t,j] (h[t topk + j] . W2[topk_ids[t,j]]),
+ * summed in slot order in fp32 and rounded once.
+ *   h device [T topk x F], rows in slot order;  q2, scales2: E matrices of K = F, N = H
+ *   topk_ids, topk_weights as flux_moe_topk_gate wrote them;  out device [T x H]
+ * A slot with an id outside [0, E) adds nothing and records FLUX_ERR_INVALID_ARG
+ * in the workspace. */
+flux_status_t flux_moe_w4_layer1(int T, int H, int F, int E, int topk, int group, flux_dtype_t dtype,
+                                 const void* h, const void* q2, const void* scales2,
+                                 const int32_t* topk_ids, const float* topk_weights, void* out,
+                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- tuning
  *

@@ -7,3 +7,4 @@ links or calls anything here, and this package imports nothing from the
 product path.
 """
 from .flux_oracle import *  # noqa: F401,F403
+from .block_oracle import *  # noqa: F401,F403

@@ -51,6 +51,8 @@ FLUX_OP_AG_GEMM_PUSH = 9
 
 FLUX_MAX_RANKS = 16
 FLUX_MAX_EXPERTS = 1024
+FLUX_BLOCK_MAX_H = 16384
+FLUX_W4_MAX_ROWS = 1024
 FLUX_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 WAIT_SITES = {1: "ready flag", 2: "smem slot free", 3: "smem slot full",
@@ -91,6 +93,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
 _vpp = ctypes.POINTER(ctypes.c_void_p)
+_f = ctypes.c_float
 _opt = ctypes.POINTER(flux_opts_t)
 
 _SIGS = {
@@ -129,6 +132,22 @@ _SIGS = {
                                    _vp, _vp, _vp, _vp, _vp, _sz, _opt, _vp], _i),
     "flux_moe_ep_gemm_combine": ([_i, _i, _i, _i, _i, _i, _i, _i, _vpp, _vpp, _vp, _vp, _vp,
                                   _vp, _vp, _vpp, _vp, _sz, _opt, _vp], _i),
+    "flux_block_norm": ([_i, _i, _i, _i, _i, _i, _i, _f, _vpp, _vpp, _vp, _vp, _vp, _vp, _vpp, _vpp,
+                         _vp, _vp, _vp], _i),
+    "flux_block_norm_workspace_size": ([_i, _i, _i, _i], _sz),
+    "flux_block_norm_bwd": ([_i, _i, _i, _i, _i, _i, _i, _vpp, _vpp, _vp, _vp, _vp, _vp, _vp, _vp,
+                             _vpp, _vpp, _vpp, _vpp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
+    "flux_moe_balance_loss": ([_i, _i, _i, _i, _f, _f, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                               _sz, _vp], _i),
+    "flux_moe_balance_workspace_size": ([_i, _i, _i, _i], _sz),
+    "flux_moe_router_bwd": ([_i, _i, _i, _i, _f, _f, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                             _vp, _vp], _i),
+    "flux_w4_weight_bytes": ([_i, _i, _i], _sz),
+    "flux_w4_workspace_size": ([_i, _i, _i, _i], _sz),
+    "flux_w4_quantize": ([_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp], _i),
+    "flux_w4_gemv": ([_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
+    "flux_moe_w4_layer0": ([_i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
+    "flux_moe_w4_layer1": ([_i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -152,6 +171,8 @@ def _ptr(x):
 
 
 def _ptrs(xs):
+    if xs is None:
+        return None
     arr = (ctypes.c_void_p * len(xs))()
     for i, x in enumerate(xs):
         arr[i] = _ptr(x)
@@ -344,6 +365,88 @@ def flux_moe_ep_gemm_combine(R, tp, T, H, F, E, topk, dtype, h_shards, w2_shards
         _ptr(topk_weights), _ptr(offsets), _ptr(slot_to_row), _ptr(row_to_slot), _ptrs(out),
         _ptr(workspace), _nbytes(workspace), _opts(opts), _stream(stream)),
         "flux_moe_ep_gemm_combine")
+
+
+def flux_block_norm_workspace_size(T: int, H: int, gate_rows: int = 0, gate_cols: int = 0) -> int:
+    return int(_lib.flux_block_norm_workspace_size(T, H, gate_rows, gate_cols))
+
+
+def flux_block_norm(R, T, H, dtype, post_norm, gate_rows, gate_cols, eps, x_shards, y_shards, w_post, gate,
+                    res_scale, w_pre, x_out, u_out, rstd_y=None, rstd_x=None, stream=None) -> None:
+    """Post-norm, gate, residual and the next block's pre-norm in one pass."""
+    _check(_lib.flux_block_norm(R, T, H, dtype, post_norm, gate_rows, gate_cols, eps, _ptrs(x_shards),
+                                _ptrs(y_shards), _ptr(w_post), _ptr(gate), _ptr(res_scale), _ptr(w_pre),
+                                _ptrs(x_out), _ptrs(u_out), _ptr(rstd_y), _ptr(rstd_x), _stream(stream)),
+           "flux_block_norm")
+
+
+def flux_block_norm_bwd(R, T, H, dtype, post_norm, gate_rows, gate_cols, x_shards, y_shards, w_post, gate,
+                        res_scale, w_pre, rstd_y, rstd_x, dx_out, du, dx, dy, dw_post, dgate, dres_scale,
+                        dw_pre, workspace, stream=None) -> None:
+    """Gradients of flux_block_norm."""
+    _check(_lib.flux_block_norm_bwd(
+        R, T, H, dtype, post_norm, gate_rows, gate_cols, _ptrs(x_shards), _ptrs(y_shards), _ptr(w_post),
+        _ptr(gate), _ptr(res_scale), _ptr(w_pre), _ptr(rstd_y), _ptr(rstd_x), _ptrs(dx_out), _ptrs(du),
+        _ptrs(dx), _ptrs(dy), _ptr(dw_post), _ptr(dgate), _ptr(dres_scale), _ptr(dw_pre), _ptr(workspace),
+        _nbytes(workspace), _stream(stream)), "flux_block_norm_bwd")
+
+
+def flux_moe_balance_workspace_size(T: int, E: int, topk: int, seqs: int) -> int:
+    return int(_lib.flux_moe_balance_workspace_size(T, E, topk, seqs))
+
+
+def flux_moe_balance_loss(T, E, topk, seqs, balance_coef, z_coef, logits, topk_ids, token_mask, loss, counts,
+                          probs, tokens, lse, workspace, stream=None) -> None:
+    """Balance and z losses of the router, with the per-expert counts."""
+    _check(_lib.flux_moe_balance_loss(
+        T, E, topk, seqs, balance_coef, z_coef, _ptr(logits), _ptr(topk_ids), _ptr(token_mask), _ptr(loss),
+        _ptr(counts), _ptr(probs), _ptr(tokens), _ptr(lse), _ptr(workspace), _nbytes(workspace),
+        _stream(stream)), "flux_moe_balance_loss")
+
+
+def flux_moe_router_bwd(T, E, topk, seqs, balance_coef, z_coef, logits, topk_ids, topk_weights, token_mask, lse,
+                        counts, tokens, dloss, dweights, dlogits, stream=None) -> None:
+    """Gradient of the router scores from both losses and from the gate weights."""
+    _check(_lib.flux_moe_router_bwd(
+        T, E, topk, seqs, balance_coef, z_coef, _ptr(logits), _ptr(topk_ids), _ptr(topk_weights),
+        _ptr(token_mask), _ptr(lse), _ptr(counts), _ptr(tokens), _ptr(dloss), _ptr(dweights), _ptr(dlogits),
+        _stream(stream)), "flux_moe_router_bwd")
+
+
+def flux_w4_weight_bytes(E: int, K: int, N: int) -> int:
+    return int(_lib.flux_w4_weight_bytes(E, K, N))
+
+
+def flux_w4_workspace_size(rows: int, N: int, K: int, E: int = 1) -> int:
+    return int(_lib.flux_w4_workspace_size(rows, N, K, E))
+
+
+def flux_w4_quantize(E, K, N, group, dtype, w, q, scales, stream=None) -> None:
+    """4-bit codes and group scales of 16-bit weights [E x K x N]."""
+    _check(_lib.flux_w4_quantize(E, K, N, group, dtype, _ptr(w), _ptr(q), _ptr(scales), _stream(stream)),
+           "flux_w4_quantize")
+
+
+def flux_w4_gemv(M, N, K, group, dtype, x, q, scales, out, workspace, stream=None) -> None:
+    """out = x . W for few rows of x and 4-bit W."""
+    _check(_lib.flux_w4_gemv(M, N, K, group, dtype, _ptr(x), _ptr(q), _ptr(scales), _ptr(out),
+                             _ptr(workspace), _nbytes(workspace), _stream(stream)), "flux_w4_gemv")
+
+
+def flux_moe_w4_layer0(T, H, F, E, topk, group, dtype, x, q1, scales1, topk_ids, h, workspace,
+                       stream=None) -> None:
+    """MoE layer0 of few tokens with 4-bit experts; h in slot order."""
+    _check(_lib.flux_moe_w4_layer0(T, H, F, E, topk, group, dtype, _ptr(x), _ptr(q1), _ptr(scales1),
+                                   _ptr(topk_ids), _ptr(h), _ptr(workspace), _nbytes(workspace),
+                                   _stream(stream)), "flux_moe_w4_layer0")
+
+
+def flux_moe_w4_layer1(T, H, F, E, topk, group, dtype, h, q2, scales2, topk_ids, topk_weights, out, workspace,
+                       stream=None) -> None:
+    """MoE layer1 + gate-weighted combine of few tokens with 4-bit experts."""
+    _check(_lib.flux_moe_w4_layer1(T, H, F, E, topk, group, dtype, _ptr(h), _ptr(q2), _ptr(scales2),
+                                   _ptr(topk_ids), _ptr(topk_weights), _ptr(out), _ptr(workspace),
+                                   _nbytes(workspace), _stream(stream)), "flux_moe_w4_layer1")
 
 
 def _tuned(st, what, best):

@@ -24,7 +24,8 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 # (-DFLUX_CHECKS=1; loaded by the binding when FLUX_CHECKED=1)
 CHECKED_LIB_PATH = os.path.join(HERE, "libflux_gb300_checked.so")
 
-SOURCES = ["flux_core.cu", "flux_dense.cu", "flux_moe.cu", "flux_noalloc.cu", "flux_tune.cu"]
+SOURCES = ["flux_core.cu", "flux_dense.cu", "flux_moe.cu", "flux_noalloc.cu", "flux_tune.cu", "flux_block.cu",
+           "flux_router.cu", "flux_w4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
           "-diag-suppress", "550", "-Xptxas", "-v"]

@@ -140,7 +140,7 @@ flux_status_t check_workspace(const void* ws, size_t have, size_t need) {
 
 using namespace flux;
 
-extern "C" int flux_version(void) { return 200; }
+extern "C" int flux_version(void) { return 300; }
 
 extern "C" int flux_checks_enabled(void) { return FLUX_CHECKS ? 1 : 0; }
 
