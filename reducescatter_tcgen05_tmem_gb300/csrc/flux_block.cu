@@ -18,6 +18,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <mutex>
 #include <type_traits>
 
 #include "flux_host.h"
@@ -48,7 +49,7 @@ struct BlockNormArgs {
   int T, H, rows_per_rank;
   int post_norm, has_y, has_u, has_dx_out;
   int gate_per, gate_cols;  // rows of one gate row; 1 or H
-  int items, sub, chunk, item_rows;  // items of `chunk` rows, `sub` in each run of `item_rows` rows
+  int ctas, run_rows;  // backward: grid; rows that share one row of a gate with a gradient of its own
   float eps;
 };
 
@@ -61,6 +62,15 @@ struct Team {
   static constexpr int CTA = W <= 8 ? 256 : W * 32;
   static constexpr int COUNT = CTA / THREADS;
 };
+
+// CTA c of `ctas` takes the rows [first_row(c), first_row(c + 1)).
+__host__ __device__ __forceinline__ int first_row(int T, int ctas, int c) {
+  return static_cast<int>(static_cast<long long>(c) * T / ctas);
+}
+// The CTA that has row t.
+__host__ __device__ __forceinline__ int cta_of_row(int T, int ctas, int t) {
+  return static_cast<int>(((t + 1ll) * ctas - 1) / T);
+}
 
 template <int DT>
 __device__ __forceinline__ void load8(const void* base, size_t elem, float (&f)[8]) {
@@ -97,7 +107,7 @@ __device__ __forceinline__ void load_gate(const BlockNormArgs& a, int t, int col
 template <int DT, int W, int V>
 __global__ void __launch_bounds__(Team<W>::CTA)
 block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
-  __shared__ float red[Team<W>::COUNT][2 * W];
+  __shared__ alignas(16) float red[Team<W>::COUNT][2 * W];
   const int team = threadIdx.x / Team<W>::THREADS, lane = threadIdx.x % Team<W>::THREADS;
   const int wit = lane / 32;
   int turn = 0;
@@ -173,284 +183,531 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
   }
 }
 
-// Backward.  A CTA walks items of `chunk` consecutive rows that share a gate
-// row; its teams take the item's rows in turn, and every thread keeps the sums
-// of its own columns in registers:
-//   pre  = sum du xn of all its rows (dw_pre);
-//   post = sum d yn: with one gate row for all tokens, dw_post = g post and
-//          dg = w_post post, so one sum serves both; with a gate per row it is
-//          sum d g yn;
-//   A    = MULTI (a CTA can meet several rows of a gate per column): sum d yn
-//          of the current item, from which dg = w_post A and post += g A.
-// The teams' sums are joined in shared memory and the CTAs' by
-// block_norm_sums_kernel, both in a fixed order, so repeat calls give the same
-// bits.
-template <int DT, int W, int V, bool MULTI>
-__global__ void __launch_bounds__(Team<W>::CTA)
+// Backward.  A CTA takes a stretch of consecutive rows, its teams one row each
+// in turn.  Every thread copies its own columns of the rows to come into its
+// own slots of shared memory (DEPTH rows deep, so the loads of the next rows
+// run while the sums of this one meet at their barriers) and keeps the sums of
+// its own columns in registers:
+//   pre = sum du xn (dw_pre);
+//   A   = sum g' d yn, g' the row's gate if it is one scalar, else 1.  With one
+//         gate row per column for all tokens dw_post = g A and dg = w_post A; with
+//         several, A is taken for each stretch of rows that share one (a run, cut
+//         at the CTA's ends), which gives its share of dg and adds g A to dw_post.
+// A run that lies in one CTA has its gradient written at once; shares of a run
+// that several CTAs cut go to the workspace, two places for each CTA (its first
+// and its last run).  The teams' sums are joined in shared memory and the CTAs'
+// by block_norm_sums_kernel, both in a fixed order, so repeat calls give the
+// same bits.
+//
+// Consecutive rows for a CTA were measured against rows dealt out in turn (T
+// 32768, H 4096): 318 against 393 us.
+template <int W, int V>
+struct BwdShape {
+  static constexpr int ROW = Team<W>::CTA * V * 64;  // bytes of four tensors' rows, all teams of the CTA
+  static constexpr int DEPTH = W <= 8 ? (V == 1 ? 4 : 3) : V == 2 ? 3 : V == 3 ? 2 : 1;
+  static constexpr int JOIN = Team<W>::COUNT > 1 ? Team<W>::CTA * V * 32 : 0;
+  static constexpr int WEIGHTS = V > 3 ? Team<W>::CTA * V * 48 : 0;  // gw in fp32, w_pre as stored
+  static constexpr int SMEM = ROW * DEPTH + JOIN + WEIGHTS;
+  static constexpr int CTAS = W <= 8 ? 2 : 1;  // per SM
+};
+
+template <int DT, int W, int V, bool HAS_Y, bool HAS_U>
+__global__ void __launch_bounds__(Team<W>::CTA, (BwdShape<W, V>::CTAS))
 block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
-  constexpr int TT = Team<W>::THREADS, TEAMS = Team<W>::COUNT;
-  __shared__ float red1[TEAMS][2 * W], red3[TEAMS][6 * W];
+  constexpr int TT = Team<W>::THREADS, TEAMS = Team<W>::COUNT, CTA = Team<W>::CTA;
+  constexpr int DEPTH = BwdShape<W, V>::DEPTH;
+  // up to two vectors a thread: the weights as floats and d in registers; three:
+  // w_pre as stored, d in two slots whose values have been used; four: the
+  // weights in shared memory too (reloaded from L2 they took 2/3 of the time)
+  constexpr bool ROOMY = V <= 2;
+  enum { X = 0, Y = 1, DU = 2, DX = 3 };
+  extern __shared__ uint4 ring[];  // [DEPTH][tensor][V][CTA]
+  float* join = reinterpret_cast<float*>(ring + BwdShape<W, V>::ROW / 16 * DEPTH);
+  __shared__ alignas(16) float red1[TEAMS][2 * W], red2[TEAMS][4 * W];
   __shared__ double sums[TEAMS];
-  __shared__ float join[TEAMS > 1 ? TEAMS * TT * V * 8 : 1];
   const int team = threadIdx.x / TT, lane = threadIdx.x % TT, wit = lane / 32;
-  int turn1 = 0, turn3 = 0;
+  int turn1 = 0, turn2 = 0;
   const float rho = a.res_scale != nullptr ? __ldg(a.res_scale) : 1.0f;
   const float inv_h = 1.0f / static_cast<float>(a.H);
   const bool row_gate = a.gate != nullptr && a.gate_cols == 1;
-  const bool item_scalar = row_gate && a.gate_per > 1;
-  float pre[V][8] = {}, post[V][8] = {};
-  double res = 0.0;
+  const bool col_gate = a.gate != nullptr && a.gate_cols != 1;
+  const bool run_scalar = row_gate && a.gate_per > 1;
+  const bool runs_split = col_gate && a.gate_per < a.T;  // A per run
+  const int begin = first_row(a.T, a.ctas, blockIdx.x), end = first_row(a.T, a.ctas, blockIdx.x + 1);
+  f32x2 pre[V][4] = {}, A[V][4] = {};
+  double res = 0.0, scalar = 0.0;  // of the team, in its first thread
 
-  // dst[col] = (w ? w[col] : 1) * sum over teams of acc
-  auto join_teams = [&](const float (&acc)[V][8], float* dst, const void* w) {
+  auto column = [&](int v) { return (v * TT + lane) * 8; };
+  auto slot = [&](int stage, int tensor, int v) -> uint4& {
+    return ring[((stage * 4 + tensor) * V + v) * CTA + threadIdx.x];
+  };
+  // The team's rows in order, DEPTH - 1 ahead of the one at work, each with what
+  // its arithmetic needs of it.
+  struct Row {
+    int rank;
+    float ry, rx, gt;
+  };
+  Row queue[DEPTH];
+  int t_a = begin + team, rank_a = t_a / a.rows_per_rank, rank_end_a = (rank_a + 1) * a.rows_per_rank, fill = 0;
+  auto issue = [&] {
+#pragma unroll
+    for (int i = 0; i + 1 < DEPTH; ++i) queue[i] = queue[i + 1];
+    if (t_a < end) {
+      while (t_a >= rank_end_a) {
+        ++rank_a;
+        rank_end_a += a.rows_per_rank;
+      }
+      Row r;
+      r.rank = rank_a;
+      r.ry = a.post_norm ? __ldg(a.rstd_y + t_a) : 1.0f;
+      r.rx = HAS_U ? __ldg(a.rstd_x + t_a) : 0.0f;
+      r.gt = row_gate ? load16<DT>(a.gate, a.gate_per == 1 ? t_a : t_a / a.gate_per) : 1.0f;
+      queue[DEPTH - 1] = r;
+      const size_t at = static_cast<size_t>(t_a - rank_a * a.rows_per_rank) * a.H + lane * 8;
+      const uint16_t* px = static_cast<const uint16_t*>(a.x[rank_a]) + at;
+      const uint16_t* py = HAS_Y ? static_cast<const uint16_t*>(a.y[rank_a]) + at : nullptr;
+      const uint16_t* pu = HAS_U ? static_cast<const uint16_t*>(a.du[rank_a]) + at : nullptr;
+      const uint16_t* pd = a.has_dx_out ? static_cast<const uint16_t*>(a.dx_out[rank_a]) + at : nullptr;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (column(v) < a.H) {
+          copy16_async(&slot(fill, X, v), px + v * TT * 8);
+          if constexpr (HAS_Y) copy16_async(&slot(fill, Y, v), py + v * TT * 8);
+          if constexpr (HAS_U) copy16_async(&slot(fill, DU, v), pu + v * TT * 8);
+          if (a.has_dx_out) copy16_async(&slot(fill, DX, v), pd + v * TT * 8);
+        }
+      }
+      t_a += TEAMS;
+    }
+    copy_commit();
+    fill = fill + 1 == DEPTH ? 0 : fill + 1;
+  };
+
+  // the product of w_post and the gate's columns, and w_pre
+  f32x2 gw_r[V <= 3 ? V : 1][4], wp_r[ROOMY ? V : 1][4];
+  uint4 wp_q[V == 3 ? V : 1];
+  uint4* gw_s = reinterpret_cast<uint4*>(join);  // V > 3: [2][V][CTA], then w_pre [V][CTA] (JOIN is 0 there)
+  uint4* wp_s = gw_s + 2 * V * CTA;
+  const uint32_t one16 = pack2<DT>(1.0f, 1.0f);
+  auto weight8 = [&](const void* base, size_t at, bool inside, f32x2 (&f)[4]) {
+    if (!inside) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = 0;
+    } else if (base != nullptr) {
+      unpack8<DT>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at)), f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = both(1.0f);
+    }
+  };
+  auto load_gw = [&](int v, int run, f32x2 (&gw)[4]) {
+    const bool inside = column(v) < a.H;
+    weight8(a.w_post, column(v), inside, gw);
+    if (col_gate) {
+      f32x2 g[4];
+      weight8(a.gate, static_cast<size_t>(run) * a.H + column(v), inside, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) gw[i] = mul2(gw[i], g[i]);
+    }
+  };
+  auto put_gw = [&](int run) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if constexpr (V <= 3) {
+        load_gw(v, run, gw_r[v]);
+      } else {
+        f32x2 gw[4];
+        load_gw(v, run, gw);
+        const ulonglong2 lo = make_ulonglong2(gw[0], gw[1]), hi = make_ulonglong2(gw[2], gw[3]);
+        gw_s[v * CTA + threadIdx.x] = *reinterpret_cast<const uint4*>(&lo);
+        gw_s[(V + v) * CTA + threadIdx.x] = *reinterpret_cast<const uint4*>(&hi);
+      }
+    }
+  };
+  auto get_gw = [&](int v, f32x2 (&gw)[4]) {
+    if constexpr (V <= 3) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) gw[i] = gw_r[v][i];
+    } else {
+      const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(gw_s + v * CTA + threadIdx.x);
+      const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(gw_s + (V + v) * CTA + threadIdx.x);
+      gw[0] = lo.x, gw[1] = lo.y, gw[2] = hi.x, gw[3] = hi.y;
+    }
+  };
+  auto get_wp = [&](int v, f32x2 (&wp)[4]) {
+    if constexpr (ROOMY) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wp[i] = wp_r[v][i];
+    } else {
+      unpack8<DT>(V == 3 ? wp_q[V == 3 ? v : 0] : wp_s[v * CTA + threadIdx.x], wp);
+    }
+  };
+  if constexpr (HAS_U) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      uint4 q = make_uint4(0, 0, 0, 0);
+      if (column(v) < a.H)
+        q = a.w_pre != nullptr
+                ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.w_pre) + column(v)))
+                : make_uint4(one16, one16, one16, one16);
+      if constexpr (ROOMY) unpack8<DT>(q, wp_r[v]);
+      else if constexpr (V == 3) wp_q[v] = q;
+      else wp_s[v * CTA + threadIdx.x] = q;
+    }
+  }
+
+  // f(column, sum over teams) for every column, four at a time
+  auto join_teams = [&](const f32x2 (&acc)[V][4], auto&& f) {
+    auto four = [&](int v, int h) {
+      const float2 lo = halves(acc[v][2 * h]), hi = halves(acc[v][2 * h + 1]);
+      return make_float4(lo.x, lo.y, hi.x, hi.y);
+    };
     if constexpr (TEAMS > 1) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int col = (v * TT + lane) * 8;
-        if (col < a.H) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) join[team * a.H + col + i] = acc[v][i];
+        if (column(v) < a.H) {
+          float4* p = reinterpret_cast<float4*>(join + team * a.H + column(v));
+          p[0] = four(v, 0);
+          p[1] = four(v, 1);
         }
       }
       __syncthreads();
-      for (int c = threadIdx.x; c < a.H; c += Team<W>::CTA) {
-        float s = join[c];
+      for (int c = threadIdx.x * 4; c < a.H; c += CTA * 4) {
+        float4 s = *reinterpret_cast<const float4*>(join + c);
 #pragma unroll
-        for (int k = 1; k < TEAMS; ++k) s += join[k * a.H + c];
-        dst[c] = w != nullptr ? s * load16<DT>(w, c) : s;
+        for (int k = 1; k < TEAMS; ++k) {
+          const float4 o = *reinterpret_cast<const float4*>(join + k * a.H + c);
+          s.x += o.x;
+          s.y += o.y;
+          s.z += o.z;
+          s.w += o.w;
+        }
+        f(c, s);
       }
       __syncthreads();
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int col = (v * TT + lane) * 8;
-        if (col < a.H) {
-          float f[8];
-          load_or_one<DT>(w, col, f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= acc[v][i];
-          reinterpret_cast<float4*>(dst + col)[0] = make_float4(f[0], f[1], f[2], f[3]);
-          reinterpret_cast<float4*>(dst + col)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        if (column(v) < a.H) {
+          f(column(v), four(v, 0));
+          f(column(v) + 4, four(v, 1));
         }
       }
     }
   };
-  auto join_scalar = [&](double v, double* dst) {
+  auto times = [&](const void* w, size_t at, float4 s) {
+    if (w != nullptr) {
+      const uint2 p = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + at));
+      const float2 lo = unpack2<DT>(p.x), hi = unpack2<DT>(p.y);
+      s.x *= lo.x;
+      s.y *= lo.y;
+      s.z *= hi.x;
+      s.w *= hi.y;
+    }
+    return s;
+  };
+  auto join_scalar = [&](double v) {
     if (lane == 0) sums[team] = v;
     __syncthreads();
+    double s = 0.0;
     if (threadIdx.x == 0) {
-      double s = sums[0];
+      s = sums[0];
       for (int k = 1; k < TEAMS; ++k) s += sums[k];
-      *dst = s;
     }
     __syncthreads();
+    return s;
   };
+  float* my_post = a.part_post + static_cast<size_t>(blockIdx.x) * a.H;
+  float* my_pre = a.part_pre + static_cast<size_t>(blockIdx.x) * a.H;
+  const f32x2 rho2 = both(rho);
 
-  for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
-    const int run = item / a.sub;
-    const int t0 = run * a.item_rows + (item - run * a.sub) * a.chunk;
-    const int t1 = min(t0 + a.chunk, (run + 1) * a.item_rows);
-    float A[MULTI ? V : 1][8] = {};
-    double scalar = 0.0;
-    for (int t = t0 + team; t < t1; t += TEAMS) {
-      const int rank = t / a.rows_per_rank;
-      const size_t row = static_cast<size_t>(t - rank * a.rows_per_rank) * a.H;
-      const float ry = a.post_norm ? __ldg(a.rstd_y + t) : 1.0f;
-      const float rx = a.has_u ? __ldg(a.rstd_x + t) : 0.0f;
+  // slots that no copy fills hold zeros: columns past H, a gradient not given
+#pragma unroll
+  for (int s = 0; s < DEPTH; ++s)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (column(v) >= a.H) slot(s, X, v) = slot(s, Y, v) = slot(s, DU, v) = make_uint4(0, 0, 0, 0);
+      if (column(v) >= a.H || !a.has_dx_out) slot(s, DX, v) = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; ++i) issue();
+  int stage = 0, t = begin + team;
+  for (int t0 = begin, t1; t0 < end; t0 = t1) {
+    const int run = t0 / a.run_rows;
+    t1 = min(end, (run + 1) * a.run_rows);
+    const bool whole = t0 == run * a.run_rows && t1 == (run + 1) * a.run_rows;
+    const size_t place = 2 * blockIdx.x + (t0 == begin ? 0 : 1);  // of a cut run
+    if constexpr (HAS_Y) put_gw(run);
+    for (; t < t1; t += TEAMS) {
+      issue();
+      const Row r = queue[0];
+      copy_wait<DEPTH - 1>();
+      const float a1 = r.ry * r.gt;
+      const f32x2 a12 = both(a1);
+      // x' = rho x + y a1 gw
       float m1 = 0.0f;
-      if (a.has_u) {
-        float s1[1] = {0.0f};
+      const f32x2 rx2 = both(r.rx);
+      if constexpr (HAS_U) {
+        f32x2 s = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const int col = (v * TT + lane) * 8;
-          if (col < a.H) {
-            float x[8], y[8], du[8], g[8], w[8], wp[8];
-            load8<DT>(a.x[rank], row + col, x);
-            load8<DT>(a.du[rank], row + col, du);
-            load_or_one<DT>(a.w_pre, col, wp);
-            if (a.has_y) {
-              load8<DT>(a.y[rank], row + col, y);
-              load_or_one<DT>(a.w_post, col, w);
-              load_gate<DT>(a, t, col, g);
-            }
+          f32x2 x[4], du[4], wp[4];
+          unpack8<DT>(slot(stage, X, v), x);
+          unpack8<DT>(slot(stage, DU, v), du);
+          get_wp(v, wp);
+          if constexpr (HAS_Y) {
+            f32x2 y[4], gw[4];
+            unpack8<DT>(slot(stage, Y, v), y);
+            get_gw(v, gw);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float x1 = a.has_y ? rho * x[i] + g[i] * (y[i] * ry * w[i]) : x[i];
-              const float p = du[i] * (x1 * rx);
-              pre[v][i] += p;
-              s1[0] += p * wp[i];
-            }
+            for (int i = 0; i < 4; ++i) x[i] = fma2(mul2(y[i], a12), gw[i], mul2(rho2, x[i]));
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x2 p = mul2(du[i], mul2(x[i], rx2));
+            pre[v][i] = add2(pre[v][i], p);
+            s = fma2(p, wp[i], s);
           }
         }
+        float s1[1] = {halves(s).x + halves(s).y};
         team_sum<W>(s1, red1[team], turn1, team, wit);
         m1 = s1[0] * inv_h;
       }
-      float d[V][8];
-      float s3[3] = {0.0f, 0.0f, 0.0f};  // sums over the row of c yn, d x and d z
+      const f32x2 k1 = both(-r.rx * r.rx * m1);
+      f32x2 d_r[ROOMY ? V : 1][4];
+      f32x2 sy = 0, sx = 0;  // sums over the row of d y gw and d x
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int col = (v * TT + lane) * 8;
-        if (col < a.H) {
-          float x[8], y[8], g[8], w[8], du[8], wp[8];
-          load8<DT>(a.x[rank], row + col, x);
-          if (a.has_y) {
-            load8<DT>(a.y[rank], row + col, y);
-            load_or_one<DT>(a.w_post, col, w);
-            load_gate<DT>(a, t, col, g);
-          }
-          if (a.has_dx_out) {
-            load8<DT>(a.dx_out[rank], row + col, d[v]);
-          } else {
+        f32x2 x[4], y[4], d[4], gw[4];
+        unpack8<DT>(slot(stage, X, v), x);
+        unpack8<DT>(slot(stage, DX, v), d);
+        if constexpr (HAS_Y) {
+          unpack8<DT>(slot(stage, Y, v), y);
+          get_gw(v, gw);
+        }
+        if constexpr (HAS_U) {
+          f32x2 du[4], wp[4];
+          unpack8<DT>(slot(stage, DU, v), du);
+          get_wp(v, wp);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[v][i] = 0.0f;
+          for (int i = 0; i < 4; ++i) {
+            f32x2 x1 = x[i];
+            if constexpr (HAS_Y) x1 = fma2(mul2(y[i], a12), gw[i], mul2(rho2, x[i]));
+            d[i] = fma2(x1, k1, fma2(mul2(wp[i], du[i]), rx2, d[i]));
           }
-          if (a.has_u) {
-            load8<DT>(a.du[rank], row + col, du);
-            load_or_one<DT>(a.w_pre, col, wp);
-          }
+        }
+        if constexpr (HAS_Y) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float yn = a.has_y ? y[i] * ry : 0.0f;
-            const float x1 = a.has_y ? rho * x[i] + g[i] * (yn * w[i]) : x[i];
-            if (a.has_u) d[v][i] += rx * (wp[i] * du[i] - x1 * rx * m1);
-            if (a.has_y) {
-              const float dn = d[v][i] * yn;
-              if constexpr (MULTI) A[v][i] += dn;
-              else post[v][i] += row_gate ? dn * g[i] : dn;
-              s3[0] += dn * g[i] * w[i];
-              s3[1] += d[v][i] * x[i];
-              s3[2] += dn * w[i];
-            }
+          for (int i = 0; i < 4; ++i) {
+            const f32x2 e = mul2(d[i], y[i]);
+            A[v][i] = fma2(e, a12, A[v][i]);
+            sy = fma2(e, gw[i], sy);
+            sx = fma2(d[i], x[i], sx);
+          }
+        }
+        if constexpr (ROOMY) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d_r[v][i] = d[i];
+        } else {
+          const ulonglong2 lo = make_ulonglong2(d[0], d[1]), hi = make_ulonglong2(d[2], d[3]);
+          slot(stage, X, v) = *reinterpret_cast<const uint4*>(&lo);
+          slot(stage, DU, v) = *reinterpret_cast<const uint4*>(&hi);
+        }
+      }
+      float k2 = 0.0f;
+      if constexpr (HAS_Y) {
+        float s2[2] = {halves(sy).x + halves(sy).y, halves(sx).x + halves(sx).y};
+        team_sum<W>(s2, red2[team], turn2, team, wit);
+        k2 = a.post_norm ? r.ry * r.ry * a1 * s2[0] * inv_h : 0.0f;
+        if (lane == 0) {
+          res += s2[1];
+          if (row_gate) {
+            const float dg = r.ry * s2[0];
+            scalar += dg;
+            if (!run_scalar && a.dgate != nullptr) a.dgate[t] = dg;
           }
         }
       }
-      float m2 = 0.0f;
-      if (a.has_y) {
-        team_sum<W>(s3, red3[team], turn3, team, wit);
-        m2 = a.post_norm ? s3[0] * inv_h : 0.0f;
-        res += s3[1];
-        scalar += s3[2];
-        if (row_gate && !item_scalar && a.dgate != nullptr && lane == 0) a.dgate[t] = s3[2];
-      }
+      const f32x2 nk2 = both(-k2);
+      const size_t at = static_cast<size_t>(t - r.rank * a.rows_per_rank) * a.H + lane * 8;
+      uint16_t* pdx = static_cast<uint16_t*>(a.out_a[r.rank]) + at;
+      uint16_t* pdy = HAS_Y ? static_cast<uint16_t*>(a.out_b[r.rank]) + at : nullptr;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int col = (v * TT + lane) * 8;
-        if (col < a.H) {
-          if (a.has_y) {
-            float y[8], g[8], w[8];
-            load8<DT>(a.y[rank], row + col, y);
-            load_or_one<DT>(a.w_post, col, w);
-            load_gate<DT>(a, t, col, g);
+        f32x2 d[4];
+        if constexpr (ROOMY) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = ry * (d[v][i] * g[i] * w[i] - y[i] * ry * m2);
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_b[rank]) + row + col) = pack8<DT>(y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) d[v][i] *= rho;
-          }
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_a[rank]) + row + col) = pack8<DT>(d[v]);
+          for (int i = 0; i < 4; ++i) d[i] = d_r[v][i];
+        } else {
+          const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(&slot(stage, X, v));
+          const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(&slot(stage, DU, v));
+          d[0] = lo.x, d[1] = lo.y, d[2] = hi.x, d[3] = hi.y;
         }
+        if constexpr (HAS_Y) {
+          f32x2 y[4], gw[4];
+          unpack8<DT>(slot(stage, Y, v), y);
+          get_gw(v, gw);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[i] = fma2(mul2(d[i], a12), gw[i], mul2(y[i], nk2));
+            d[i] = mul2(d[i], rho2);
+          }
+          if (column(v) < a.H) *reinterpret_cast<uint4*>(pdy + v * TT * 8) = pack8<DT>(y);
+        }
+        if (column(v) < a.H) *reinterpret_cast<uint4*>(pdx + v * TT * 8) = pack8<DT>(d);
       }
+      stage = stage + 1 == DEPTH ? 0 : stage + 1;
     }
-    if constexpr (MULTI) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int col = (v * TT + lane) * 8;
-        if (col < a.H) {
-          float g[8];
-          load8<DT>(a.gate, static_cast<size_t>(run) * a.H + col, g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) post[v][i] += g[i] * A[v][i];
+    if (runs_split) {
+      const size_t grow = static_cast<size_t>(run) * a.H;
+      join_teams(A, [&](int c, float4 s) {
+        if (a.dgate != nullptr) {
+          if (whole) *reinterpret_cast<float4*>(a.dgate + grow + c) = times(a.w_post, c, s);
+          else *reinterpret_cast<float4*>(a.part_gate + place * a.H + c) = s;
         }
-      }
-      if (a.dgate != nullptr) {
-        if (a.sub == 1) join_teams(A, a.dgate + static_cast<size_t>(run) * a.H, a.w_post);
-        else join_teams(A, a.part_gate + static_cast<size_t>(item) * a.H, nullptr);
-      }
+        // the same thread holds these columns in every run
+        s = times(a.gate, grow + c, s);
+        if (t0 != begin) {
+          const float4 o = *reinterpret_cast<const float4*>(my_post + c);
+          s.x += o.x;
+          s.y += o.y;
+          s.z += o.z;
+          s.w += o.w;
+        }
+        *reinterpret_cast<float4*>(my_post + c) = s;
+      });
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) A[v][i] = 0;
     }
-    if (item_scalar) join_scalar(scalar, a.part_scalar + item);
+    if (run_scalar) {
+      const double s = join_scalar(scalar);
+      if (threadIdx.x == 0 && a.dgate != nullptr) {
+        if (whole) a.dgate[run] = static_cast<float>(s);
+        else a.part_scalar[place] = s;
+      }
+      scalar = 0.0;
+    }
   }
-  if (a.has_u) join_teams(pre, a.part_pre + static_cast<size_t>(blockIdx.x) * a.H, nullptr);
-  if (a.has_y) {
-    join_teams(post, a.part_post + static_cast<size_t>(blockIdx.x) * a.H, nullptr);
-    join_scalar(res, a.part_res + blockIdx.x);
+  if constexpr (HAS_U) join_teams(pre, [&](int c, float4 s) { *reinterpret_cast<float4*>(my_pre + c) = s; });
+  if constexpr (HAS_Y) {
+    if (!runs_split) join_teams(A, [&](int c, float4 s) { *reinterpret_cast<float4*>(my_post + c) = s; });
+    const double s = join_scalar(res);
+    if (threadIdx.x == 0) a.part_res[blockIdx.x] = s;
   }
 }
 
-constexpr int SUM_COLS = 32, SUM_WARPS = 8;
+constexpr int SUM_COLS = 32, SUM_WARPS = 32, SUM_BATCH = 10;
+
+constexpr int SUM_THREADS = SUM_COLS * SUM_WARPS;
+// blocks of block_norm_sums_kernel: dw_pre and dw_post by columns, the scalars, cut runs by columns
+inline int sum_blocks(int H) { return (H + SUM_COLS - 1) / SUM_COLS; }
+inline int run_blocks(int H) { return (H + 4 * SUM_THREADS - 1) / (4 * SUM_THREADS); }
 
 // Joins the CTAs' partial sums, each column in a fixed order, and leaves the
-// partial sums zero.  blockIdx.y: 0 dw_pre, 1 dw_post (and the gradient of a
-// gate of one row), 2 the scalars, 3 + g the gate row g of several.
+// partial sums zero.
 template <int DT>
-__global__ void __launch_bounds__(SUM_COLS* SUM_WARPS)
-block_norm_sums_kernel(const __grid_constant__ BlockNormArgs a, int ctas, int multi) {
+__global__ void __launch_bounds__(SUM_THREADS)
+block_norm_sums_kernel(const __grid_constant__ BlockNormArgs a, int col_blocks, int per_run_blocks) {
   __shared__ float part[SUM_WARPS][SUM_COLS];
   const int lane = threadIdx.x % SUM_COLS, warp = threadIdx.x / SUM_COLS;
-  const int job = blockIdx.y;
-  if (job == 2) {
-    if (!a.has_y || blockIdx.x != 0) return;
-    if (warp == 0) {
-      double s = 0.0;
-      for (int i = lane; i < ctas; i += 32) {
-        s += a.part_res[i];
-        a.part_res[i] = 0.0;
-      }
+  const bool one_row = a.gate != nullptr && a.gate_cols != 1 && a.gate_per == a.T;
+  if (blockIdx.x < 2 * col_blocks) {
+    const bool is_pre = blockIdx.x < col_blocks;
+    if (is_pre ? !a.has_u : !a.has_y) return;
+    float* src = is_pre ? a.part_pre : a.part_post;
+    const int col = (is_pre ? blockIdx.x : blockIdx.x - col_blocks) * SUM_COLS + lane;
+    float s = 0.0f;
+    if (col < a.H) {
+      // the loads of a batch are in flight together: one after another, each
+      // behind the store of the last, they cost more than all the rest
+      for (int i0 = warp; i0 < a.ctas; i0 += SUM_WARPS * SUM_BATCH) {
+        float v[SUM_BATCH];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-      if (a.dres != nullptr && lane == 0) a.dres[0] = static_cast<float>(s);
-    }
-    if (a.gate != nullptr && a.gate_cols == 1 && a.gate_per > 1) {
-      for (int g = threadIdx.x; g < a.items / a.sub; g += SUM_COLS * SUM_WARPS) {
-        double s = 0.0;
-        for (int i = g * a.sub; i < (g + 1) * a.sub; ++i) {
-          s += a.part_scalar[i];
-          a.part_scalar[i] = 0.0;
+        for (int j = 0; j < SUM_BATCH; ++j) {
+          const int i = i0 + j * SUM_WARPS;
+          v[j] = i < a.ctas ? src[static_cast<size_t>(i) * a.H + col] : 0.0f;
         }
-        if (a.dgate != nullptr) a.dgate[g] = static_cast<float>(s);
+#pragma unroll
+        for (int j = 0; j < SUM_BATCH; ++j) {
+          const int i = i0 + j * SUM_WARPS;
+          if (i < a.ctas) src[static_cast<size_t>(i) * a.H + col] = 0.0f;
+          s += v[j];
+        }
       }
     }
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp != 0 || col >= a.H) return;
+#pragma unroll
+    for (int w = 1; w < SUM_WARPS; ++w) s += part[w][lane];
+    if (is_pre) {
+      if (a.dw_pre != nullptr) a.dw_pre[col] = s;
+    } else {
+      if (a.dw_post != nullptr) a.dw_post[col] = one_row ? s * load16<DT>(a.gate, col) : s;
+      if (one_row && a.dgate != nullptr) a.dgate[col] = a.w_post != nullptr ? s * load16<DT>(a.w_post, col) : s;
+    }
     return;
   }
-  float* src;
-  int n;
-  if (job == 0) {
-    if (!a.has_u) return;
-    src = a.part_pre;
-    n = ctas;
-  } else if (job == 1) {
-    if (!a.has_y) return;
-    src = a.part_post;
-    n = ctas;
-  } else {
-    src = a.part_gate + static_cast<size_t>(job - 3) * a.sub * a.H;
-    n = a.sub;
+  if (blockIdx.x == 2 * col_blocks) {
+    if (!a.has_y || warp != 0) return;
+    double s = 0.0;
+    for (int i = lane; i < a.ctas; i += 32) {
+      s += a.part_res[i];
+      a.part_res[i] = 0.0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (a.dres != nullptr && lane == 0) a.dres[0] = static_cast<float>(s);
+    return;
   }
-  const int col = blockIdx.x * SUM_COLS + lane;
-  float s = 0.0f;
-  if (col < a.H) {
-    for (int i = warp; i < n; i += SUM_WARPS) {
-      float* p = src + static_cast<size_t>(i) * a.H + col;
-      s += *p;
-      *p = 0.0f;
+  // the run that CTA b - 1 and CTA b share, if b is the first to continue it
+  const int k = blockIdx.x - 2 * col_blocks - 1;
+  const int b = 1 + k / per_run_blocks, at = first_row(a.T, a.ctas, b), run = at / a.run_rows;
+  const int r0 = run * a.run_rows;
+  if (r0 == at) return;
+  const int c0 = cta_of_row(a.T, a.ctas, r0), c1 = cta_of_row(a.T, a.ctas, r0 + a.run_rows - 1);
+  if (c0 != b - 1) return;
+  const int first = 2 * c0 + (first_row(a.T, a.ctas, c0) == r0 ? 0 : 1);
+  auto place = [&](int i) { return i == 0 ? first : 2 * (c0 + i); };
+  const int n = c1 - c0 + 1;
+  if (a.gate_cols == 1) {
+    if (threadIdx.x != 0 || k % per_run_blocks != 0) return;
+    double s = 0.0;
+    for (int i = 0; i < n; ++i) {
+      s += a.part_scalar[place(i)];
+      a.part_scalar[place(i)] = 0.0;
+    }
+    a.dgate[run] = static_cast<float>(s);
+    return;
+  }
+  const int col = (k % per_run_blocks * SUM_THREADS + threadIdx.x) * 4;
+  if (col >= a.H) return;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i0 = 0; i0 < n; i0 += SUM_BATCH) {
+    float4 v[SUM_BATCH];
+#pragma unroll
+    for (int j = 0; j < SUM_BATCH; ++j)
+      if (i0 + j < n) v[j] = *reinterpret_cast<const float4*>(a.part_gate + static_cast<size_t>(place(i0 + j)) * a.H + col);
+#pragma unroll
+    for (int j = 0; j < SUM_BATCH; ++j) {
+      if (i0 + j >= n) break;
+      *reinterpret_cast<float4*>(a.part_gate + static_cast<size_t>(place(i0 + j)) * a.H + col) =
+          make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      s.x += v[j].x;
+      s.y += v[j].y;
+      s.z += v[j].z;
+      s.w += v[j].w;
     }
   }
-  part[warp][lane] = s;
-  __syncthreads();
-  if (warp != 0 || col >= a.H) return;
-#pragma unroll
-  for (int w = 1; w < SUM_WARPS; ++w) s += part[w][lane];
-  if (job == 0) {
-    if (a.dw_pre != nullptr) a.dw_pre[col] = s;
-    return;
+  if (a.w_post != nullptr) {
+    s.x *= load16<DT>(a.w_post, col);
+    s.y *= load16<DT>(a.w_post, col + 1);
+    s.z *= load16<DT>(a.w_post, col + 2);
+    s.w *= load16<DT>(a.w_post, col + 3);
   }
-  const bool one_row = a.gate != nullptr && a.gate_cols != 1 && !multi;
-  if (job == 1) {
-    if (a.dw_post != nullptr) a.dw_post[col] = one_row ? s * load16<DT>(a.gate, col) : s;
-    if (one_row && a.dgate != nullptr) a.dgate[col] = a.w_post != nullptr ? s * load16<DT>(a.w_post, col) : s;
-    return;
-  }
-  if (a.dgate != nullptr)
-    a.dgate[static_cast<size_t>(job - 3) * a.H + col] = a.w_post != nullptr ? s * load16<DT>(a.w_post, col) : s;
+  *reinterpret_cast<float4*>(a.dgate + static_cast<size_t>(run) * a.H + col) = s;
 }
 
 template <int N>
@@ -470,42 +727,22 @@ flux_status_t by_width(int H, F&& f) {
   return f(Int<16>{}, Int<4>{});
 }
 
-// How the backward pass cuts T rows into items, and its workspace.
+// The backward pass's grid and workspace.
 struct BwdPlan {
-  int teams, max_ctas, item_rows, sub, chunk, items, ctas;
-  bool multi;
+  int ctas, run_rows;
+  bool cut_runs;  // several gate rows with a gradient of their own (not one written token by token)
   size_t pre, post, gate, res, scalar, total;
 };
 
 BwdPlan bwd_plan(int T, int H, int gate_rows, int gate_cols) {
   BwdPlan p{};
   const int nvec = H / 8;
-  p.teams = nvec <= 64 ? 8 : nvec <= 128 ? 4 : nvec <= 256 ? 2 : 1;
-  p.max_ctas = nvec <= 512 ? BN_MAX_CTAS : BN_MAX_CTAS / 2;
-  // several gate rows: an item stays inside one (a gate per token has its
-  // gradient written row by row)
+  const int teams = nvec <= 64 ? 8 : nvec <= 128 ? 4 : nvec <= 256 ? 2 : 1;
+  p.ctas = std::min(nvec <= 512 ? BN_MAX_CTAS : BN_MAX_CTAS / 2, (T + teams - 1) / teams);
   const int per = gate_rows > 0 ? T / gate_rows : T;
-  p.multi = gate_rows > 1 && gate_cols > 1;
-  const bool split = gate_rows > 1 && (p.multi || per > 1);
-  p.item_rows = split ? per : T;
-  const int runs = split ? gate_rows : 1;
-  // rounds of the grid x (rows of an item + one row's worth for its joins)
-  long long best = -1;
-  const int most = (p.item_rows + p.teams - 1) / p.teams;
-  for (int s = 1; s <= most; ++s) {
-    if (s > 1 && static_cast<long long>(runs) * s > 2 * p.max_ctas) break;
-    const int chunk = (p.item_rows + s - 1) / s;
-    const int sub = (p.item_rows + chunk - 1) / chunk;
-    const long long items = static_cast<long long>(runs) * sub;
-    const long long cost = (items + p.max_ctas - 1) / p.max_ctas * ((chunk + p.teams - 1) / p.teams + 1);
-    if (best < 0 || cost < best) {
-      best = cost;
-      p.sub = sub;
-      p.chunk = chunk;
-      p.items = static_cast<int>(items);
-    }
-  }
-  p.ctas = std::min(p.items, p.max_ctas);
+  const bool rows = gate_rows > 1 && gate_cols > 1, scalars = gate_cols == 1 && per > 1;
+  p.cut_runs = rows || scalars;
+  p.run_rows = p.cut_runs ? per : T;
   size_t at = WS_HEADER;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -514,9 +751,9 @@ BwdPlan bwd_plan(int T, int H, int gate_rows, int gate_cols) {
   };
   p.pre = take(sizeof(float) * p.ctas * H);
   p.post = take(sizeof(float) * p.ctas * H);
-  p.gate = take(p.multi && p.sub > 1 ? sizeof(float) * p.items * static_cast<size_t>(H) : 0);
+  p.gate = take(rows ? sizeof(float) * 2 * p.ctas * H : 0);
   p.res = take(sizeof(double) * p.ctas);
-  p.scalar = take(split && !p.multi ? sizeof(double) * p.items : 0);
+  p.scalar = take(scalars ? sizeof(double) * 2 * p.ctas : 0);
   p.total = at;
   return p;
 }
@@ -585,19 +822,30 @@ flux_status_t launch_fwd(const BlockNormArgs& a, cudaStream_t s) {
   });
 }
 
+template <int DT, int W, int V, bool HAS_Y, bool HAS_U>
+flux_status_t launch_bwd_form(const BlockNormArgs& a, const BwdPlan& p, cudaStream_t s) {
+  constexpr int smem = BwdShape<W, V>::SMEM;
+  constexpr auto kernel = block_norm_bwd_kernel<DT, W, V, HAS_Y, HAS_U>;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] { attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  if (attr != cudaSuccess) return cuda_fail(attr);
+  kernel<<<p.ctas, Team<W>::CTA, smem, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
+}
+
 template <int DT>
 flux_status_t launch_bwd(const BlockNormArgs& a, const BwdPlan& p, cudaStream_t s) {
   flux_status_t st = by_width(a.H, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
-    if (p.multi) block_norm_bwd_kernel<DT, W, V, true><<<p.ctas, Team<W>::CTA, 0, s>>>(a);
-    else block_norm_bwd_kernel<DT, W, V, false><<<p.ctas, Team<W>::CTA, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
+    if (!a.has_y) return launch_bwd_form<DT, W, V, false, true>(a, p, s);
+    return a.has_u ? launch_bwd_form<DT, W, V, true, true>(a, p, s) : launch_bwd_form<DT, W, V, true, false>(a, p, s);
   });
   if (st != FLUX_OK) return st;
-  const int rows = p.multi && p.sub > 1 && a.dgate != nullptr ? p.items / p.sub : 0;
-  const dim3 grid((a.H + SUM_COLS - 1) / SUM_COLS, 3 + rows);
-  block_norm_sums_kernel<DT><<<grid, SUM_COLS * SUM_WARPS, 0, s>>>(a, p.ctas, p.multi);
+  const int cols = sum_blocks(a.H), per_run = a.gate_cols == 1 ? 1 : run_blocks(a.H);
+  const int cut = p.cut_runs && a.dgate != nullptr ? (p.ctas - 1) * per_run : 0;
+  block_norm_sums_kernel<DT><<<2 * cols + 1 + cut, SUM_THREADS, 0, s>>>(a, cols, per_run);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
@@ -712,9 +960,7 @@ extern "C" flux_status_t flux_block_norm_bwd(int R, int T, int H, flux_dtype_t d
   a.part_gate = reinterpret_cast<float*>(ws + p.gate);
   a.part_res = reinterpret_cast<double*>(ws + p.res);
   a.part_scalar = reinterpret_cast<double*>(ws + p.scalar);
-  a.items = p.items;
-  a.sub = p.sub;
-  a.chunk = p.chunk;
-  a.item_rows = p.item_rows;
+  a.ctas = p.ctas;
+  a.run_rows = p.run_rows;
   return dtype == FLUX_BF16 ? launch_bwd<1>(a, p, s) : launch_bwd<0>(a, p, s);
 }
