@@ -6,6 +6,7 @@
 // the lanes of a warp use them: in each run of 128 inputs, 16 bytes for every
 // c of 0..3, in them one 32-bit word for every j of 0..3, whose nibbles i and
 // i + 4 hold the inputs 32 j + 8 c + 2 i and 32 j + 8 c + 2 i + 1.
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -24,7 +25,7 @@ enum W4Mode { W4_DENSE = 0, W4_LAYER0 = 1, W4_LAYER1 = 2 };
 
 constexpr int W4_WARPS = 8, W4_THREADS = W4_WARPS * 32;
 constexpr int W4_COLS = W4_WARPS * 16;      // columns of a tile: 16 for each warp
-constexpr int W4_MAX_CTAS = 2 * 160;        // two CTAs per SM
+constexpr int W4_MAX_CTAS = 3 * 160;        // at most three CTAs per SM
 constexpr int W4_RUN_BYTES = W4_RUN / 2;
 
 struct W4Args {
@@ -53,12 +54,12 @@ template <int DT>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                             uint32_t b1) {
   if constexpr (DT == 1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   } else {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -110,12 +111,12 @@ __device__ __forceinline__ void copy16_or_zero(void* smem, const void* gmem, boo
 // MT tiles of 8 rows; SR scales per run and column (a group of 128 or a multiple: 1, of 64: 2, else 4).
 template <int MT, int SR>
 struct W4Shape {
-  static constexpr int WORDS = W4_COLS * W4_RUN_BYTES;
-  static constexpr int XS = MT * 8 * W4_RUN * 2;
-  static constexpr int SC = SR * W4_COLS * 2;
-  static constexpr int STAGE = WORDS + XS + SC;
-  static constexpr int STAGES = MT == 1 ? 8 : MT == 2 ? 7 : 5;  // two CTAs fit an SM
-  static constexpr int SMEM = STAGE * STAGES;
+  static constexpr int CHUNK = MT == 1 ? 24 : MT == 2 ? 16 : 8;  // runs whose rows of x and scales are in shared memory
+  static constexpr int XRUN = MT * 8 * W4_RUN * 2;
+  static constexpr int SRUN = SR * W4_COLS * 2;
+  static constexpr int SMEM = CHUNK * (XRUN + SRUN);
+  static constexpr int AHEAD = 4;                // runs of codes that a thread has on the way
+  static constexpr int CTAS = 2;                 // per SM
   static constexpr int PART = W4_COLS * MT * 8;  // floats of a partial tile
 };
 
@@ -135,13 +136,13 @@ struct W4Shape {
 // sums.  The CTAs that share a tile leave their sums in the workspace, and the
 // last to arrive adds them in CTA order: repeat calls give the same bits.
 template <int DT, int MT, int SR>
-__global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const __grid_constant__ W4Args a) {
+__global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel(const __grid_constant__ W4Args a) {
   using S = W4Shape<MT, SR>;
   extern __shared__ uint4 ring4[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(ring4);
   __shared__ uint16_t order[FLUX_W4_MAX_ROWS];       // slots by expert
   __shared__ W4RowTile tiles[FLUX_W4_MAX_ROWS];
-  __shared__ int hist[FLUX_MAX_EXPERTS];
+  int* hist = reinterpret_cast<int*>(ring);  // before the ring is used
   __shared__ int scan[2][W4_WARPS];
   __shared__ int last_here;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -239,106 +240,122 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const __grid_constant
     }
   }
 
-  const long long units = static_cast<long long>(row_tiles) * col_tiles * a.runs;
+  const int units = row_tiles * col_tiles * a.runs;
   // every CTA that works has a unit: the arrivals at a cut tile are counted by CTA
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), units));
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const long long u0 = units * blockIdx.x / ctas, u1 = units * (blockIdx.x + 1) / ctas;
+  const int ctas = min(static_cast<int>(gridDim.x), units), me = blockIdx.x;
+  if (me >= ctas) return;
+  const int each = units / ctas, more = units - each * ctas;  // the first `more` CTAs have one unit more
+  auto first_unit = [&](int cta) { return cta * each + min(cta, more); };
+  auto cta_of = [&](int unit) {
+    const int big = more * (each + 1);
+    return unit < big ? unit / (each + 1) : more + (unit - big) / each;
+  };
+  const int u0 = first_unit(me), n_units = first_unit(me + 1) - u0;
+  int tile = u0 / a.runs, run = u0 - tile * a.runs;
 
-  // the unit that is copied next
-  long long ahead = u0;
-  int run_a = static_cast<int>(u0 % a.runs), ct_a = static_cast<int>(u0 / a.runs % col_tiles),
-      rt_a = static_cast<int>(u0 / a.runs / col_tiles), fill = 0;
-  auto issue = [&] {
-    if (ahead < u1) {
-      uint8_t* st = ring + fill * S::STAGE;
-      const W4RowTile rt = tiles[rt_a];
-      const int col0 = ct_a * W4_COLS;
+  const int x_from0 = g * 256 + c * 16 + ((g & 1) << 6), x_from1 = x_from0 ^ 64;
+  constexpr int P = S::AHEAD;
+  constexpr int XROWS = MT == 1 ? 8 : 16, XRUNS = 16 / XROWS;  // rows and runs of x that the CTA copies at a time
+  int todo = n_units;
+#pragma unroll 1
+  for (bool first_tile = true; todo > 0; ++tile, run = 0, first_tile = false) {
+    const int n_runs = min(a.runs - run, todo);
+    const bool whole = n_runs == a.runs;
+    todo -= n_runs;
+    const int rt_i = tile / col_tiles, ct = tile - rt_i * col_tiles, col0 = ct * W4_COLS;
+    const W4RowTile rt = tiles[rt_i];
+    // this thread's words of the columns g and g + 8 of the warp's 16
+    const int my_col = col0 + warp * 16 + g;
+    const uint4* qa = reinterpret_cast<const uint4*>(
+        a.q + ((static_cast<size_t>(rt.expert) * a.N + min(my_col, a.N - 1)) * a.runs + run) * W4_RUN_BYTES + c * 16);
+    const uint4* qb = reinterpret_cast<const uint4*>(
+        a.q + ((static_cast<size_t>(rt.expert) * a.N + min(my_col + 8, a.N - 1)) * a.runs + run) * W4_RUN_BYTES + c * 16);
+    uint4 wa[P], wb[P];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int col = col0 + warp * 16 + g + 8 * h;
-        if (col < a.N)
-          copy16_async(st + (h * W4_THREADS + tid) * 16,
-                       a.q + ((static_cast<size_t>(rt.expert) * a.N + col) * a.runs + run_a) * W4_RUN_BYTES + c * 16);
-      }
-      // rows of x, 16 bytes (8 inputs) at a time: chunk 4 j + c of a row lies at
-      // 4 (j ^ (row & 1)) + c, so that two rows' reads meet different banks
-      for (int i = tid; i < rt.rows * 16; i += W4_THREADS) {
-        const int m = i >> 4, k = i & 15, slot = order[rt.first + m];
-        const int row = a.mode == W4_LAYER0 ? slot / a.topk : slot;
-        const int at = run_a * W4_RUN + k * 8;
-        copy16_or_zero(st + S::WORDS + m * 256 + ((k ^ ((m & 1) << 2)) << 4),
-                       a.x + static_cast<size_t>(row) * a.K + (at < a.K ? at : 0), at < a.K);
-      }
-      if (tid < SR * (W4_COLS / 8)) {
-        const int r = tid / (W4_COLS / 8), col = tid % (W4_COLS / 8) * 8;
-        const int at = run_a * W4_RUN + r * (W4_RUN / SR);
-        if (col0 + col < a.N && at < a.K)
-          copy16_async(st + S::WORDS + S::XS + (r * W4_COLS + col) * 2,
-                       a.scales + (static_cast<size_t>(rt.expert) * a.groups + at / a.group) * a.N + col0 + col);
-      }
-      ++ahead;
-      if (++run_a == a.runs) {
-        run_a = 0;
-        if (++ct_a == col_tiles) {
-          ct_a = 0;
-          ++rt_a;
-        }
+    for (int i = 0; i < P; ++i) {
+      if (i < n_runs) {
+        wa[i] = __ldcs(qa + i * 4);
+        wb[i] = __ldcs(qb + i * 4);
       }
     }
-    copy_commit();
-    fill = fill + 1 == S::STAGES ? 0 : fill + 1;
-  };
-#pragma unroll 1
-  for (int i = 0; i < S::STAGES - 1; ++i) issue();
-
-  int stage = 0;
-  long long tile = u0 / a.runs;
-  int run = static_cast<int>(u0 - tile * a.runs);
-  for (long long u = u0; u < u1; ++tile, run = 0) {
-    const int run_end = static_cast<int>(min(static_cast<long long>(a.runs), run + (u1 - u)));
-    const bool whole = run == 0 && run_end == a.runs;
-    const int ct = static_cast<int>(tile % col_tiles);
-    const W4RowTile rt = tiles[tile / col_tiles];
-    const bool first_tile = u == u0;
     float acc[MT][4] = {};
-    for (; run < run_end; ++run, ++u) {
-      copy_wait<S::STAGES - 2>();
-      __syncthreads();
-      issue();
-      const uint8_t* st = ring + stage * S::STAGE;
-      stage = stage + 1 == S::STAGES ? 0 : stage + 1;
-      const uint4 qa = *reinterpret_cast<const uint4*>(st + tid * 16);
-      const uint4 qb = *reinterpret_cast<const uint4*>(st + (W4_THREADS + tid) * 16);
-      const uint32_t wa[4] = {qa.x, qa.y, qa.z, qa.w}, wb[4] = {qb.x, qb.y, qb.z, qb.w};
-      const uint16_t* sc = reinterpret_cast<const uint16_t*>(st + S::WORDS + S::XS) + warp * 16 + g;
-      float part[MT][4] = {};
+#pragma unroll 1
+    for (int r0 = 0; r0 < n_runs; r0 += S::CHUNK) {
+      const int n = min(S::CHUNK, n_runs - r0);
+      __syncthreads();  // the last chunk has been read
+      // rows of x in 16-byte chunks (8 inputs): chunk 4 j + c of a row lies at
+      // 4 (j ^ (row & 1)) + c, so that two rows' reads meet different banks
+      {
+        const int k = tid & 15, k0 = (run + r0) * W4_RUN + k * 8;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t pa[4], pb[4];
-        codes8<DT>(wa[j], pa);
-        codes8<DT>(wb[j], pb);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (m > 0 && rt.rows <= m * 8) break;
-          const uint4 xv = *reinterpret_cast<const uint4*>(st + S::WORDS + (m * 8 + g) * 256 + (((j * 4 + c) ^ ((g & 1) << 2)) << 4));
-          mma_16x8x16<DT>(part[m], pa[0], pb[0], pa[1], pb[1], xv.x, xv.y);
-          mma_16x8x16<DT>(part[m], pa[2], pb[2], pa[3], pb[3], xv.z, xv.w);
+        for (int p = 0; p < (MT * 8 + 15) / 16; ++p) {
+          const int m = p * 16 + (tid >> 4) % XROWS;
+          if (m < rt.rows) {
+            const int slot = order[rt.first + m];
+            const uint16_t* row = a.x + static_cast<size_t>(a.mode == W4_LAYER0 ? slot / a.topk : slot) * a.K;
+            uint8_t* to = ring + m * 256 + ((k ^ ((m & 1) << 2)) << 4);
+#pragma unroll 4
+            for (int r = (tid >> 4) / XROWS; r < n; r += XRUNS) {
+              const int at = k0 + r * W4_RUN;
+              copy16_or_zero(to + r * S::XRUN, row + (at < a.K ? at : 0), at < a.K);
+            }
+          }
         }
-        if ((j + 1) % (4 / SR) == 0) {
-          const int r = j / (4 / SR);
-          // inputs past K are zeros; their group has no scale in memory
-          const bool in = run * W4_RUN + r * (W4_RUN / SR) < a.K;
-          const float s0 = in ? unpack2<DT>(sc[r * W4_COLS]).x : 0.0f, s1 = in ? unpack2<DT>(sc[r * W4_COLS + 8]).x : 0.0f;
+        constexpr int AT_ONCE = W4_THREADS / (SR * W4_COLS / 8);
+        const int sr = tid / (W4_COLS / 8) % SR, col = tid % (W4_COLS / 8) * 8;
+        for (int r = tid / (SR * W4_COLS / 8); r < n; r += AT_ONCE) {
+          const int at = (run + r0 + r) * W4_RUN + sr * (W4_RUN / SR);
+          const bool in = at < a.K && col0 + col < a.N;
+          const size_t from = (static_cast<size_t>(rt.expert) * a.groups + (in ? at / a.group : 0)) * a.N + (in ? col0 + col : 0);
+          copy16_or_zero(ring + S::CHUNK * S::XRUN + r * S::SRUN + (sr * W4_COLS + col) * 2, a.scales + from, in);
+        }
+        copy_commit();
+        copy_wait<0>();
+      }
+      __syncthreads();
+      const uint8_t* xs = ring;
+      const uint16_t* sc = reinterpret_cast<const uint16_t*>(ring + S::CHUNK * S::XRUN) + warp * 16 + g;
+#pragma unroll 1
+      for (int r = 0; r < n; r += P, xs += P * S::XRUN, sc += P * S::SRUN / 2, qa += P * 4, qb += P * 4) {
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            if (m > 0 && rt.rows <= m * 8) break;
-            acc[m][0] += s0 * part[m][0];
-            acc[m][1] += s0 * part[m][1];
-            acc[m][2] += s1 * part[m][2];
-            acc[m][3] += s1 * part[m][3];
+        for (int i = 0; i < P; ++i) {
+          if (r + i >= n) break;
+          const uint32_t va[4] = {wa[i].x, wa[i].y, wa[i].z, wa[i].w}, vb[4] = {wb[i].x, wb[i].y, wb[i].z, wb[i].w};
+          if (r0 + r + i + P < n_runs) {
+            wa[i] = __ldcs(qa + (i + P) * 4);
+            wb[i] = __ldcs(qb + (i + P) * 4);
+          }
+          float part[MT][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[m][i] = 0.0f;
+          for (int j = 0; j < 4; ++j) {
+            uint32_t pa[4], pb[4];
+            codes8<DT>(va[j], pa);
+            codes8<DT>(vb[j], pb);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              if (m == 0 || rt.rows > m * 8) {
+                const uint4 xv = *reinterpret_cast<const uint4*>(xs + i * S::XRUN + (j & 1 ? x_from1 : x_from0) + (j >> 1) * 128 + m * 2048);
+                if (j % (4 / SR) == 0) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) part[m][k] = 0.0f;
+                }
+                mma_16x8x16<DT>(part[m], pa[0], pb[0], pa[1], pb[1], xv.x, xv.y);
+                mma_16x8x16<DT>(part[m], pa[2], pb[2], pa[3], pb[3], xv.z, xv.w);
+              }
+            }
+            if ((j + 1) % (4 / SR) == 0) {
+              const uint16_t* s = sc + i * (S::SRUN / 2) + j / (4 / SR) * W4_COLS;
+              const float s0 = unpack2<DT>(s[0]).x, s1 = unpack2<DT>(s[8]).x;
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                if (m == 0 || rt.rows > m * 8) {
+                  acc[m][0] += s0 * part[m][0];
+                  acc[m][1] += s0 * part[m][1];
+                  acc[m][2] += s1 * part[m][2];
+                  acc[m][3] += s1 * part[m][3];
+                }
+              }
+            }
           }
         }
       }
@@ -346,14 +363,13 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const __grid_constant
 
     if (!whole) {
       // leave the sums; the last CTA of the tile adds everybody's
-      const int place = 2 * blockIdx.x + (first_tile ? 0 : 1);
+      const int place = 2 * me + (first_tile ? 0 : 1);
       float4* mine = reinterpret_cast<float4*>(a.parts + static_cast<size_t>(place) * S::PART);
 #pragma unroll
       for (int m = 0; m < MT; ++m) mine[m * W4_THREADS + tid] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
       __threadfence();
       __syncthreads();
-      const long long tu0 = tile * a.runs, tu1 = tu0 + a.runs;
-      const int c0 = static_cast<int>(((tu0 + 1) * ctas - 1) / units), c1 = static_cast<int>((tu1 * ctas - 1) / units);
+      const int tu0 = tile * a.runs, c0 = cta_of(tu0), c1 = cta_of(tu0 + a.runs - 1);
       if (tid == 0) {
         const uint32_t seen = atomicAdd(a.cut + c0, 1u);
         last_here = seen == static_cast<uint32_t>(c1 - c0);
@@ -364,7 +380,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const __grid_constant
       __threadfence();
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.0f;
-      constexpr int BATCH = 8 / MT;  // loads in flight together
+      constexpr int BATCH = MT == 1 ? 4 : 2;  // CTAs whose loads are in flight together
       for (int k0 = c0; k0 <= c1; k0 += BATCH) {
         float4 v[BATCH][MT];
         float4* p[BATCH];
@@ -373,7 +389,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_kernel(const __grid_constant
           const int k = k0 + b;
           if (k > c1) break;
           // the tile is the first of CTA k unless it begins inside its stretch
-          p[b] = reinterpret_cast<float4*>(a.parts + static_cast<size_t>(2 * k + (units * k / ctas >= tu0 ? 0 : 1)) * S::PART);
+          p[b] = reinterpret_cast<float4*>(a.parts + static_cast<size_t>(2 * k + (first_unit(k) >= tu0 ? 0 : 1)) * S::PART);
 #pragma unroll
           for (int m = 0; m < MT; ++m) v[b][m] = __ldcg(p[b] + m * W4_THREADS + tid);
         }
@@ -523,7 +539,8 @@ flux_status_t w4_launch(const W4Args& a, const DeviceInfo& dev, cudaStream_t s) 
   const long long col_tiles = (a.N + W4_COLS - 1) / W4_COLS;
   const long long row_tiles = a.mode == W4_DENSE ? (a.slots + MT * 8 - 1) / (MT * 8) : a.slots;
   const long long units = row_tiles * col_tiles * a.runs;
-  const int grid = static_cast<int>(std::min<long long>(units, std::min(2 * dev.sm_count, W4_MAX_CTAS)));
+  if (units > INT_MAX) return FLUX_ERR_UNSUPPORTED;
+  const int grid = static_cast<int>(std::min<long long>(units, std::min(W4Shape<MT, SR>::CTAS * dev.sm_count, W4_MAX_CTAS)));
   w4_kernel<DT, MT, SR><<<grid, W4_THREADS, smem, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
