@@ -11,8 +11,10 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "flux_host.h"
+#include "flux_ptx.cuh"
 #include "flux_rows.cuh"
 
 namespace flux {
@@ -23,10 +25,28 @@ constexpr int W4_RUN = 128;  // inputs per run of 64 bytes
 
 enum W4Mode { W4_DENSE = 0, W4_LAYER0 = 1, W4_LAYER1 = 2 };
 
-constexpr int W4_WARPS = 8, W4_THREADS = W4_WARPS * 32;
-constexpr int W4_COLS = W4_WARPS * 16;      // columns of a tile: 16 for each warp
-constexpr int W4_MAX_CTAS = 3 * 160;        // at most three CTAs per SM
+constexpr int W4_WARPS = 4, W4_THREADS = W4_WARPS * 32;
+constexpr int W4_CA = 2;                         // A operands (16 columns each) of a warp
+constexpr int W4_COLS = W4_WARPS * 16 * W4_CA;   // columns of a tile
+constexpr int W4_MIN_UNITS = 4;
+constexpr int W4_MAX_CTAS = 4 * 160;             // at most four CTAs per SM
 constexpr int W4_RUN_BYTES = W4_RUN / 2;
+constexpr int W4_NONE = 0xFFFF;                  // row tile of a slot whose expert id is out of range
+
+// Equal stretches of units: CTA i has the units [first(i), first(i + 1)).
+struct W4Split {
+  int each, more;  // the first `more` CTAs have one unit more
+  __device__ __forceinline__ int first(int cta) const { return cta * each + min(cta, more); }
+  __device__ __forceinline__ int cta_of(int unit) const {
+    const int big = more * (each + 1);
+    return unit < big ? unit / (each + 1) : more + (unit - big) / each;
+  }
+};
+
+// Where a slot's sums are: its row tile (W4_NONE: nowhere) and its row in it.
+struct W4Slot {
+  uint16_t tile, row;
+};
 
 struct W4Args {
   const uint16_t* x;
@@ -36,9 +56,13 @@ struct W4Args {
   const float* weights;
   uint16_t* out;
   uint32_t* hdr;
-  uint32_t* cut;        // [grid] arrivals at the tile that CTA i is the first of several to work on
-  uint32_t* done;       // [column tiles] layer1: finished row tiles
-  float* parts;         // [2 grid] partial tiles: of each CTA's first and last
+  // how the products' kernel cut its units, for the one that joins them: known to
+  // the host (dense) or left in the workspace
+  W4Split dense_split;
+  W4Split* split;
+  W4Slot* where;        // [slots]
+  uint32_t* joined;     // blocks of the joining kernel that are done with those
+  float* parts;         // [2 grid] sums of cut tiles: of each CTA's first and last
   float* rows_f32;      // layer1: [slots x N]
   int slots;            // rows of x . W: M, or T topk
   int T, N, K, runs, group, groups, E, topk, mode;
@@ -49,20 +73,27 @@ struct W4RowTile {
   uint16_t expert, first, rows;  // `rows` entries of the slot order from `first`
 };
 
-// 16 x 8 += 16 x 16 . 16 x 8; A four and B two registers of two 16-bit values.
-template <int DT>
+// d (+)= 16 x 16 . 16 x 8; A four and B two registers of two 16-bit values.
+// A kernel launched behind this one may start; and, in that kernel, the wait for
+// everything this one has written.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <int DT, bool FROM_ZERO>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                             uint32_t b1) {
+  const float c0 = FROM_ZERO ? 0.0f : d[0], c1 = FROM_ZERO ? 0.0f : d[1], c2 = FROM_ZERO ? 0.0f : d[2],
+              c3 = FROM_ZERO ? 0.0f : d[3];
   if constexpr (DT == 1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
   } else {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
   }
 }
 
@@ -102,6 +133,26 @@ __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&p)[4]) {
   }
 }
 
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+// Codes are read once, 64 bytes of a column at a time; the hint has L2 fetch the
+// next runs of the column with them.
+__device__ __forceinline__ uint4 load_codes(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+template <int DT>
+__device__ __forceinline__ float shared_scale(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return unpack2<DT>(v).x;
+}
+
 // 16 bytes to shared memory, or zeros where `take` is false.
 __device__ __forceinline__ void copy16_or_zero(void* smem, const void* gmem, bool take) {
   const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
@@ -111,13 +162,15 @@ __device__ __forceinline__ void copy16_or_zero(void* smem, const void* gmem, boo
 // MT tiles of 8 rows; SR scales per run and column (a group of 128 or a multiple: 1, of 64: 2, else 4).
 template <int MT, int SR>
 struct W4Shape {
-  static constexpr int CHUNK = MT == 1 ? 24 : MT == 2 ? 16 : 8;  // runs whose rows of x and scales are in shared memory
+  static constexpr int CTAS = MT == 4 ? 2 : 4;                  // per SM
+  static constexpr int AHEAD = 2;                               // runs of codes that a thread has on the way
+  static constexpr int CHUNK = MT == 1 ? 6 : MT == 2 ? 4 : 2;   // runs whose rows of x and scales make one buffer
+  static_assert(CHUNK % AHEAD == 0, "the words on the way keep their places from one buffer to the next");
   static constexpr int XRUN = MT * 8 * W4_RUN * 2;
   static constexpr int SRUN = SR * W4_COLS * 2;
-  static constexpr int SMEM = CHUNK * (XRUN + SRUN);
-  static constexpr int AHEAD = 4;                // runs of codes that a thread has on the way
-  static constexpr int CTAS = 2;                 // per SM
-  static constexpr int PART = W4_COLS * MT * 8;  // floats of a partial tile
+  static constexpr int BUFFER = CHUNK * (XRUN + SRUN);
+  static constexpr int SMEM = 2 * BUFFER;
+  static constexpr int PART = W4_COLS * MT * 8;  // floats of a cut tile's sums
 };
 
 // out = x . W for few rows.  The work is units of one tile of 128 columns, up
@@ -125,26 +178,25 @@ struct W4Shape {
 // runs of a tile, then the column tiles, then the row tiles, and every CTA
 // takes an equal stretch of them, so a tile may be cut between CTAs.
 //
-// A warp multiplies 16 columns: the codes are the A operand of 16 x 8 x 16
+// A warp multiplies 32 columns: the codes are two A operands of 16 x 8 x 16
 // tensor instructions, the rows of x the B operand (a matrix-vector product
 // leaves 7 of its 8 columns idle, which costs nothing: the kernel is bound by
 // the bytes of the codes and by the instructions that unpack them).  Every
-// thread copies the words that it will unpack itself; rows of x and scales are
-// shared by the CTA, in a ring of STAGES runs with one barrier per run.
+// thread loads the words that it will unpack itself, AHEAD runs ahead; rows of
+// x and scales are shared by the CTA, in two buffers of CHUNK runs, one filled
+// while the other is used.
 //
 // The sums of a group are exact products in fp32, then scaled into the tile's
-// sums.  The CTAs that share a tile leave their sums in the workspace, and the
-// last to arrive adds them in CTA order: repeat calls give the same bits.
+// sums.  CTAs that share a tile leave their sums in the workspace, where
+// w4_join_kernel adds them in CTA order: repeat calls give the same bits.
 template <int DT, int MT, int SR>
 __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel(const __grid_constant__ W4Args a) {
   using S = W4Shape<MT, SR>;
-  extern __shared__ uint4 ring4[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>(ring4);
+  extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint16_t order[FLUX_W4_MAX_ROWS];       // slots by expert
   __shared__ W4RowTile tiles[FLUX_W4_MAX_ROWS];
   int* hist = reinterpret_cast<int*>(ring);  // before the ring is used
   __shared__ int scan[2][W4_WARPS];
-  __shared__ int last_here;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int col_tiles = (a.N + W4_COLS - 1) / W4_COLS;
   int row_tiles;
@@ -167,14 +219,13 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
     }
     if (bad) atomicCAS(a.hdr, 0u, static_cast<uint32_t>(FLUX_ERR_INVALID_ARG));
     __syncthreads();
-    // exclusive sums of slots and row tiles; thread i has the experts 4 i .. 4 i + 3
-    int n[4], slots = 0, rt = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int e = tid * 4 + k;
-      n[k] = e < a.E ? hist[e] : 0;
-      slots += n[k];
-      rt += (n[k] + MT * 8 - 1) / (MT * 8);
+    // exclusive sums of slots and row tiles over the experts
+    constexpr int PER = FLUX_MAX_EXPERTS / W4_THREADS;
+    int slots = 0, rt = 0;
+    for (int k = 0; k < PER; ++k) {
+      const int e = tid * PER + k, n = e < a.E ? hist[e] : 0;
+      slots += n;
+      rt += (n + MT * 8 - 1) / (MT * 8);
     }
     int s0 = slots, r0 = rt;
 #pragma unroll
@@ -201,14 +252,13 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
       }
       row_tiles += scan[1][w];
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int e = tid * 4 + k;
+    for (int k = 0; k < PER; ++k) {
+      const int e = tid * PER + k, n = e < a.E ? hist[e] : 0;
       if (e < a.E) hist[e] = s0;
-      for (int m = 0; m < n[k]; m += MT * 8)
+      for (int m = 0; m < n; m += MT * 8)
         tiles[r0++] = W4RowTile{static_cast<uint16_t>(e), static_cast<uint16_t>(s0 + m),
-                                static_cast<uint16_t>(min(MT * 8, n[k] - m))};
-      s0 += n[k];
+                                static_cast<uint16_t>(min(MT * 8, n - m))};
+      s0 += n;
     }
     __syncthreads();
     if (warp == 0) {
@@ -218,251 +268,281 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
         const unsigned same = __match_any_sync(0xFFFFFFFFu, in ? e : -1 - lane);
         const int at = in ? hist[e] : 0;
         __syncwarp();
+        const int place = at + __popc(same & ((1u << lane) - 1u));
         if (in) {
-          order[at + __popc(same & ((1u << lane) - 1u))] = static_cast<uint16_t>(i);
+          order[place] = static_cast<uint16_t>(i);
           if (lane == __ffs(same) - 1) hist[e] = at + __popc(same);
         }
         __syncwarp();
+        if (blockIdx.x == 0 && i < a.slots && !in) a.where[i] = W4Slot{W4_NONE, 0};
       }
     }
     __syncthreads();
-    if (a.mode == W4_LAYER0) {  // slots of no expert
-      for (int i = blockIdx.x; i < a.slots; i += gridDim.x) {
-        const int e = a.ids[i];
-        if (e < 0 || e >= a.E)
-          for (int k = tid * 8; k < a.N; k += W4_THREADS * 8)
-            *reinterpret_cast<uint4*>(a.out + static_cast<size_t>(i) * a.N + k) = make_uint4(0, 0, 0, 0);
-      }
-    } else if (row_tiles == 0) {
-      for (size_t k = (static_cast<size_t>(blockIdx.x) * W4_THREADS + tid) * 8; k < static_cast<size_t>(a.T) * a.N;
-           k += static_cast<size_t>(gridDim.x) * W4_THREADS * 8)
-        *reinterpret_cast<uint4*>(a.out + k) = make_uint4(0, 0, 0, 0);
+    if (blockIdx.x == 0) {
+      for (int r = warp; r < row_tiles; r += W4_WARPS)
+        for (int m = lane; m < tiles[r].rows; m += 32)
+          a.where[order[tiles[r].first + m]] = W4Slot{static_cast<uint16_t>(r), static_cast<uint16_t>(m)};
     }
   }
 
   const int units = row_tiles * col_tiles * a.runs;
   // every CTA that works has a unit: the arrivals at a cut tile are counted by CTA
   const int ctas = min(static_cast<int>(gridDim.x), units), me = blockIdx.x;
+  launch_dependents();
   if (me >= ctas) return;
-  const int each = units / ctas, more = units - each * ctas;  // the first `more` CTAs have one unit more
-  auto first_unit = [&](int cta) { return cta * each + min(cta, more); };
-  auto cta_of = [&](int unit) {
-    const int big = more * (each + 1);
-    return unit < big ? unit / (each + 1) : more + (unit - big) / each;
-  };
-  const int u0 = first_unit(me), n_units = first_unit(me + 1) - u0;
+  const W4Split split{units / ctas, units % ctas};
+  if (me == 0 && tid == 0 && a.mode != W4_DENSE) *a.split = split;
+  const int u0 = split.first(me), n_units = split.first(me + 1) - u0;
   int tile = u0 / a.runs, run = u0 - tile * a.runs;
 
-  const int x_from0 = g * 256 + c * 16 + ((g & 1) << 6), x_from1 = x_from0 ^ 64;
+  const uint32_t ring_at = smem_u32(ring), x_from = g * 256 + c * 16 + ((g & 1) << 6),
+                 sc_from = S::CHUNK * S::XRUN + (warp * 16 * W4_CA + g) * 2;
   constexpr int P = S::AHEAD;
-  constexpr int XROWS = MT == 1 ? 8 : 16, XRUNS = 16 / XROWS;  // rows and runs of x that the CTA copies at a time
-  int todo = n_units;
-#pragma unroll 1
-  for (bool first_tile = true; todo > 0; ++tile, run = 0, first_tile = false) {
-    const int n_runs = min(a.runs - run, todo);
-    const bool whole = n_runs == a.runs;
-    todo -= n_runs;
-    const int rt_i = tile / col_tiles, ct = tile - rt_i * col_tiles, col0 = ct * W4_COLS;
+
+  // rows of x and scales of n runs from `first` of a tile, into one buffer
+  auto stage = [&](uint8_t* to, int of_tile, int first, int n) {
+    const int rt_i = of_tile / col_tiles, col0 = (of_tile - rt_i * col_tiles) * W4_COLS;
     const W4RowTile rt = tiles[rt_i];
-    // this thread's words of the columns g and g + 8 of the warp's 16
-    const int my_col = col0 + warp * 16 + g;
-    const uint4* qa = reinterpret_cast<const uint4*>(
-        a.q + ((static_cast<size_t>(rt.expert) * a.N + min(my_col, a.N - 1)) * a.runs + run) * W4_RUN_BYTES + c * 16);
-    const uint4* qb = reinterpret_cast<const uint4*>(
-        a.q + ((static_cast<size_t>(rt.expert) * a.N + min(my_col + 8, a.N - 1)) * a.runs + run) * W4_RUN_BYTES + c * 16);
-    uint4 wa[P], wb[P];
+    // rows in 16-byte chunks (8 inputs): chunk 4 j + c of a row lies at
+    // 4 (j ^ (row & 1)) + c, so that two rows' reads meet different banks
+    const int k = tid & 15, k0 = first * W4_RUN + k * 8;
+    static_assert(W4_THREADS / 16 == 8, "eight rows of x at a time");
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      if (i < n_runs) {
-        wa[i] = __ldcs(qa + i * 4);
-        wb[i] = __ldcs(qb + i * 4);
+    for (int p = 0; p < MT; ++p) {
+      const int m = p * 8 + (tid >> 4);
+      if (m < rt.rows) {
+        const int slot = order[rt.first + m];
+        const uint16_t* row = a.x + static_cast<size_t>(a.mode == W4_LAYER0 ? slot / a.topk : slot) * a.K;
+        uint8_t* at = to + m * 256 + ((k ^ ((m & 1) << 2)) << 4);
+        for (int r = 0; r < n; ++r) {
+          const int in = k0 + r * W4_RUN;
+          copy16_or_zero(at + r * S::XRUN, row + (in < a.K ? in : 0), in < a.K);
+        }
       }
     }
-    float acc[MT][4] = {};
-#pragma unroll 1
-    for (int r0 = 0; r0 < n_runs; r0 += S::CHUNK) {
-      const int n = min(S::CHUNK, n_runs - r0);
-      __syncthreads();  // the last chunk has been read
-      // rows of x in 16-byte chunks (8 inputs): chunk 4 j + c of a row lies at
-      // 4 (j ^ (row & 1)) + c, so that two rows' reads meet different banks
-      {
-        const int k = tid & 15, k0 = (run + r0) * W4_RUN + k * 8;
+    constexpr int AT_ONCE = W4_THREADS / (SR * W4_COLS / 8);
+    const int sr = tid / (W4_COLS / 8) % SR, col = tid % (W4_COLS / 8) * 8;
+    for (int r = tid / (SR * W4_COLS / 8); r < n; r += AT_ONCE) {
+      const int at = (first + r) * W4_RUN + sr * (W4_RUN / SR);
+      const bool in = at < a.K && col0 + col < a.N;
+      const size_t from = (static_cast<size_t>(rt.expert) * a.groups + (in ? at / a.group : 0)) * a.N + (in ? col0 + col : 0);
+      copy16_or_zero(to + S::CHUNK * S::XRUN + r * S::SRUN + (sr * W4_COLS + col) * 2, a.scales + from, in);
+    }
+  };
+  // this thread's words: columns g and g + 8 of each of the warp's 16
+  constexpr int HALVES = 2 * W4_CA;
+  const uint4* q[HALVES];
+  uint4 words[P][HALVES];
+  auto load_words = [&](int of_tile, int first, int n) {
+    const int rt_i = of_tile / col_tiles, col = (of_tile - rt_i * col_tiles) * W4_COLS + warp * 16 * W4_CA + g;
+    const size_t col0 = static_cast<size_t>(tiles[rt_i].expert) * a.N;
 #pragma unroll
-        for (int p = 0; p < (MT * 8 + 15) / 16; ++p) {
-          const int m = p * 16 + (tid >> 4) % XROWS;
-          if (m < rt.rows) {
-            const int slot = order[rt.first + m];
-            const uint16_t* row = a.x + static_cast<size_t>(a.mode == W4_LAYER0 ? slot / a.topk : slot) * a.K;
-            uint8_t* to = ring + m * 256 + ((k ^ ((m & 1) << 2)) << 4);
-#pragma unroll 4
-            for (int r = (tid >> 4) / XROWS; r < n; r += XRUNS) {
-              const int at = k0 + r * W4_RUN;
-              copy16_or_zero(to + r * S::XRUN, row + (at < a.K ? at : 0), at < a.K);
-            }
-          }
-        }
-        constexpr int AT_ONCE = W4_THREADS / (SR * W4_COLS / 8);
-        const int sr = tid / (W4_COLS / 8) % SR, col = tid % (W4_COLS / 8) * 8;
-        for (int r = tid / (SR * W4_COLS / 8); r < n; r += AT_ONCE) {
-          const int at = (run + r0 + r) * W4_RUN + sr * (W4_RUN / SR);
-          const bool in = at < a.K && col0 + col < a.N;
-          const size_t from = (static_cast<size_t>(rt.expert) * a.groups + (in ? at / a.group : 0)) * a.N + (in ? col0 + col : 0);
-          copy16_or_zero(ring + S::CHUNK * S::XRUN + r * S::SRUN + (sr * W4_COLS + col) * 2, a.scales + from, in);
-        }
-        copy_commit();
-        copy_wait<0>();
-      }
-      __syncthreads();
-      const uint8_t* xs = ring;
-      const uint16_t* sc = reinterpret_cast<const uint16_t*>(ring + S::CHUNK * S::XRUN) + warp * 16 + g;
+    for (int h = 0; h < HALVES; ++h) {
+      q[h] = reinterpret_cast<const uint4*>(a.q + ((col0 + min(col + 8 * h, a.N - 1)) * a.runs + first) * W4_RUN_BYTES + c * 16);
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (i < n) words[i][h] = load_codes(q[h] + i * 4);
+    }
+  };
+
+  int todo = n_units, buffer = 0;
+  int n_runs = min(a.runs - run, todo);
+  load_words(tile, run, n_runs);
+  stage(ring, tile, run, min(S::CHUNK, n_runs));
+  copy_commit();
 #pragma unroll 1
-      for (int r = 0; r < n; r += P, xs += P * S::XRUN, sc += P * S::SRUN / 2, qa += P * 4, qb += P * 4) {
+  for (bool first_tile = true; todo > 0; first_tile = false) {
+    const bool whole = n_runs == a.runs;
+    todo -= n_runs;
+    const int rt_i = tile / col_tiles, ct = tile - rt_i * col_tiles;
+    const W4RowTile rt = tiles[rt_i];
+    const int next_runs = min(a.runs, todo);  // of the next tile
+    float acc[W4_CA][MT][4] = {};
+    // n runs of the tile from r0, their rows of x and scales at `at`
+    auto multiply = [&](auto live_tiles, uint32_t at, int r0, int n) {
+      constexpr int LIVE = decltype(live_tiles)::value;
+      uint32_t x0 = at + x_from, x1 = x0 ^ 64, sc = at + sc_from;
+#pragma unroll 1
+      for (int r = 0; r < n; r += P) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           if (r + i >= n) break;
-          const uint32_t va[4] = {wa[i].x, wa[i].y, wa[i].z, wa[i].w}, vb[4] = {wb[i].x, wb[i].y, wb[i].z, wb[i].w};
-          if (r0 + r + i + P < n_runs) {
-            wa[i] = __ldcs(qa + (i + P) * 4);
-            wb[i] = __ldcs(qb + (i + P) * 4);
+          uint32_t w[HALVES][4];
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) {
+            w[h][0] = words[i][h].x, w[h][1] = words[i][h].y, w[h][2] = words[i][h].z, w[h][3] = words[i][h].w;
+            if (r0 + r + i + P < n_runs) words[i][h] = load_codes(q[h] + (i + P) * 4);
           }
-          float part[MT][4];
+          float part[W4_CA][LIVE][4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t pa[4], pb[4];
-            codes8<DT>(va[j], pa);
-            codes8<DT>(vb[j], pb);
+            uint4 xv[LIVE];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              if (m == 0 || rt.rows > m * 8) {
-                const uint4 xv = *reinterpret_cast<const uint4*>(xs + i * S::XRUN + (j & 1 ? x_from1 : x_from0) + (j >> 1) * 128 + m * 2048);
-                if (j % (4 / SR) == 0) {
+            for (int m = 0; m < LIVE; ++m) xv[m] = shared16((j & 1 ? x1 : x0) + i * S::XRUN + (j >> 1) * 128 + m * 2048);
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) part[m][k] = 0.0f;
-                }
-                mma_16x8x16<DT>(part[m], pa[0], pb[0], pa[1], pb[1], xv.x, xv.y);
-                mma_16x8x16<DT>(part[m], pa[2], pb[2], pa[3], pb[3], xv.z, xv.w);
+            for (int ca = 0; ca < W4_CA; ++ca) {
+              uint32_t pa[4], pb[4];
+              codes8<DT>(w[2 * ca][j], pa);
+              codes8<DT>(w[2 * ca + 1][j], pb);
+#pragma unroll
+              for (int m = 0; m < LIVE; ++m) {
+                if (j % (4 / SR) == 0) mma_16x8x16<DT, true>(part[ca][m], pa[0], pb[0], pa[1], pb[1], xv[m].x, xv[m].y);
+                else mma_16x8x16<DT, false>(part[ca][m], pa[0], pb[0], pa[1], pb[1], xv[m].x, xv[m].y);
+                mma_16x8x16<DT, false>(part[ca][m], pa[2], pb[2], pa[3], pb[3], xv[m].z, xv[m].w);
               }
             }
             if ((j + 1) % (4 / SR) == 0) {
-              const uint16_t* s = sc + i * (S::SRUN / 2) + j / (4 / SR) * W4_COLS;
-              const float s0 = unpack2<DT>(s[0]).x, s1 = unpack2<DT>(s[8]).x;
+              const uint32_t s = sc + i * S::SRUN + j / (4 / SR) * (W4_COLS * 2);
 #pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                if (m == 0 || rt.rows > m * 8) {
-                  acc[m][0] += s0 * part[m][0];
-                  acc[m][1] += s0 * part[m][1];
-                  acc[m][2] += s1 * part[m][2];
-                  acc[m][3] += s1 * part[m][3];
+              for (int ca = 0; ca < W4_CA; ++ca) {
+                const float s0 = shared_scale<DT>(s + ca * 32), s1 = shared_scale<DT>(s + ca * 32 + 16);
+#pragma unroll
+                for (int m = 0; m < LIVE; ++m) {
+                  acc[ca][m][0] += s0 * part[ca][m][0];
+                  acc[ca][m][1] += s0 * part[ca][m][1];
+                  acc[ca][m][2] += s1 * part[ca][m][2];
+                  acc[ca][m][3] += s1 * part[ca][m][3];
                 }
               }
             }
           }
         }
+        x0 += P * S::XRUN;
+        x1 += P * S::XRUN;
+        sc += P * S::SRUN;
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) q[h] += P * 4;
+      }
+    };
+#pragma unroll 1
+    for (int r0 = 0; r0 < n_runs; r0 += S::CHUNK) {
+      const int n = min(S::CHUNK, n_runs - r0);
+      copy_wait<0>();
+      __syncthreads();  // this buffer is filled, the other one has been read
+      if (r0 + n < n_runs) stage(ring + (buffer ^ 1) * S::BUFFER, tile, run + r0 + n, min(S::CHUNK, n_runs - r0 - n));
+      else if (next_runs > 0) stage(ring + (buffer ^ 1) * S::BUFFER, tile + 1, 0, min(S::CHUNK, next_runs));
+      copy_commit();
+      const uint32_t at = ring_at + buffer * S::BUFFER;
+      buffer ^= 1;
+      // by the row tiles of 8 that are there, tested here: instructions on absent
+      // ones would run all the same inside the loop
+      if constexpr (MT == 1) {
+        multiply(std::integral_constant<int, 1>{}, at, r0, n);
+      } else {
+        if (rt.rows <= 8) multiply(std::integral_constant<int, 1>{}, at, r0, n);
+        else if (MT == 2 || rt.rows <= 16) multiply(std::integral_constant<int, 2>{}, at, r0, n);
+        else multiply(std::integral_constant<int, MT>{}, at, r0, n);
       }
     }
+    ++tile;
+    run = 0;
+    n_runs = next_runs;
+    if (next_runs > 0) load_words(tile, 0, next_runs);  // on their way while this tile is written
 
-    if (!whole) {
-      // leave the sums; the last CTA of the tile adds everybody's
-      const int place = 2 * me + (first_tile ? 0 : 1);
-      float4* mine = reinterpret_cast<float4*>(a.parts + static_cast<size_t>(place) * S::PART);
+    // columns g and g + 8 of each of the warp's 16, rows 2 c and 2 c + 1 of every
+    // eight; a cut tile's sums go to the workspace, by rows
+    float* part = a.parts + static_cast<size_t>(2 * me + (first_tile ? 0 : 1)) * S::PART;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) mine[m * W4_THREADS + tid] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
-      __threadfence();
-      __syncthreads();
-      const int tu0 = tile * a.runs, c0 = cta_of(tu0), c1 = cta_of(tu0 + a.runs - 1);
-      if (tid == 0) {
-        const uint32_t seen = atomicAdd(a.cut + c0, 1u);
-        last_here = seen == static_cast<uint32_t>(c1 - c0);
-        if (last_here) a.cut[c0] = 0u;
+    for (int m = 0; m < MT; ++m) {
+      if (m * 8 >= rt.rows) break;
+#pragma unroll
+      for (int ca = 0; ca < W4_CA; ++ca) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = m * 8 + 2 * c + (i & 1), col = (warp * W4_CA + ca) * 16 + g + (i >> 1) * 8, n = ct * W4_COLS + col;
+          if (r >= rt.rows || n >= a.N) continue;
+          if (!whole) {
+            part[r * W4_COLS + col] = acc[ca][m][i];
+          } else {
+            const size_t at = static_cast<size_t>(order[rt.first + r]) * a.N + n;
+            if (a.mode == W4_LAYER1) a.rows_f32[at] = acc[ca][m][i];
+            else a.out[at] = static_cast<uint16_t>(pack2<DT>(acc[ca][m][i], 0.0f));
+          }
+        }
       }
-      __syncthreads();
-      if (!last_here) continue;
-      __threadfence();
-#pragma unroll
-      for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.0f;
-      constexpr int BATCH = MT == 1 ? 4 : 2;  // CTAs whose loads are in flight together
+    }
+  }
+}
+
+constexpr int W4_JOIN_THREADS = 128;
+
+// The second half of a product: adds the parts of cut tiles in CTA order, for
+// layer1 the tokens' slots in slot order, and writes zeros for slots of no
+// expert.  Four columns of one row of the output per thread.  Leaves what it
+// reads of the workspace zero.
+template <int DT, int MT>
+__global__ void __launch_bounds__(W4_JOIN_THREADS) w4_join_kernel(const __grid_constant__ W4Args a) {
+  constexpr int PART = W4_COLS * MT * 8;
+  constexpr int BATCH = 8;  // loads in flight together
+  wait_for_primary();
+  const int n = (blockIdx.x * W4_JOIN_THREADS + threadIdx.x) * 4;
+  const int col_tiles = (a.N + W4_COLS - 1) / W4_COLS, ct = n / W4_COLS, col = n - ct * W4_COLS;
+  const W4Split split = a.mode == W4_DENSE ? a.dense_split : *a.split;
+  const int row = blockIdx.y, per = a.mode == W4_LAYER1 ? a.topk : 1;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  bool write = n < a.N;
+  for (int j = 0; j < per && write; ++j) {
+    const int slot = row * per + j;
+    W4Slot at{static_cast<uint16_t>(slot / (MT * 8)), static_cast<uint16_t>(slot % (MT * 8))};
+    if (a.mode != W4_DENSE) {
+      at = a.where[slot];
+      if (at.tile == W4_NONE) continue;
+    }
+    const int unit = (at.tile * col_tiles + ct) * a.runs, c0 = split.cta_of(unit), c1 = split.cta_of(unit + a.runs - 1);
+    const float w = a.mode == W4_LAYER1 ? a.weights[slot] : 1.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c0 == c1) {
+      if (a.mode != W4_LAYER1) {
+        write = false;  // written already
+        break;
+      }
+      float4* p = reinterpret_cast<float4*>(a.rows_f32 + static_cast<size_t>(slot) * a.N + n);
+      v = *p;
+      *p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    } else {
       for (int k0 = c0; k0 <= c1; k0 += BATCH) {
-        float4 v[BATCH][MT];
-        float4* p[BATCH];
+        float4 f[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+          const int k = min(k0 + b, c1);
+          // the tile is the first of CTA k unless it begins inside its stretch
+          f[b] = *reinterpret_cast<const float4*>(a.parts + static_cast<size_t>(2 * k + (split.first(k) >= unit ? 0 : 1)) * PART +
+                                                  at.row * W4_COLS + col);
+        }
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
           const int k = k0 + b;
           if (k > c1) break;
-          // the tile is the first of CTA k unless it begins inside its stretch
-          p[b] = reinterpret_cast<float4*>(a.parts + static_cast<size_t>(2 * k + (first_unit(k) >= tu0 ? 0 : 1)) * S::PART);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) v[b][m] = __ldcg(p[b] + m * W4_THREADS + tid);
-        }
-#pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-          if (k0 + b > c1) break;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            p[b][m * W4_THREADS + tid] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            acc[m][0] += v[b][m].x;
-            acc[m][1] += v[b][m].y;
-            acc[m][2] += v[b][m].z;
-            acc[m][3] += v[b][m].w;
-          }
+          *reinterpret_cast<float4*>(a.parts + static_cast<size_t>(2 * k + (split.first(k) >= unit ? 0 : 1)) * PART +
+                                     at.row * W4_COLS + col) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          v.x += f[b].x;
+          v.y += f[b].y;
+          v.z += f[b].z;
+          v.w += f[b].w;
         }
       }
     }
-    // columns g and g + 8 of the warp's 16, rows 2 c and 2 c + 1 of every eight
-    const int col = ct * W4_COLS + warp * 16 + g;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = m * 8 + 2 * c + (i & 1), n = col + (i >> 1) * 8;
-        if (r < rt.rows && n < a.N) {
-          const size_t at = static_cast<size_t>(order[rt.first + r]) * a.N + n;
-          if (a.mode == W4_LAYER1) a.rows_f32[at] = acc[m][i];
-          else a.out[at] = static_cast<uint16_t>(pack2<DT>(acc[m][i], 0.0f));
-        }
-      }
-    }
-    if (a.mode != W4_LAYER1) continue;
-    // the last row tile of these columns adds the slots of every token
+    sum.x += w * v.x;
+    sum.y += w * v.y;
+    sum.z += w * v.z;
+    sum.w += w * v.w;
+  }
+  if (write)
+    *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(row) * a.N + n) = make_uint2(pack2<DT>(sum.x, sum.y), pack2<DT>(sum.z, sum.w));
+  if (a.mode == W4_DENSE) return;
+  // the last block takes the routing out of the workspace
+  __shared__ int last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
     __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      last_here = atomicAdd(a.done + ct, 1u) == static_cast<uint32_t>(row_tiles - 1);
-      if (last_here) a.done[ct] = 0u;
-    }
-    __syncthreads();
-    if (!last_here) continue;
-    __threadfence();
-    const int cols = min(W4_COLS, a.N - ct * W4_COLS);
-    for (int i = tid; i < a.T * (W4_COLS / 4); i += W4_THREADS) {
-      const int t = i / (W4_COLS / 4), n = i % (W4_COLS / 4) * 4;
-      if (n >= cols) continue;
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int k0 = 0; k0 < a.topk; k0 += 8) {
-        float4 v[8];
-        float w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int slot = t * a.topk + k0 + k;
-          const int e = k0 + k < a.topk ? a.ids[slot] : -1;
-          const bool in = e >= 0 && e < a.E;
-          w[k] = in ? a.weights[slot] : 0.0f;
-          v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (in) v[k] = __ldcg(reinterpret_cast<const float4*>(a.rows_f32 + static_cast<size_t>(slot) * a.N + ct * W4_COLS + n));
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (k0 + k < a.topk)
-            *reinterpret_cast<float4*>(a.rows_f32 + static_cast<size_t>(t * a.topk + k0 + k) * a.N + ct * W4_COLS + n) =
-                make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          s.x += w[k] * v[k].x;
-          s.y += w[k] * v[k].y;
-          s.z += w[k] * v[k].z;
-          s.w += w[k] * v[k].w;
-        }
-      }
-      *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(t) * a.N + ct * W4_COLS + n) =
-          make_uint2(pack2<DT>(s.x, s.y), pack2<DT>(s.z, s.w));
-    }
+    last = atomicAdd(a.joined, 1u) == gridDim.x * gridDim.y - 1;
+  }
+  __syncthreads();
+  if (last == 0) return;
+  for (int i = threadIdx.x; i < a.slots; i += W4_JOIN_THREADS) a.where[i] = W4Slot{0, 0};
+  if (threadIdx.x == 0) {
+    *a.split = W4Split{0, 0};
+    *a.joined = 0u;
   }
 }
 
@@ -505,7 +585,7 @@ w4_quantize_kernel(int K, int N, int runs, int group, int groups, const void* __
 
 // Workspace: header, arrivals, finished row tiles, partial tiles, fp32 rows.
 struct W4Ws {
-  size_t cut, done, parts, rows, total;
+  size_t split, joined, where, parts, rows, total;
 };
 
 int w4_row_tiles_of_8(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
@@ -518,8 +598,9 @@ W4Ws w4_ws(int slots, int N) {
     at += round_up(bytes, WS_ALIGN);
     return here;
   };
-  w.cut = take(sizeof(uint32_t) * W4_MAX_CTAS);
-  w.done = take(sizeof(uint32_t) * ((N + W4_COLS - 1) / W4_COLS));
+  w.split = take(sizeof(W4Split));
+  w.joined = take(sizeof(uint32_t));
+  w.where = take(sizeof(W4Slot) * slots);
   w.parts = take(sizeof(float) * 2 * W4_MAX_CTAS * W4_COLS * 8 * w4_row_tiles_of_8(slots));
   w.rows = take(sizeof(float) * slots * static_cast<size_t>(N));
   w.total = at;
@@ -527,7 +608,7 @@ W4Ws w4_ws(int slots, int N) {
 }
 
 template <int DT, int MT, int SR>
-flux_status_t w4_launch(const W4Args& a, const DeviceInfo& dev, cudaStream_t s) {
+flux_status_t w4_launch(W4Args a, const DeviceInfo& dev, cudaStream_t s) {
   constexpr int smem = W4Shape<MT, SR>::SMEM;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
@@ -540,9 +621,24 @@ flux_status_t w4_launch(const W4Args& a, const DeviceInfo& dev, cudaStream_t s) 
   const long long row_tiles = a.mode == W4_DENSE ? (a.slots + MT * 8 - 1) / (MT * 8) : a.slots;
   const long long units = row_tiles * col_tiles * a.runs;
   if (units > INT_MAX) return FLUX_ERR_UNSUPPORTED;
-  const int grid = static_cast<int>(std::min<long long>(units, std::min(W4Shape<MT, SR>::CTAS * dev.sm_count, W4_MAX_CTAS)));
+  const long long fill = std::min(W4Shape<MT, SR>::CTAS * dev.sm_count, W4_MAX_CTAS);
+  const int grid = static_cast<int>(std::min(units, std::max(std::min(fill, units / W4_MIN_UNITS), std::min<long long>(fill, dev.sm_count))));
+  a.dense_split = W4Split{static_cast<int>(units / grid), static_cast<int>(units % grid)};
   w4_kernel<DT, MT, SR><<<grid, W4_THREADS, smem, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  // no tile is cut if the CTAs' stretches are whole tiles
+  if (a.mode == W4_DENSE && units % grid == 0 && units / grid % a.runs == 0) return FLUX_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.N + 4 * W4_JOIN_THREADS - 1) / (4 * W4_JOIN_THREADS), a.mode == W4_LAYER1 ? a.T : a.slots, 1);
+  cfg.blockDim = dim3(W4_JOIN_THREADS, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr_pdl[1];
+  attr_pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr_pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr_pdl;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, w4_join_kernel<DT, MT>, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
@@ -555,8 +651,10 @@ flux_status_t w4_launch_groups(const W4Args& a, const DeviceInfo& dev, cudaStrea
 
 template <int DT>
 flux_status_t w4_launch_rows(const W4Args& a, const DeviceInfo& dev, cudaStream_t s) {
-  // the most rows one expert can have
-  const int mt = w4_row_tiles_of_8(a.mode == W4_DENSE ? a.slots : a.T);
+  // rows of one tile: all of them, and for the experts about twice what one gets
+  // on the average (an expert with more rows has several tiles, whose codes
+  // come from L2 again)
+  const int mt = w4_row_tiles_of_8(a.mode == W4_DENSE ? a.slots : std::min(a.T, 2 * ((a.slots + a.E - 1) / a.E)));
   if (mt == 1) return w4_launch_groups<DT, 1>(a, dev, s);
   if (mt == 2) return w4_launch_groups<DT, 2>(a, dev, s);
   return w4_launch_groups<DT, 4>(a, dev, s);
@@ -597,8 +695,9 @@ flux_status_t w4_run(W4Mode mode, int rows, int slots, int T, int N, int K, int 
   a.weights = weights;
   a.out = static_cast<uint16_t*>(out);
   a.hdr = static_cast<uint32_t*>(workspace);
-  a.cut = reinterpret_cast<uint32_t*>(ws + w.cut);
-  a.done = reinterpret_cast<uint32_t*>(ws + w.done);
+  a.split = reinterpret_cast<W4Split*>(ws + w.split);
+  a.joined = reinterpret_cast<uint32_t*>(ws + w.joined);
+  a.where = reinterpret_cast<W4Slot*>(ws + w.where);
   a.parts = reinterpret_cast<float*>(ws + w.parts);
   a.rows_f32 = reinterpret_cast<float*>(ws + w.rows);
   a.slots = slots;
