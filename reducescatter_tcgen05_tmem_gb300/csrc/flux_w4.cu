@@ -29,7 +29,7 @@ constexpr int W4_WARPS = 4, W4_THREADS = W4_WARPS * 32;
 constexpr int W4_CA = 2;                         // A operands (16 columns each) of a warp
 constexpr int W4_COLS = W4_WARPS * 16 * W4_CA;   // columns of a tile
 constexpr int W4_MIN_UNITS = 4;
-constexpr int W4_MAX_CTAS = 4 * 160;             // at most four CTAs per SM
+constexpr int W4_MAX_CTAS = 5 * 160;             // at most five CTAs per SM
 constexpr int W4_RUN_BYTES = W4_RUN / 2;
 constexpr int W4_NONE = 0xFFFF;                  // row tile of a slot whose expert id is out of range
 
@@ -146,11 +146,13 @@ __device__ __forceinline__ uint4 load_codes(const uint4* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
+// Scales of four columns, each twice for the two rows it multiplies.
 template <int DT>
-__device__ __forceinline__ float shared_scale(uint32_t at) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
-  return unpack2<DT>(v).x;
+__device__ __forceinline__ void shared_scales(uint32_t at, f32x2 (&s)[4]) {
+  uint32_t lo, hi;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(lo), "=r"(hi) : "r"(at));
+  const float2 a = unpack2<DT>(lo), b = unpack2<DT>(hi);
+  s[0] = both(a.x), s[1] = both(a.y), s[2] = both(b.x), s[3] = both(b.y);
 }
 
 // 16 bytes to shared memory, or zeros where `take` is false.
@@ -162,7 +164,7 @@ __device__ __forceinline__ void copy16_or_zero(void* smem, const void* gmem, boo
 // MT tiles of 8 rows; SR scales per run and column (a group of 128 or a multiple: 1, of 64: 2, else 4).
 template <int MT, int SR>
 struct W4Shape {
-  static constexpr int CTAS = MT == 4 ? 2 : 4;                  // per SM
+  static constexpr int CTAS = MT == 4 ? 2 : MT == 2 ? 3 : 4;                  // per SM
   static constexpr int AHEAD = 2;                               // runs of codes that a thread has on the way
   static constexpr int CHUNK = MT == 1 ? 6 : MT == 2 ? 4 : 2;   // runs whose rows of x and scales make one buffer
   static_assert(CHUNK % AHEAD == 0, "the words on the way keep their places from one buffer to the next");
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
   int tile = u0 / a.runs, run = u0 - tile * a.runs;
 
   const uint32_t ring_at = smem_u32(ring), x_from = g * 256 + c * 16 + ((g & 1) << 6),
-                 sc_from = S::CHUNK * S::XRUN + (warp * 16 * W4_CA + g) * 2;
+                 sc_from = S::CHUNK * S::XRUN + (warp * 16 * W4_CA + g * 4) * 2;
   constexpr int P = S::AHEAD;
 
   // rows of x and scales of n runs from `first` of a tile, into one buffer
@@ -329,16 +331,18 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
       copy16_or_zero(to + S::CHUNK * S::XRUN + r * S::SRUN + (sr * W4_COLS + col) * 2, a.scales + from, in);
     }
   };
-  // this thread's words: columns g and g + 8 of each of the warp's 16
+  // this thread's words: columns 4 g + h of the warp's 32, which are the rows g and
+  // g + 8 of its two A operands; its scales and its sums are of neighbours then
   constexpr int HALVES = 2 * W4_CA;
+  static_assert(HALVES == 4, "a thread's columns are four neighbours");
   const uint4* q[HALVES];
   uint4 words[P][HALVES];
   auto load_words = [&](int of_tile, int first, int n) {
-    const int rt_i = of_tile / col_tiles, col = (of_tile - rt_i * col_tiles) * W4_COLS + warp * 16 * W4_CA + g;
+    const int rt_i = of_tile / col_tiles, col = (of_tile - rt_i * col_tiles) * W4_COLS + warp * 16 * W4_CA + g * 4;
     const size_t col0 = static_cast<size_t>(tiles[rt_i].expert) * a.N;
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
-      q[h] = reinterpret_cast<const uint4*>(a.q + ((col0 + min(col + 8 * h, a.N - 1)) * a.runs + first) * W4_RUN_BYTES + c * 16);
+      q[h] = reinterpret_cast<const uint4*>(a.q + ((col0 + min(col + h, a.N - 1)) * a.runs + first) * W4_RUN_BYTES + c * 16);
 #pragma unroll
       for (int i = 0; i < P; ++i)
         if (i < n) words[i][h] = load_codes(q[h] + i * 4);
@@ -357,7 +361,7 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
     const int rt_i = tile / col_tiles, ct = tile - rt_i * col_tiles;
     const W4RowTile rt = tiles[rt_i];
     const int next_runs = min(a.runs, todo);  // of the next tile
-    float acc[W4_CA][MT][4] = {};
+    f32x2 acc[HALVES][MT] = {};  // column 4 g + h of the warp's 32, rows 2 c and 2 c + 1 of each eight
     // n runs of the tile from r0, their rows of x and scales at `at`
     auto multiply = [&](auto live_tiles, uint32_t at, int r0, int n) {
       constexpr int LIVE = decltype(live_tiles)::value;
@@ -393,17 +397,13 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
             }
             if ((j + 1) % (4 / SR) == 0) {
               const uint32_t s = sc + i * S::SRUN + j / (4 / SR) * (W4_COLS * 2);
+              f32x2 f[HALVES];
+              shared_scales<DT>(s, f);
 #pragma unroll
-              for (int ca = 0; ca < W4_CA; ++ca) {
-                const float s0 = shared_scale<DT>(s + ca * 32), s1 = shared_scale<DT>(s + ca * 32 + 16);
+              for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-                for (int m = 0; m < LIVE; ++m) {
-                  acc[ca][m][0] += s0 * part[ca][m][0];
-                  acc[ca][m][1] += s0 * part[ca][m][1];
-                  acc[ca][m][2] += s1 * part[ca][m][2];
-                  acc[ca][m][3] += s1 * part[ca][m][3];
-                }
-              }
+                for (int m = 0; m < LIVE; ++m)
+                  acc[h][m] = fma2(f[h], pair(part[h / 2][m][h % 2 * 2], part[h / 2][m][h % 2 * 2 + 1]), acc[h][m]);
             }
           }
         }
@@ -439,25 +439,25 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
     n_runs = next_runs;
     if (next_runs > 0) load_words(tile, 0, next_runs);  // on their way while this tile is written
 
-    // columns g and g + 8 of each of the warp's 16, rows 2 c and 2 c + 1 of every
-    // eight; a cut tile's sums go to the workspace, by rows
+    // a cut tile's sums go to the workspace, by rows
     float* part = a.parts + static_cast<size_t>(2 * me + (first_tile ? 0 : 1)) * S::PART;
+    const int col = warp * 16 * W4_CA + g * 4, n = ct * W4_COLS + col;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if (m * 8 >= rt.rows) break;
 #pragma unroll
-      for (int ca = 0; ca < W4_CA; ++ca) {
+      for (int b = 0; b < 2; ++b) {
+        const int r = m * 8 + 2 * c + b;
+        if (r >= rt.rows || n >= a.N) continue;
+        float f[HALVES];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = m * 8 + 2 * c + (i & 1), col = (warp * W4_CA + ca) * 16 + g + (i >> 1) * 8, n = ct * W4_COLS + col;
-          if (r >= rt.rows || n >= a.N) continue;
-          if (!whole) {
-            part[r * W4_COLS + col] = acc[ca][m][i];
-          } else {
-            const size_t at = static_cast<size_t>(order[rt.first + r]) * a.N + n;
-            if (a.mode == W4_LAYER1) a.rows_f32[at] = acc[ca][m][i];
-            else a.out[at] = static_cast<uint16_t>(pack2<DT>(acc[ca][m][i], 0.0f));
-          }
+        for (int h = 0; h < HALVES; ++h) f[h] = b == 0 ? halves(acc[h][m]).x : halves(acc[h][m]).y;
+        const float4 v = make_float4(f[0], f[1], f[2], f[3]);
+        if (!whole) {
+          *reinterpret_cast<float4*>(part + r * W4_COLS + col) = v;
+        } else {
+          const size_t at = static_cast<size_t>(order[rt.first + r]) * a.N + n;
+          if (a.mode == W4_LAYER1) *reinterpret_cast<float4*>(a.rows_f32 + at) = v;
+          else *reinterpret_cast<uint2*>(a.out + at) = make_uint2(pack2<DT>(v.x, v.y), pack2<DT>(v.z, v.w));
         }
       }
     }
@@ -466,66 +466,99 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
 
 constexpr int W4_JOIN_THREADS = 128;
 
+// Sums of one slot's columns n .. n + 3 in the workspace, left zero there.
+template <int MT>
+struct W4Parts {
+  static constexpr int PART = W4_COLS * MT * 8;
+  const W4Args& a;
+  W4Split split;
+  int col_tiles, ct, col;
+  int unit, row, c0, c1;  // of the slot
+
+  // whether several CTAs have sums of the slot's tile
+  __device__ __forceinline__ bool open(W4Slot at) {
+    unit = (at.tile * col_tiles + ct) * a.runs;
+    row = at.row;
+    c0 = split.cta_of(unit);
+    c1 = split.cta_of(unit + a.runs - 1);
+    return c0 != c1;
+  }
+  __device__ __forceinline__ float4* part(int k) const {
+    // the tile is the first of CTA k unless it begins inside its stretch
+    return reinterpret_cast<float4*>(a.parts + static_cast<size_t>(2 * k + (split.first(k) >= unit ? 0 : 1)) * PART + row * W4_COLS + col);
+  }
+  // adds the parts of the CTAs from `first` on, BATCH loads in flight together
+  template <int BATCH>
+  __device__ __forceinline__ void add(int first, float4& v) const {
+    for (int k0 = first; k0 <= c1; k0 += BATCH) {
+      float4 f[BATCH];
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) f[b] = *part(min(k0 + b, c1));
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        if (k0 + b > c1) break;
+        *part(k0 + b) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        v.x += f[b].x;
+        v.y += f[b].y;
+        v.z += f[b].z;
+        v.w += f[b].w;
+      }
+    }
+  }
+};
+
 // The second half of a product: adds the parts of cut tiles in CTA order, for
 // layer1 the tokens' slots in slot order, and writes zeros for slots of no
 // expert.  Four columns of one row of the output per thread.  Leaves what it
 // reads of the workspace zero.
-template <int DT, int MT>
+template <int DT, int MT, bool LAYER1>
 __global__ void __launch_bounds__(W4_JOIN_THREADS) w4_join_kernel(const __grid_constant__ W4Args a) {
-  constexpr int PART = W4_COLS * MT * 8;
-  constexpr int BATCH = 8;  // loads in flight together
   wait_for_primary();
-  const int n = (blockIdx.x * W4_JOIN_THREADS + threadIdx.x) * 4;
-  const int col_tiles = (a.N + W4_COLS - 1) / W4_COLS, ct = n / W4_COLS, col = n - ct * W4_COLS;
-  const W4Split split = a.mode == W4_DENSE ? a.dense_split : *a.split;
-  const int row = blockIdx.y, per = a.mode == W4_LAYER1 ? a.topk : 1;
+  const int n = (blockIdx.x * W4_JOIN_THREADS + threadIdx.x) * 4, row = blockIdx.y;
+  const int col_tiles = (a.N + W4_COLS - 1) / W4_COLS, ct = n / W4_COLS;
+  W4Parts<MT> p{a, a.mode == W4_DENSE ? a.dense_split : *a.split, col_tiles, ct, n - ct * W4_COLS, 0, 0, 0, 0};
   float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   bool write = n < a.N;
-  for (int j = 0; j < per && write; ++j) {
-    const int slot = row * per + j;
-    W4Slot at{static_cast<uint16_t>(slot / (MT * 8)), static_cast<uint16_t>(slot % (MT * 8))};
-    if (a.mode != W4_DENSE) {
-      at = a.where[slot];
-      if (at.tile == W4_NONE) continue;
-    }
-    const int unit = (at.tile * col_tiles + ct) * a.runs, c0 = split.cta_of(unit), c1 = split.cta_of(unit + a.runs - 1);
-    const float w = a.mode == W4_LAYER1 ? a.weights[slot] : 1.0f;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (c0 == c1) {
-      if (a.mode != W4_LAYER1) {
-        write = false;  // written already
-        break;
+  if constexpr (LAYER1) {
+    // four slots at a time, the first load of each in flight together
+    constexpr int SLOTS = 4;
+    for (int j0 = 0; j0 < a.topk && write; j0 += SLOTS) {
+      float4 f[SLOTS];
+      W4Slot at[SLOTS];
+      float w[SLOTS];
+#pragma unroll
+      for (int j = 0; j < SLOTS; ++j) {
+        const int slot = row * a.topk + j0 + j;
+        at[j] = j0 + j < a.topk ? a.where[slot] : W4Slot{W4_NONE, 0};
+        w[j] = at[j].tile != W4_NONE ? a.weights[slot] : 0.0f;
       }
-      float4* p = reinterpret_cast<float4*>(a.rows_f32 + static_cast<size_t>(slot) * a.N + n);
-      v = *p;
-      *p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    } else {
-      for (int k0 = c0; k0 <= c1; k0 += BATCH) {
-        float4 f[BATCH];
 #pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-          const int k = min(k0 + b, c1);
-          // the tile is the first of CTA k unless it begins inside its stretch
-          f[b] = *reinterpret_cast<const float4*>(a.parts + static_cast<size_t>(2 * k + (split.first(k) >= unit ? 0 : 1)) * PART +
-                                                  at.row * W4_COLS + col);
-        }
+      for (int j = 0; j < SLOTS; ++j) {
+        f[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (at[j].tile == W4_NONE) continue;
+        f[j] = p.open(at[j]) ? *p.part(p.c0)
+                             : *reinterpret_cast<const float4*>(a.rows_f32 + static_cast<size_t>(row * a.topk + j0 + j) * a.N + n);
+      }
 #pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-          const int k = k0 + b;
-          if (k > c1) break;
-          *reinterpret_cast<float4*>(a.parts + static_cast<size_t>(2 * k + (split.first(k) >= unit ? 0 : 1)) * PART +
-                                     at.row * W4_COLS + col) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          v.x += f[b].x;
-          v.y += f[b].y;
-          v.z += f[b].z;
-          v.w += f[b].w;
-        }
+      for (int j = 0; j < SLOTS; ++j) {
+        if (at[j].tile == W4_NONE) continue;
+        const bool cut = p.open(at[j]);
+        float4* from = cut ? p.part(p.c0) : reinterpret_cast<float4*>(a.rows_f32 + static_cast<size_t>(row * a.topk + j0 + j) * a.N + n);
+        *from = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (cut) p.template add<2>(p.c0 + 1, f[j]);
+        sum.x += w[j] * f[j].x;
+        sum.y += w[j] * f[j].y;
+        sum.z += w[j] * f[j].z;
+        sum.w += w[j] * f[j].w;
       }
     }
-    sum.x += w * v.x;
-    sum.y += w * v.y;
-    sum.z += w * v.z;
-    sum.w += w * v.w;
+  } else if (write) {
+    const W4Slot at = a.mode == W4_DENSE ? W4Slot{static_cast<uint16_t>(row / (MT * 8)), static_cast<uint16_t>(row % (MT * 8))}
+                                         : a.where[row];
+    if (at.tile != W4_NONE) {
+      write = p.open(at);  // else written already
+      if (write) p.template add<12>(p.c0, sum);
+    }
   }
   if (write)
     *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(row) * a.N + n) = make_uint2(pack2<DT>(sum.x, sum.y), pack2<DT>(sum.z, sum.w));
@@ -638,7 +671,8 @@ flux_status_t w4_launch(W4Args a, const DeviceInfo& dev, cudaStream_t s) {
   attr_pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr_pdl;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, w4_join_kernel<DT, MT>, a);
+  e = a.mode == W4_LAYER1 ? cudaLaunchKernelEx(&cfg, w4_join_kernel<DT, MT, true>, a)
+                          : cudaLaunchKernelEx(&cfg, w4_join_kernel<DT, MT, false>, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
