@@ -34,267 +34,590 @@ namespace flux {
 namespace {
 
 constexpr int RT_WARPS = 8, RT_THREADS = RT_WARPS * 32;
-constexpr int RT_ITEMS = 608;  // about this many partial sums of the forward pass
+constexpr int RT_ITEMS = 608;       // about this many CTAs: four per SM
+// the items of a sequence, and their sums, that its last CTA joins; more are joined
+// by a second kernel
+constexpr int RT_HERE_ITEMS = 64, RT_HERE_SUMS = 8192;
+constexpr int JOIN_COLS = 32, JOIN_WARPS = 16, JOIN_THREADS = JOIN_COLS * JOIN_WARPS;
 
-// How the forward pass cuts the tokens: `sub` items of `chunk` tokens per sequence.
-struct BalancePlan {
-  int sub, chunk, items;
-  size_t probs, counts, kept, z, total;
+// A token's scores are held by LPT lanes, four by four: V vectors of four a
+// lane.  Vectors of a row of 4 n experts are 16-byte loads of neighbours, other
+// rows are read one score at a time, neighbours in neighbouring lanes.
+template <int LPT, int V, bool VEC>
+struct Lanes {
+  static constexpr int TPW = 32 / LPT;             // tokens of a warp at a time
+  static constexpr int TPC = RT_WARPS * TPW;       // of a CTA
+  static __device__ __forceinline__ int expert(int l, int v, int i) {
+    return VEC ? (v * LPT + l) * 4 + i : (v * 4 + i) * LPT + l;
+  }
+  // f[v][i] = row[expert], `other` past E
+  static __device__ __forceinline__ void load(const float* row, int l, int E, float other, float (&f)[V][4]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if constexpr (VEC) {
+        const int e = expert(l, v, 0);
+        const float4 q = e < E ? __ldg(reinterpret_cast<const float4*>(row + e)) : make_float4(other, other, other, other);
+        f[v][0] = q.x, f[v][1] = q.y, f[v][2] = q.z, f[v][3] = q.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[v][i] = expert(l, v, i) < E ? __ldg(row + expert(l, v, i)) : other;
+      }
+    }
+  }
+  // sums over the LPT lanes of a token
+  static __device__ __forceinline__ float sum(float x) {
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    return x;
+  }
+  static __device__ __forceinline__ float max(float x) {
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+    return x;
+  }
 };
+
+// exp(x) for x <= 0, one multiplication and the hardware's 2^x (relative error
+// about 2^-22 + |x| 2^-24; results below 2^-126 are 0).
+__device__ __forceinline__ float exp_down(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+
+// How the forward pass cuts the tokens: `sub` items of `chunk` tokens per
+// sequence, one CTA each.
+struct BalancePlan {
+  int sub, chunk, items, cols;  // cols: column blocks of the joining kernel, 0 if there is none
+  size_t probs, counts, kept, z, bal, seq_z, arrived, total;
+};
+
+struct BalanceArgs {
+  const float* logits;
+  const int32_t* ids;
+  const uint8_t* mask;
+  float* loss;
+  int32_t* counts;
+  float* probs;
+  int32_t* tokens;
+  float* lse;
+  uint32_t* hdr;
+  // workspace: the items' sums, then one value per sequence (and column block)
+  float* part_probs;
+  int* part_counts;
+  int* part_kept;
+  float* part_z;
+  double* part_bal;
+  double* seq_z;
+  uint32_t* arrived;  // [S] items of a sequence, then [1] sequences (or blocks)
+  int E, topk, S, per, sub, chunk, cols;
+  float balance_coef, z_coef;
+};
+
+// Arrival of this CTA, its stores made visible first, at a counter that
+// `others` others arrive at too; true in the last one, which leaves the counter
+// zero and sees the others' stores.
+__device__ __forceinline__ bool last_to_arrive(uint32_t* counter, int others, int* flag) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const bool last = atomicAdd(counter, 1u) == static_cast<uint32_t>(others);
+    if (last) *counter = 0u;
+    *flag = last;
+    __threadfence();
+  }
+  __syncthreads();
+  return *flag != 0;
+}
+
+// Sum of one double per thread, in thread order of a fixed tree; in thread 0.
+template <int THREADS>
+__device__ __forceinline__ double cta_sum(double v, double* smem) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int w = 1; w < THREADS / 32; ++w) v += smem[w];
+  return v;
+}
+
+// The two losses and the count of all tokens from the n parts of the balance
+// loss and the sequences' z terms and counts; leaves the parts zero.
+template <int THREADS>
+__device__ __forceinline__ void write_losses(const BalanceArgs& a, int n, double* smem) {
+  double bal = 0.0, z = 0.0, all = 0.0;
+  for (int i = threadIdx.x; i < n; i += THREADS) {
+    bal += __ldcg(a.part_bal + i);
+    a.part_bal[i] = 0.0;
+  }
+  for (int s = threadIdx.x; s < a.S; s += THREADS) {
+    z += __ldcg(a.seq_z + s);
+    a.seq_z[s] = 0.0;
+    all += __ldcg(a.tokens + s);
+  }
+  bal = cta_sum<THREADS>(bal, smem);
+  z = cta_sum<THREADS>(z, smem);
+  all = cta_sum<THREADS>(all, smem);
+  if (threadIdx.x == 0) {
+    a.loss[0] = static_cast<float>(bal * a.balance_coef * a.E / (static_cast<double>(a.topk) * a.S));
+    a.loss[1] = static_cast<float>(z * a.z_coef / fmax(all, 1.0));
+    a.tokens[a.S] = static_cast<int>(all);
+  }
+}
+
+// Forward.  One read of the scores: a token's maximum, exponentials and their
+// sum stay in the registers of its lanes, which add its probabilities to their
+// own experts' sums.  An item's sums are joined over its warps in shared memory,
+// a sequence's over its items by the last of their CTAs to end, or, where they
+// are many, by balance_join_kernel; all in fixed orders.
+template <int LPT, int V, bool VEC>
+__global__ void __launch_bounds__(RT_THREADS)
+balance_kernel(const __grid_constant__ BalanceArgs a) {
+  using L = Lanes<LPT, V, VEC>;
+  constexpr int WIDE = LPT * V * 4;  // experts the lanes have room for
+  __shared__ float probs_w[RT_WARPS][WIDE];
+  __shared__ int cnt[WIDE];
+  __shared__ int kept_w[RT_WARPS];
+  __shared__ float z_w[RT_WARPS];
+  __shared__ double red[RT_WARPS];
+  __shared__ int flag;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT, tg = lane / LPT;
+  const int item = blockIdx.x, seq = item / a.sub, E = a.E;
+  const int t0 = seq * a.per + (item - seq * a.sub) * a.chunk, t1 = min(t0 + a.chunk, (seq + 1) * a.per);
+  if (a.cols > 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int e = threadIdx.x; e < WIDE; e += RT_THREADS) cnt[e] = 0;
+  __syncthreads();
+  float sums[V][4] = {};
+  float z = 0.0f;
+  int kept = 0;
+  bool bad = false;
+  for (int tw = t0 + warp * L::TPW; tw < t1; tw += L::TPC) {
+    const int t = tw + tg;
+    const bool here = t < t1;
+    const bool keep = here && (a.mask == nullptr || __ldg(a.mask + t) != 0);
+    const int32_t* id = a.ids + static_cast<size_t>(here ? t : t0) * a.topk;
+    const int first = l < a.topk ? __ldg(id + l) : 0;
+    float f[V][4];
+    L::load(a.logits + static_cast<size_t>(here ? t : t0) * E, l, E, -INFINITY, f);
+    float top = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, f[v][i]);  // a NaN gives way to the other operand
+    top = L::max(top);
+    float s = 0.0f;
+    if (!isinf(top)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[v][i] = exp_down((f[v][i] != f[v][i] ? -INFINITY : f[v][i]) - top);
+          s += f[v][i];
+        }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool in = L::expert(l, v, i) < E;
+          f[v][i] = in && ((f[v][i] != f[v][i] ? -INFINITY : f[v][i]) == top) ? 1.0f : 0.0f;
+          s += f[v][i];
+        }
+    }
+    s = L::sum(s);
+    const float lse = isinf(top) ? top : top + logf(s);
+    if (here && l == 0) a.lse[t] = lse;
+    const float share = keep ? 1.0f / s : 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sums[v][i] += f[v][i] * share;
+    if (keep) {
+      if (l == 0) {
+        ++kept;
+        if (!isinf(top)) z += lse * lse;
+      }
+      for (int j = l; j < a.topk; j += LPT) {
+        const int e = j == l ? first : id[j];
+        if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+        else bad = true;
+      }
+    }
+  }
+  // tokens side by side in a warp, then the warps
+#pragma unroll
+  for (int o = LPT; o < 32; o <<= 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sums[v][i] += __shfl_xor_sync(0xFFFFFFFFu, sums[v][i], o);
+  }
+  z = warp_sum(z);
+  kept = __reduce_add_sync(0xFFFFFFFFu, kept);
+  if (lane < LPT) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) probs_w[warp][L::expert(l, v, i)] = sums[v][i];
+  }
+  if (lane == 0) {
+    kept_w[warp] = kept;
+    z_w[warp] = z;
+  }
+  if (bad) atomicCAS(a.hdr, 0u, static_cast<uint32_t>(FLUX_ERR_INVALID_ARG));
+  __syncthreads();
+  int n = 0;
+  float z_item = 0.0f;
+#pragma unroll
+  for (int w = 0; w < RT_WARPS; ++w) {
+    n += kept_w[w];
+    z_item += z_w[w];
+  }
+  auto expert_sum = [&](int e) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < RT_WARPS; ++w) s += probs_w[w][e];
+    return s;
+  };
+  double bal = 0.0;
+  auto write = [&](int e, float p, int c, int n_seq) {
+    const float m = static_cast<float>(max(n_seq, 1));
+    p /= m;
+    a.probs[static_cast<size_t>(seq) * E + e] = p;
+    a.counts[static_cast<size_t>(seq) * E + e] = c;
+    bal += static_cast<double>(c) / m * p;
+  };
+  if (a.sub == 1) {
+    for (int e = threadIdx.x; e < E; e += RT_THREADS) write(e, expert_sum(e), cnt[e], n);
+    if (threadIdx.x == 0) {
+      a.tokens[seq] = n;
+      a.seq_z[seq] = z_item;
+    }
+  } else {
+    for (int e = threadIdx.x; e < E; e += RT_THREADS) {
+      a.part_probs[static_cast<size_t>(item) * E + e] = expert_sum(e);
+      a.part_counts[static_cast<size_t>(item) * E + e] = cnt[e];
+    }
+    if (threadIdx.x == 0) {
+      a.part_kept[item] = n;
+      a.part_z[item] = z_item;
+    }
+    if (a.cols > 0) return;  // balance_join_kernel goes on
+    if (!last_to_arrive(a.arrived + seq, a.sub - 1, &flag)) return;
+    const int i0 = seq * a.sub;
+    int n_seq = 0;
+    double z_seq = 0.0;
+    if (warp == 0) {
+      for (int i = lane; i < a.sub; i += 32) {
+        n_seq += __ldcg(a.part_kept + i0 + i);
+        z_seq += __ldcg(a.part_z + i0 + i);
+        a.part_kept[i0 + i] = 0;
+        a.part_z[i0 + i] = 0.0f;
+      }
+      n_seq = __reduce_add_sync(0xFFFFFFFFu, n_seq);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) z_seq += __shfl_xor_sync(0xFFFFFFFFu, z_seq, o);
+      if (lane == 0) {
+        kept_w[0] = n_seq;
+        a.tokens[seq] = n_seq;
+        a.seq_z[seq] = z_seq;
+      }
+    }
+    __syncthreads();
+    n_seq = kept_w[0];
+    // an expert per warp, its items over the lanes, four experts in flight
+    constexpr int BATCH = 4;
+    for (int e0 = warp; e0 < E; e0 += RT_WARPS * BATCH) {
+      float p[BATCH] = {};
+      int c[BATCH] = {};
+      for (int i = lane; i < a.sub; i += 32) {
+        const size_t row = static_cast<size_t>(i0 + i) * E;
+        float fp[BATCH];
+        int fc[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+          const int e = e0 + b * RT_WARPS;
+          fp[b] = e < E ? __ldcg(a.part_probs + row + e) : 0.0f;
+          fc[b] = e < E ? __ldcg(a.part_counts + row + e) : 0;
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+          const int e = e0 + b * RT_WARPS;
+          if (e < E) {
+            a.part_probs[row + e] = 0.0f;
+            a.part_counts[row + e] = 0;
+          }
+          p[b] += fp[b];
+          c[b] += fc[b];
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        const int e = e0 + b * RT_WARPS;
+        p[b] = warp_sum(p[b]);
+        c[b] = __reduce_add_sync(0xFFFFFFFFu, c[b]);
+        if (lane == 0 && e < E) write(e, p[b], c[b], n_seq);
+      }
+    }
+  }
+  bal = cta_sum<RT_THREADS>(bal, red);
+  if (threadIdx.x == 0) a.part_bal[seq] = bal;
+  if (!last_to_arrive(a.arrived + a.S, a.S - 1, &flag)) return;
+  write_losses<RT_THREADS>(a, a.S, red);
+}
+
+// Joins the items' sums of 32 experts of one sequence.
+__global__ void __launch_bounds__(JOIN_THREADS) balance_join_kernel(const __grid_constant__ BalanceArgs a) {
+  __shared__ float probs_w[JOIN_WARPS][JOIN_COLS];
+  __shared__ int cnt_w[JOIN_WARPS][JOIN_COLS];
+  __shared__ double red[JOIN_WARPS];
+  __shared__ int kept, flag;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int seq = blockIdx.y, i0 = seq * a.sub, e = blockIdx.x * JOIN_COLS + lane;
+  if (warp == 0) {  // every block of the sequence needs its count
+    int n = 0;
+    double z = 0.0;
+    for (int i = lane; i < a.sub; i += 32) {
+      n += a.part_kept[i0 + i];
+      z += a.part_z[i0 + i];
+    }
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+    if (lane == 0) {
+      kept = n;
+      if (blockIdx.x == 0) {
+        a.tokens[seq] = n;
+        a.seq_z[seq] = z;
+      }
+    }
+  }
+  constexpr int BATCH = 8;
+  float p = 0.0f;
+  int c = 0;
+  if (e < a.E) {
+    for (int i1 = warp; i1 < a.sub; i1 += JOIN_WARPS * BATCH) {
+      float fp[BATCH];
+      int fc[BATCH];
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        const int i = i1 + b * JOIN_WARPS;
+        const size_t at = static_cast<size_t>(i0 + i) * a.E + e;
+        fp[b] = i < a.sub ? a.part_probs[at] : 0.0f;
+        fc[b] = i < a.sub ? a.part_counts[at] : 0;
+      }
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        const int i = i1 + b * JOIN_WARPS;
+        const size_t at = static_cast<size_t>(i0 + i) * a.E + e;
+        if (i < a.sub) {
+          a.part_probs[at] = 0.0f;
+          a.part_counts[at] = 0;
+        }
+        p += fp[b];
+        c += fc[b];
+      }
+    }
+  }
+  probs_w[warp][lane] = p;
+  cnt_w[warp][lane] = c;
+  __syncthreads();
+  double bal = 0.0;
+  if (warp == 0 && e < a.E) {
+    for (int w = 1; w < JOIN_WARPS; ++w) {
+      p += probs_w[w][lane];
+      c += cnt_w[w][lane];
+    }
+    const float n = static_cast<float>(max(kept, 1));
+    p /= n;
+    a.probs[static_cast<size_t>(seq) * a.E + e] = p;
+    a.counts[static_cast<size_t>(seq) * a.E + e] = c;
+    bal = static_cast<double>(c) / n * p;
+  }
+  bal = cta_sum<JOIN_THREADS>(bal, red);
+  if (threadIdx.x == 0) a.part_bal[seq * gridDim.x + blockIdx.x] = bal;
+  if (!last_to_arrive(a.arrived + a.S, gridDim.x * gridDim.y - 1, &flag)) return;
+  for (int i = threadIdx.x; i < a.S * a.sub; i += JOIN_THREADS) {
+    a.part_kept[i] = 0;
+    a.part_z[i] = 0.0f;
+  }
+  write_losses<JOIN_THREADS>(a, gridDim.x * gridDim.y, red);
+}
+
+struct RouterBwdArgs {
+  const float* logits;
+  const int32_t* ids;
+  const float* weights;
+  const uint8_t* mask;
+  const float* lse;
+  const int32_t* counts;
+  const int32_t* tokens;
+  const float* dloss;
+  const float* dweights;
+  float* dlogits;
+  int E, topk, S, per, sub, chunk;
+  float balance_coef, z_coef;
+};
+
+// Backward: one read of the scores, one write of their gradient.  A CTA stays in
+// one sequence, whose counts its lanes hold; the gate's terms of a token meet
+// the others through a row of shared memory.
+template <int LPT, int V, bool VEC>
+__global__ void __launch_bounds__(RT_THREADS)
+router_bwd_kernel(const __grid_constant__ RouterBwdArgs a) {
+  using L = Lanes<LPT, V, VEC>;
+  constexpr int WIDE = LPT * V * 4;
+  __shared__ alignas(16) float gate[RT_WARPS * L::TPW][WIDE];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT, tg = lane / LPT;
+  const int item = blockIdx.x, seq = item / a.sub, E = a.E;
+  const int t0 = seq * a.per + (item - seq * a.sub) * a.chunk, t1 = min(t0 + a.chunk, (seq + 1) * a.per);
+  float* g = gate[warp * L::TPW + tg];
+  const bool gates = a.dweights != nullptr;
+  if (gates)
+    for (int e = l; e < WIDE; e += LPT) g[e] = 0.0f;
+  const float db = a.dloss != nullptr ? __ldg(a.dloss) : 1.0f, dz = a.dloss != nullptr ? __ldg(a.dloss + 1) : 1.0f;
+  const float n = static_cast<float>(max(__ldg(a.tokens + seq), 1)), all = static_cast<float>(max(__ldg(a.tokens + a.S), 1));
+  const float scale = db * (a.balance_coef * E / (static_cast<float>(a.topk) * a.S)) / (n * n);
+  const float z_scale = dz * (2.0f * a.z_coef) / all;
+  float A[V][4];
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = L::expert(l, v, i);
+      A[v][i] = e < E ? scale * static_cast<float>(__ldg(a.counts + static_cast<size_t>(seq) * E + e)) : 0.0f;
+    }
+  __syncwarp();
+  for (int tw = t0 + warp * L::TPW; tw < t1; tw += L::TPC) {
+    const int t = tw + tg;
+    const bool here = t < t1;
+    const size_t row = static_cast<size_t>(here ? t : t0);
+    const bool keep = here && (a.mask == nullptr || __ldg(a.mask + t) != 0);
+    const float lse = __ldg(a.lse + row);
+    const bool flat = isinf(lse) || lse != lse;
+    float w = 0.0f, dw = 0.0f;
+    int id = -1;
+    if (gates && l < a.topk) {
+      w = __ldg(a.weights + row * a.topk + l);
+      dw = __ldg(a.dweights + row * a.topk + l);
+      id = __ldg(a.ids + row * a.topk + l);
+    }
+    float f[V][4];
+    if (keep) {
+      L::load(a.logits + row * E, l, E, -INFINITY, f);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[v][i] = -INFINITY;
+    }
+    float mean = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[v][i] = flat || f[v][i] != f[v][i] ? 0.0f : exp_down(f[v][i] - lse);
+        mean += f[v][i] * A[v][i];
+      }
+    mean = L::sum(mean);
+    const float shift = (flat ? 0.0f : z_scale * lse) - mean;
+    if (gates) {
+      float dot = w * dw;
+      for (int j = l + LPT; j < a.topk; j += LPT) dot += __ldg(a.weights + row * a.topk + j) * __ldg(a.dweights + row * a.topk + j);
+      dot = L::sum(dot);
+      if (here && !flat) {
+        for (int j = l; j < a.topk; j += LPT) {
+          if (j != l) {
+            w = __ldg(a.weights + row * a.topk + j);
+            dw = __ldg(a.dweights + row * a.topk + j);
+            id = __ldg(a.ids + row * a.topk + j);
+          }
+          if (id >= 0 && id < E) g[id] = w * (dw - dot);
+        }
+      }
+      __syncwarp();
+    }
+    float* out = a.dlogits + row * E;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float d[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = f[v][i] * (A[v][i] + shift);
+      if constexpr (VEC) {
+        const int e = L::expert(l, v, 0);
+        if (gates) {
+          float4* at = reinterpret_cast<float4*>(g + e);
+          const float4 q = *at;
+          *at = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          d[0] += q.x, d[1] += q.y, d[2] += q.z, d[3] += q.w;
+        }
+        if (here && e < E) *reinterpret_cast<float4*>(out + e) = make_float4(d[0], d[1], d[2], d[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = L::expert(l, v, i);
+          if (gates) {
+            d[i] += g[e];
+            g[e] = 0.0f;
+          }
+          if (here && e < E) out[e] = d[i];
+        }
+      }
+    }
+    if (gates) __syncwarp();
+  }
+}
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// Calls f(LPT, V, VEC) for the lanes that hold a row of E scores.
+template <typename F>
+auto by_experts(int E, F&& f) {
+  auto vec = [&](auto lpt, auto v) { return E % 4 == 0 ? f(lpt, v, std::true_type{}) : f(lpt, v, std::false_type{}); };
+  if (E <= 4) return vec(Int<1>{}, Int<1>{});
+  if (E <= 8) return vec(Int<2>{}, Int<1>{});
+  if (E <= 16) return vec(Int<4>{}, Int<1>{});
+  if (E <= 32) return vec(Int<8>{}, Int<1>{});
+  if (E <= 64) return vec(Int<16>{}, Int<1>{});
+  if (E <= 128) return vec(Int<32>{}, Int<1>{});
+  if (E <= 256) return vec(Int<32>{}, Int<2>{});
+  if (E <= 512) return vec(Int<32>{}, Int<4>{});
+  return vec(Int<32>{}, Int<8>{});
+}
+
+// Items of a sequence: about RT_ITEMS CTAs in all, each with work for its warps.
+void cut_tokens(int E, int per, int S, int* sub, int* chunk) {
+  const int tokens = by_experts(E, [](auto lpt, auto, auto) { return RT_WARPS * 32 / decltype(lpt)::value; });
+  *sub = std::max(1, std::min((RT_ITEMS + S - 1) / S, (per + tokens - 1) / tokens));
+  *chunk = (per + *sub - 1) / *sub;
+  *sub = (per + *chunk - 1) / *chunk;
+}
 
 BalancePlan balance_plan(int T, int E, int S) {
   BalancePlan p{};
-  const int per = T / S;
-  p.sub = std::max(1, std::min((RT_ITEMS + S - 1) / S, (per + RT_WARPS - 1) / RT_WARPS));
-  p.chunk = std::max(1, (per + p.sub - 1) / p.sub);
-  p.sub = std::max(1, (per + p.chunk - 1) / p.chunk);
+  cut_tokens(E, T / S, S, &p.sub, &p.chunk);
   p.items = p.sub * S;
+  p.cols = p.sub > RT_HERE_ITEMS || (p.sub > 1 && static_cast<long long>(p.sub) * E > RT_HERE_SUMS) ? (E + JOIN_COLS - 1) / JOIN_COLS : 0;
   size_t at = WS_HEADER;
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at += round_up(bytes, WS_ALIGN);
     return here;
   };
-  p.probs = take(sizeof(float) * p.items * static_cast<size_t>(E));
-  p.counts = take(sizeof(int) * p.items * static_cast<size_t>(E));
-  p.kept = take(sizeof(int) * p.items);
-  p.z = take(sizeof(float) * p.items);
+  const size_t parts = p.sub > 1 ? static_cast<size_t>(p.items) : 0;
+  p.probs = take(sizeof(float) * parts * E);
+  p.counts = take(sizeof(int) * parts * E);
+  p.kept = take(sizeof(int) * parts);
+  p.z = take(sizeof(float) * parts);
+  p.bal = take(sizeof(double) * S * static_cast<size_t>(std::max(1, p.cols)));
+  p.seq_z = take(sizeof(double) * S);
+  p.arrived = take(sizeof(uint32_t) * (static_cast<size_t>(S) + 1));
   p.total = at;
   return p;
-}
-
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
-}
-
-// One item per CTA, one token per warp at a time; lane i holds the experts
-// i, i + 32, ... and the sums of their probabilities.
-template <int N>
-__global__ void __launch_bounds__(RT_THREADS)
-balance_kernel(int T, int E, int topk, int per, int sub, int chunk, const float* __restrict__ logits,
-               const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask, float* __restrict__ lse,
-               float* part_probs, int* part_counts, int* part_kept, float* part_z, uint32_t* hdr) {
-  extern __shared__ float sm[];  // E counts, then RT_WARPS x E probability sums
-  int* cnt = reinterpret_cast<int*>(sm);
-  float* probs = sm + E;
-  __shared__ int kept_w[RT_WARPS];
-  __shared__ float z_w[RT_WARPS];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int item = blockIdx.x, seq = item / sub;
-  const int t0 = seq * per + (item - seq * sub) * chunk, t1 = min(t0 + chunk, (seq + 1) * per);
-  for (int e = threadIdx.x; e < E; e += RT_THREADS) cnt[e] = 0;
-  __syncthreads();
-  float sum[N] = {};
-  float z = 0.0f;
-  int kept = 0;
-  bool bad = false;
-  for (int t = t0 + warp; t < t1; t += RT_WARPS) {
-    const float* row = logits + static_cast<size_t>(t) * E;
-    float v[N];
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = lane + 32 * i;
-      v[i] = e < E ? __ldg(row + e) : -INFINITY;
-      if (v[i] != v[i]) v[i] = -INFINITY;
-      top = fmaxf(top, v[i]);
-    }
-    top = warp_max(top);
-    const bool inf_top = isinf(top);
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = lane + 32 * i;
-      v[i] = e >= E ? 0.0f : inf_top ? (v[i] == top ? 1.0f : 0.0f) : expf(v[i] - top);
-      s += v[i];
-    }
-    s = warp_sum(s);
-    const float l = inf_top ? top : top + logf(s);
-    if (lane == 0) lse[t] = l;
-    if (mask == nullptr || mask[t] != 0) {
-      const float inv = 1.0f / s;
-#pragma unroll
-      for (int i = 0; i < N; ++i) sum[i] += v[i] * inv;
-      ++kept;
-      if (!inf_top) z += l * l;
-      for (int j = lane; j < topk; j += 32) {
-        const int e = ids[static_cast<size_t>(t) * topk + j];
-        if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
-        else bad = true;
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = lane + 32 * i;
-    if (e < E) probs[warp * E + e] = sum[i];
-  }
-  if (lane == 0) {
-    kept_w[warp] = kept;
-    z_w[warp] = z;
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += RT_THREADS) {
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < RT_WARPS; ++w) s += probs[w * E + e];
-    part_probs[static_cast<size_t>(item) * E + e] = s;
-    part_counts[static_cast<size_t>(item) * E + e] = cnt[e];
-  }
-  if (threadIdx.x == 0) {
-    int k = 0;
-    float s = 0.0f;
-    for (int w = 0; w < RT_WARPS; ++w) {
-      k += kept_w[w];
-      s += z_w[w];
-    }
-    part_kept[item] = k;
-    part_z[item] = s;
-  }
-  if (bad) atomicCAS(hdr, 0u, static_cast<uint32_t>(FLUX_ERR_INVALID_ARG));
-}
-
-// One CTA joins the items of each sequence in order, then the sequences, and
-// leaves the partial sums zero.
-__global__ void __launch_bounds__(1024)
-balance_sums_kernel(int E, int topk, int S, int sub, float balance_coef, float z_coef, float* part_probs,
-                    int* part_counts, int* part_kept, float* part_z, float* loss, int32_t* counts, float* probs,
-                    int32_t* tokens) {
-  __shared__ double warp_part[32];
-  __shared__ int kept;
-  double bal = 0.0;  // thread 0 .. E - 1: their expert's terms
-  int all = 0;
-  double z = 0.0;
-  for (int s = 0; s < S; ++s) {
-    if (threadIdx.x == 0) {
-      int k = 0;
-      for (int i = s * sub; i < (s + 1) * sub; ++i) {
-        k += part_kept[i];
-        z += part_z[i];
-        part_kept[i] = 0;
-        part_z[i] = 0.0f;
-      }
-      kept = k;
-      all += k;
-      tokens[s] = k;
-    }
-    __syncthreads();
-    const int e = threadIdx.x;
-    if (e < E) {
-      float p = 0.0f;
-      int c = 0;
-      for (int i = s * sub; i < (s + 1) * sub; ++i) {
-        const size_t at = static_cast<size_t>(i) * E + e;
-        p += part_probs[at];
-        c += part_counts[at];
-        part_probs[at] = 0.0f;
-        part_counts[at] = 0;
-      }
-      const float n = static_cast<float>(max(kept, 1));
-      p /= n;
-      probs[static_cast<size_t>(s) * E + e] = p;
-      counts[static_cast<size_t>(s) * E + e] = c;
-      bal += static_cast<double>(c) / n * p;
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) bal += __shfl_xor_sync(0xFFFFFFFFu, bal, o);
-  if ((threadIdx.x & 31) == 0) warp_part[threadIdx.x >> 5] = bal;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double b = 0.0;
-    for (int w = 0; w < 32; ++w) b += warp_part[w];
-    loss[0] = static_cast<float>(b * balance_coef * E / (static_cast<double>(topk) * S));
-    loss[1] = static_cast<float>(z * z_coef / max(all, 1));
-    tokens[S] = all;
-  }
-}
-
-// One token per warp: the loss terms first, then the gate's.
-template <int N>
-__global__ void __launch_bounds__(RT_THREADS)
-router_bwd_kernel(int T, int E, int topk, int S, int per, float balance_coef, float z_coef,
-                  const float* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ weights,
-                  const uint8_t* __restrict__ mask, const float* __restrict__ lse, const int32_t* __restrict__ counts,
-                  const int32_t* __restrict__ tokens, const float* __restrict__ dloss,
-                  const float* __restrict__ dweights, float* __restrict__ dlogits) {
-  extern __shared__ float sm[];  // RT_WARPS x E: the gate's terms of the warp's token
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* gate = sm + warp * E;
-  const float db = dloss != nullptr ? dloss[0] : 1.0f, dz = dloss != nullptr ? dloss[1] : 1.0f;
-  const float nall = static_cast<float>(max(tokens[S], 1));
-  if (dweights != nullptr) {
-    for (int e = lane; e < E; e += 32) gate[e] = 0.0f;
-    __syncwarp();
-  }
-  for (long long t = static_cast<long long>(blockIdx.x) * RT_WARPS + warp; t < T;
-       t += static_cast<long long>(gridDim.x) * RT_WARPS) {
-    const int seq = static_cast<int>(t) / per;
-    const float* row = logits + static_cast<size_t>(t) * E;
-    const float l = lse[t];
-    const bool flat = isinf(l) || l != l;
-    const bool keep = !flat && (mask == nullptr || mask[t] != 0);
-    float p[N], a[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = a[i] = 0.0f;
-    float mean = 0.0f, zt = 0.0f;
-    if (keep) {
-      const float n = static_cast<float>(max(tokens[seq], 1));
-      const float scale = db * (balance_coef * E / (static_cast<float>(topk) * S)) / (n * n);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int e = lane + 32 * i;
-        if (e < E) {
-          const float v = __ldg(row + e);
-          p[i] = v != v ? 0.0f : expf(v - l);
-          a[i] = scale * static_cast<float>(counts[static_cast<size_t>(seq) * E + e]);
-          mean += p[i] * a[i];
-        }
-      }
-      mean = warp_sum(mean);
-      zt = dz * (2.0f * z_coef) * l / nall;
-    }
-    if (dweights != nullptr && !flat) {
-      const float* w = weights + static_cast<size_t>(t) * topk;
-      const float* dw = dweights + static_cast<size_t>(t) * topk;
-      const int32_t* id = ids + static_cast<size_t>(t) * topk;
-      float dot = 0.0f;
-      for (int j = lane; j < topk; j += 32) dot += w[j] * dw[j];
-      dot = warp_sum(dot);
-      for (int j = lane; j < topk; j += 32) {
-        const int e = id[j];
-        if (e >= 0 && e < E) gate[e] = w[j] * (dw[j] - dot);
-      }
-      __syncwarp();
-    }
-    float* out = dlogits + static_cast<size_t>(t) * E;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E) {
-        float d = p[i] * (a[i] - mean + zt);
-        if (dweights != nullptr) {
-          d += gate[e];
-          gate[e] = 0.0f;
-        }
-        out[e] = d;
-      }
-    }
-    __syncwarp();
-  }
-}
-
-template <typename F>
-flux_status_t by_experts(int E, F&& f) {
-  if (E <= 32) return f(std::integral_constant<int, 1>{});
-  if (E <= 64) return f(std::integral_constant<int, 2>{});
-  if (E <= 128) return f(std::integral_constant<int, 4>{});
-  if (E <= 256) return f(std::integral_constant<int, 8>{});
-  if (E <= 512) return f(std::integral_constant<int, 16>{});
-  return f(std::integral_constant<int, 32>{});
 }
 
 bool router_sizes_ok(int T, int E, int topk, int seqs) {
@@ -340,22 +663,47 @@ extern "C" flux_status_t flux_moe_balance_loss(int T, int E, int topk, int seqs,
   DeviceInfo dev;
   if ((st = current_device(&dev)) != FLUX_OK) return st;
   char* ws = static_cast<char*>(workspace);
-  float* part_probs = reinterpret_cast<float*>(ws + p.probs);
-  int* part_counts = reinterpret_cast<int*>(ws + p.counts);
-  int* part_kept = reinterpret_cast<int*>(ws + p.kept);
-  float* part_z = reinterpret_cast<float*>(ws + p.z);
-  st = by_experts(E, [&](auto n) {
-    const size_t smem = sizeof(float) * E * (1 + RT_WARPS);
-    balance_kernel<decltype(n)::value><<<p.items, RT_THREADS, smem, s>>>(
-        T, E, topk, T / seqs, p.sub, p.chunk, logits, topk_ids, token_mask, lse, part_probs, part_counts, part_kept,
-        part_z, static_cast<uint32_t*>(workspace));
-    const cudaError_t le = cudaGetLastError();
-    return le == cudaSuccess ? FLUX_OK : cuda_fail(le);
+  BalanceArgs a{};
+  a.logits = logits;
+  a.ids = topk_ids;
+  a.mask = token_mask;
+  a.loss = loss;
+  a.counts = counts;
+  a.probs = probs;
+  a.tokens = tokens;
+  a.lse = lse;
+  a.hdr = static_cast<uint32_t*>(workspace);
+  a.part_probs = reinterpret_cast<float*>(ws + p.probs);
+  a.part_counts = reinterpret_cast<int*>(ws + p.counts);
+  a.part_kept = reinterpret_cast<int*>(ws + p.kept);
+  a.part_z = reinterpret_cast<float*>(ws + p.z);
+  a.part_bal = reinterpret_cast<double*>(ws + p.bal);
+  a.seq_z = reinterpret_cast<double*>(ws + p.seq_z);
+  a.arrived = reinterpret_cast<uint32_t*>(ws + p.arrived);
+  a.E = E;
+  a.topk = topk;
+  a.S = seqs;
+  a.per = T / seqs;
+  a.sub = p.sub;
+  a.chunk = p.chunk;
+  a.cols = p.cols;
+  a.balance_coef = balance_coef;
+  a.z_coef = z_coef;
+  by_experts(E, [&](auto lpt, auto v, auto vec) {
+    balance_kernel<decltype(lpt)::value, decltype(v)::value, decltype(vec)::value><<<p.items, RT_THREADS, 0, s>>>(a);
   });
-  if (st != FLUX_OK) return st;
-  balance_sums_kernel<<<1, 1024, 0, s>>>(E, topk, seqs, p.sub, balance_coef, z_coef, part_probs, part_counts,
-                                         part_kept, part_z, loss, counts, probs, tokens);
-  e = cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
+  if (p.cols == 0) return FLUX_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.cols, seqs, 1);
+  cfg.blockDim = dim3(JOIN_THREADS, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, balance_join_kernel, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
@@ -377,12 +725,27 @@ extern "C" flux_status_t flux_moe_router_bwd(int T, int E, int topk, int seqs, f
   flux_status_t st = current_device(&dev);
   if (st != FLUX_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return by_experts(E, [&](auto n) {
-    const int grid = std::min((T + RT_WARPS - 1) / RT_WARPS, dev.sm_count * 8);
-    router_bwd_kernel<decltype(n)::value><<<grid, RT_THREADS, sizeof(float) * E * RT_WARPS, s>>>(
-        T, E, topk, seqs, T / seqs, balance_coef, z_coef, logits, topk_ids, topk_weights, token_mask, lse, counts,
-        tokens, dloss, dweights, dlogits);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
+  RouterBwdArgs a{};
+  a.logits = logits;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.mask = token_mask;
+  a.lse = lse;
+  a.counts = counts;
+  a.tokens = tokens;
+  a.dloss = dloss;
+  a.dweights = dweights;
+  a.dlogits = dlogits;
+  a.E = E;
+  a.topk = topk;
+  a.S = seqs;
+  a.per = T / seqs;
+  cut_tokens(E, a.per, seqs, &a.sub, &a.chunk);
+  a.balance_coef = balance_coef;
+  a.z_coef = z_coef;
+  by_experts(E, [&](auto lpt, auto v, auto vec) {
+    router_bwd_kernel<decltype(lpt)::value, decltype(v)::value, decltype(vec)::value><<<a.sub * seqs, RT_THREADS, 0, s>>>(a);
   });
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
