@@ -37,7 +37,7 @@ constexpr int RT_WARPS = 8, RT_THREADS = RT_WARPS * 32;
 constexpr int RT_ITEMS = 608;       // about this many CTAs: four per SM
 // the items of a sequence, and their sums, that its last CTA joins; more are joined
 // by a second kernel
-constexpr int RT_HERE_ITEMS = 64, RT_HERE_SUMS = 8192;
+constexpr int RT_HERE_ITEMS = 64, RT_HERE_SUMS = 2048;
 constexpr int JOIN_COLS = 32, JOIN_WARPS = 16, JOIN_THREADS = JOIN_COLS * JOIN_WARPS;
 
 // A token's scores are held by LPT lanes, four by four: V vectors of four a
@@ -77,11 +77,23 @@ struct Lanes {
   }
 };
 
-// exp(x) for x <= 0, one multiplication and the hardware's 2^x (relative error
-// about 2^-22 + |x| 2^-24; results below 2^-126 are 0).
-__device__ __forceinline__ float exp_down(float x) {
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+// The hardware's 2^x, log2 x and 1 / x (relative error about 2^-22; results below
+// 2^-126 are 0).
+__device__ __forceinline__ float exp2_fast(float x) {
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float inverse_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -107,11 +119,11 @@ struct BalanceArgs {
   int* part_counts;
   int* part_kept;
   float* part_z;
-  double* part_bal;
-  double* seq_z;
+  float* part_bal;
+  float* seq_z;
   uint32_t* arrived;  // [S] items of a sequence, then [1] sequences (or blocks)
   int E, topk, S, per, sub, chunk, cols;
-  float balance_coef, z_coef;
+  float balance_scale, z_coef;
 };
 
 // Arrival of this CTA, its stores made visible first, at a counter that
@@ -130,41 +142,52 @@ __device__ __forceinline__ bool last_to_arrive(uint32_t* counter, int others, in
   return *flag != 0;
 }
 
-// Sum of one double per thread, in thread order of a fixed tree; in thread 0.
+// Sums of two floats and an integer over the CTA, in a fixed order; in thread 0.
 template <int THREADS>
-__device__ __forceinline__ double cta_sum(double v, double* smem) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+__device__ __forceinline__ void cta_sums(float& x, float& y, int& n, float* smem) {
+  x = warp_sum(x);
+  y = warp_sum(y);
+  n = __reduce_add_sync(0xFFFFFFFFu, n);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) {
+    float* at = smem + (threadIdx.x >> 5) * 3;
+    at[0] = x;
+    at[1] = y;
+    at[2] = __int_as_float(n);
+  }
   __syncthreads();
-  if (threadIdx.x == 0)
-    for (int w = 1; w < THREADS / 32; ++w) v += smem[w];
-  return v;
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < THREADS / 32; ++w) {
+      x += smem[w * 3];
+      y += smem[w * 3 + 1];
+      n += __float_as_int(smem[w * 3 + 2]);
+    }
+  }
 }
 
-// The two losses and the count of all tokens from the n parts of the balance
-// loss and the sequences' z terms and counts; leaves the parts zero.
+__device__ __forceinline__ void write_losses(const BalanceArgs& a, float bal, float z, int all) {
+  a.loss[0] = bal * a.balance_scale;
+  a.loss[1] = z * a.z_coef / static_cast<float>(max(all, 1));
+  a.tokens[a.S] = all;
+}
+
+// The losses from the n parts of the balance loss and the sequences' z terms and
+// counts, once all are there; leaves the parts zero.
 template <int THREADS>
-__device__ __forceinline__ void write_losses(const BalanceArgs& a, int n, double* smem) {
-  double bal = 0.0, z = 0.0, all = 0.0;
+__device__ __forceinline__ void join_losses(const BalanceArgs& a, int n, float* smem) {
+  float bal = 0.0f, z = 0.0f;
+  int all = 0;
   for (int i = threadIdx.x; i < n; i += THREADS) {
     bal += __ldcg(a.part_bal + i);
-    a.part_bal[i] = 0.0;
+    a.part_bal[i] = 0.0f;
   }
   for (int s = threadIdx.x; s < a.S; s += THREADS) {
     z += __ldcg(a.seq_z + s);
-    a.seq_z[s] = 0.0;
+    a.seq_z[s] = 0.0f;
     all += __ldcg(a.tokens + s);
   }
-  bal = cta_sum<THREADS>(bal, smem);
-  z = cta_sum<THREADS>(z, smem);
-  all = cta_sum<THREADS>(all, smem);
-  if (threadIdx.x == 0) {
-    a.loss[0] = static_cast<float>(bal * a.balance_coef * a.E / (static_cast<double>(a.topk) * a.S));
-    a.loss[1] = static_cast<float>(z * a.z_coef / fmax(all, 1.0));
-    a.tokens[a.S] = static_cast<int>(all);
-  }
+  cta_sums<THREADS>(bal, z, all, smem);
+  if (threadIdx.x == 0) write_losses(a, bal, z, all);
 }
 
 // Forward.  One read of the scores: a token's maximum, exponentials and their
@@ -181,7 +204,7 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
   __shared__ int cnt[WIDE];
   __shared__ int kept_w[RT_WARPS];
   __shared__ float z_w[RT_WARPS];
-  __shared__ double red[RT_WARPS];
+  __shared__ float red[RT_WARPS * 3];
   __shared__ int flag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT, tg = lane / LPT;
   const int item = blockIdx.x, seq = item / a.sub, E = a.E;
@@ -193,19 +216,30 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
   float z = 0.0f;
   int kept = 0;
   bool bad = false;
+  // the next tokens' scores, mask and first expert are on their way while these
+  // are at work
+  float next[V][4];
+  int next_id = 0, next_mask = 1;
+  auto fetch = [&](int t) {
+    const size_t at = static_cast<size_t>(t < t1 ? t : t0);
+    L::load(a.logits + at * E, l, E, -INFINITY, next);
+    if (l < a.topk) next_id = __ldg(a.ids + at * a.topk + l);
+    if (a.mask != nullptr) next_mask = __ldg(a.mask + at);
+  };
+  if (t0 + warp * L::TPW < t1) fetch(t0 + warp * L::TPW + tg);
   for (int tw = t0 + warp * L::TPW; tw < t1; tw += L::TPC) {
-    const int t = tw + tg;
-    const bool here = t < t1;
-    const bool keep = here && (a.mask == nullptr || __ldg(a.mask + t) != 0);
-    const int32_t* id = a.ids + static_cast<size_t>(here ? t : t0) * a.topk;
-    const int first = l < a.topk ? __ldg(id + l) : 0;
+    const int t = tw + tg, first = next_id;
+    const bool here = t < t1, keep = here && next_mask != 0;
     float f[V][4];
-    L::load(a.logits + static_cast<size_t>(here ? t : t0) * E, l, E, -INFINITY, f);
     float top = -INFINITY;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, f[v][i]);  // a NaN gives way to the other operand
+      for (int i = 0; i < 4; ++i) {
+        f[v][i] = fmaxf(next[v][i], -INFINITY);  // a NaN gives way to the other operand
+        top = fmaxf(top, f[v][i]);
+      }
+    if (tw + L::TPC < t1) fetch(t + L::TPC);
     top = L::max(top);
     float s = 0.0f;
     if (!isinf(top)) {
@@ -213,7 +247,7 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          f[v][i] = exp_down((f[v][i] != f[v][i] ? -INFINITY : f[v][i]) - top);
+          f[v][i] = exp2_fast((f[v][i] - top) * LOG2E);
           s += f[v][i];
         }
     } else {
@@ -221,15 +255,14 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool in = L::expert(l, v, i) < E;
-          f[v][i] = in && ((f[v][i] != f[v][i] ? -INFINITY : f[v][i]) == top) ? 1.0f : 0.0f;
+          f[v][i] = L::expert(l, v, i) < E && f[v][i] == top ? 1.0f : 0.0f;
           s += f[v][i];
         }
     }
     s = L::sum(s);
-    const float lse = isinf(top) ? top : top + logf(s);
+    const float lse = isinf(top) ? top : top + log2_fast(s) * LN2;
     if (here && l == 0) a.lse[t] = lse;
-    const float share = keep ? 1.0f / s : 0.0f;
+    const float share = keep ? inverse_fast(s) : 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -240,7 +273,7 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
         if (!isinf(top)) z += lse * lse;
       }
       for (int j = l; j < a.topk; j += LPT) {
-        const int e = j == l ? first : id[j];
+        const int e = j == l ? first : a.ids[static_cast<size_t>(t) * a.topk + j];
         if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
         else bad = true;
       }
@@ -281,20 +314,16 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
     for (int w = 0; w < RT_WARPS; ++w) s += probs_w[w][e];
     return s;
   };
-  double bal = 0.0;
+  float bal = 0.0f;
   auto write = [&](int e, float p, int c, int n_seq) {
     const float m = static_cast<float>(max(n_seq, 1));
     p /= m;
     a.probs[static_cast<size_t>(seq) * E + e] = p;
     a.counts[static_cast<size_t>(seq) * E + e] = c;
-    bal += static_cast<double>(c) / m * p;
+    bal += static_cast<float>(c) / m * p;
   };
   if (a.sub == 1) {
     for (int e = threadIdx.x; e < E; e += RT_THREADS) write(e, expert_sum(e), cnt[e], n);
-    if (threadIdx.x == 0) {
-      a.tokens[seq] = n;
-      a.seq_z[seq] = z_item;
-    }
   } else {
     for (int e = threadIdx.x; e < E; e += RT_THREADS) {
       a.part_probs[static_cast<size_t>(item) * E + e] = expert_sum(e);
@@ -307,9 +336,9 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
     if (a.cols > 0) return;  // balance_join_kernel goes on
     if (!last_to_arrive(a.arrived + seq, a.sub - 1, &flag)) return;
     const int i0 = seq * a.sub;
-    int n_seq = 0;
-    double z_seq = 0.0;
     if (warp == 0) {
+      int n_seq = 0;
+      float z_seq = 0.0f;
       for (int i = lane; i < a.sub; i += 32) {
         n_seq += __ldcg(a.part_kept + i0 + i);
         z_seq += __ldcg(a.part_z + i0 + i);
@@ -317,16 +346,15 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
         a.part_z[i0 + i] = 0.0f;
       }
       n_seq = __reduce_add_sync(0xFFFFFFFFu, n_seq);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) z_seq += __shfl_xor_sync(0xFFFFFFFFu, z_seq, o);
+      z_seq = warp_sum(z_seq);
       if (lane == 0) {
         kept_w[0] = n_seq;
-        a.tokens[seq] = n_seq;
-        a.seq_z[seq] = z_seq;
+        z_w[0] = z_seq;
       }
     }
     __syncthreads();
-    n_seq = kept_w[0];
+    n = kept_w[0];
+    z_item = z_w[0];
     // an expert per warp, its items over the lanes, four experts in flight
     constexpr int BATCH = 4;
     for (int e0 = warp; e0 < E; e0 += RT_WARPS * BATCH) {
@@ -358,35 +386,44 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
         const int e = e0 + b * RT_WARPS;
         p[b] = warp_sum(p[b]);
         c[b] = __reduce_add_sync(0xFFFFFFFFu, c[b]);
-        if (lane == 0 && e < E) write(e, p[b], c[b], n_seq);
+        if (lane == 0 && e < E) write(e, p[b], c[b], n);
       }
     }
   }
-  bal = cta_sum<RT_THREADS>(bal, red);
-  if (threadIdx.x == 0) a.part_bal[seq] = bal;
-  if (!last_to_arrive(a.arrived + a.S, a.S - 1, &flag)) return;
-  write_losses<RT_THREADS>(a, a.S, red);
+  float none = 0.0f;
+  int no = 0;
+  cta_sums<RT_THREADS>(bal, none, no, red);
+  if (threadIdx.x == 0) {
+    a.tokens[seq] = n;
+    if (a.S == 1) {
+      write_losses(a, bal, z_item, n);
+    } else {
+      a.part_bal[seq] = bal;
+      a.seq_z[seq] = z_item;
+    }
+  }
+  if (a.S == 1 || !last_to_arrive(a.arrived + a.S, a.S - 1, &flag)) return;
+  join_losses<RT_THREADS>(a, a.S, red);
 }
 
 // Joins the items' sums of 32 experts of one sequence.
 __global__ void __launch_bounds__(JOIN_THREADS) balance_join_kernel(const __grid_constant__ BalanceArgs a) {
   __shared__ float probs_w[JOIN_WARPS][JOIN_COLS];
   __shared__ int cnt_w[JOIN_WARPS][JOIN_COLS];
-  __shared__ double red[JOIN_WARPS];
+  __shared__ float red[JOIN_WARPS * 3];
   __shared__ int kept, flag;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int seq = blockIdx.y, i0 = seq * a.sub, e = blockIdx.x * JOIN_COLS + lane;
   if (warp == 0) {  // every block of the sequence needs its count
     int n = 0;
-    double z = 0.0;
+    float z = 0.0f;
     for (int i = lane; i < a.sub; i += 32) {
       n += a.part_kept[i0 + i];
       z += a.part_z[i0 + i];
     }
     n = __reduce_add_sync(0xFFFFFFFFu, n);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+    z = warp_sum(z);
     if (lane == 0) {
       kept = n;
       if (blockIdx.x == 0) {
@@ -425,7 +462,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) balance_join_kernel(const __grid
   probs_w[warp][lane] = p;
   cnt_w[warp][lane] = c;
   __syncthreads();
-  double bal = 0.0;
+  float bal = 0.0f;
   if (warp == 0 && e < a.E) {
     for (int w = 1; w < JOIN_WARPS; ++w) {
       p += probs_w[w][lane];
@@ -435,16 +472,18 @@ __global__ void __launch_bounds__(JOIN_THREADS) balance_join_kernel(const __grid
     p /= n;
     a.probs[static_cast<size_t>(seq) * a.E + e] = p;
     a.counts[static_cast<size_t>(seq) * a.E + e] = c;
-    bal = static_cast<double>(c) / n * p;
+    bal = static_cast<float>(c) / n * p;
   }
-  bal = cta_sum<JOIN_THREADS>(bal, red);
-  if (threadIdx.x == 0) a.part_bal[seq * gridDim.x + blockIdx.x] = bal;
+  if (warp == 0) {
+    bal = warp_sum(bal);
+    if (lane == 0) a.part_bal[seq * gridDim.x + blockIdx.x] = bal;
+  }
   if (!last_to_arrive(a.arrived + a.S, gridDim.x * gridDim.y - 1, &flag)) return;
   for (int i = threadIdx.x; i < a.S * a.sub; i += JOIN_THREADS) {
     a.part_kept[i] = 0;
     a.part_z[i] = 0.0f;
   }
-  write_losses<JOIN_THREADS>(a, gridDim.x * gridDim.y, red);
+  join_losses<JOIN_THREADS>(a, gridDim.x * gridDim.y, red);
 }
 
 struct RouterBwdArgs {
@@ -519,7 +558,7 @@ router_bwd_kernel(const __grid_constant__ RouterBwdArgs a) {
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f[v][i] = flat || f[v][i] != f[v][i] ? 0.0f : exp_down(f[v][i] - lse);
+        f[v][i] = flat || f[v][i] != f[v][i] ? 0.0f : exp2_fast((f[v][i] - lse) * LOG2E);
         mean += f[v][i] * A[v][i];
       }
     mean = L::sum(mean);
@@ -613,8 +652,8 @@ BalancePlan balance_plan(int T, int E, int S) {
   p.counts = take(sizeof(int) * parts * E);
   p.kept = take(sizeof(int) * parts);
   p.z = take(sizeof(float) * parts);
-  p.bal = take(sizeof(double) * S * static_cast<size_t>(std::max(1, p.cols)));
-  p.seq_z = take(sizeof(double) * S);
+  p.bal = take(sizeof(float) * S * static_cast<size_t>(std::max(1, p.cols)));
+  p.seq_z = take(sizeof(float) * S);
   p.arrived = take(sizeof(uint32_t) * (static_cast<size_t>(S) + 1));
   p.total = at;
   return p;
@@ -677,8 +716,8 @@ extern "C" flux_status_t flux_moe_balance_loss(int T, int E, int topk, int seqs,
   a.part_counts = reinterpret_cast<int*>(ws + p.counts);
   a.part_kept = reinterpret_cast<int*>(ws + p.kept);
   a.part_z = reinterpret_cast<float*>(ws + p.z);
-  a.part_bal = reinterpret_cast<double*>(ws + p.bal);
-  a.seq_z = reinterpret_cast<double*>(ws + p.seq_z);
+  a.part_bal = reinterpret_cast<float*>(ws + p.bal);
+  a.seq_z = reinterpret_cast<float*>(ws + p.seq_z);
   a.arrived = reinterpret_cast<uint32_t*>(ws + p.arrived);
   a.E = E;
   a.topk = topk;
@@ -687,7 +726,7 @@ extern "C" flux_status_t flux_moe_balance_loss(int T, int E, int topk, int seqs,
   a.sub = p.sub;
   a.chunk = p.chunk;
   a.cols = p.cols;
-  a.balance_coef = balance_coef;
+  a.balance_scale = static_cast<float>(static_cast<double>(balance_coef) * E / (static_cast<double>(topk) * seqs));
   a.z_coef = z_coef;
   by_experts(E, [&](auto lpt, auto v, auto vec) {
     balance_kernel<decltype(lpt)::value, decltype(v)::value, decltype(vec)::value><<<p.items, RT_THREADS, 0, s>>>(a);
