@@ -15,6 +15,7 @@
 // Every element takes part in two (forward) or two dependent (backward) sums
 // over its row, so a row is held by one team of warps from its load to its
 // store and crosses HBM once in each direction.
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -72,114 +73,152 @@ __host__ __device__ __forceinline__ int cta_of_row(int T, int ctas, int t) {
   return static_cast<int>(((t + 1ll) * ctas - 1) / T);
 }
 
-template <int DT>
-__device__ __forceinline__ void load8(const void* base, size_t elem, float (&f)[8]) {
-  unpack8<DT>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elem)), f);
-}
+// Forward.  A team of W warps walks rows, V vectors of 8 columns per thread; as
+// in the backward pass below every thread copies its own columns of the rows to
+// come into its own slots of shared memory, and holds x' between its two sums
+// in registers.
+template <int W, int V>
+struct FwdShape {
+  static constexpr int ROW = Team<W>::CTA * V * 32;  // bytes of two tensors' rows, all teams of the CTA
+  static constexpr int DEPTH = V == 4 ? 2 : 3;
+  static constexpr int SMEM = ROW * DEPTH;
+  static constexpr int CTAS = W <= 8 ? 4 : V == 2 ? 2 : 1;  // per SM
+};
 
-// Weights of the vector at column `col`, or ones.
-template <int DT>
-__device__ __forceinline__ void load_or_one(const void* base, size_t elem, float (&f)[8]) {
-  if (base != nullptr) {
-    load8<DT>(base, elem, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 1.0f;
-  }
-}
-
-// Gate of row t at column `col`.
-template <int DT>
-__device__ __forceinline__ void load_gate(const BlockNormArgs& a, int t, int col, float (&f)[8]) {
-  if (a.gate == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 1.0f;
-  } else if (a.gate_cols == 1) {
-    const float g = load16<DT>(a.gate, t / a.gate_per);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = g;
-  } else {
-    load8<DT>(a.gate, static_cast<size_t>(t / a.gate_per) * a.H + col, f);
-  }
-}
-
-// Forward: one team of W warps per row, V vectors of 8 columns per thread.
-template <int DT, int W, int V>
-__global__ void __launch_bounds__(Team<W>::CTA)
+template <int DT, int W, int V, bool HAS_Y>
+__global__ void __launch_bounds__(Team<W>::CTA, (FwdShape<W, V>::CTAS))
 block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
-  __shared__ alignas(16) float red[Team<W>::COUNT][2 * W];
-  const int team = threadIdx.x / Team<W>::THREADS, lane = threadIdx.x % Team<W>::THREADS;
-  const int wit = lane / 32;
+  constexpr int TT = Team<W>::THREADS, TEAMS = Team<W>::COUNT, CTA = Team<W>::CTA, DEPTH = FwdShape<W, V>::DEPTH;
+  extern __shared__ uint4 ring[];  // [DEPTH][x, y][V][CTA]
+  __shared__ alignas(16) float red[TEAMS][2 * W];
+  const int team = threadIdx.x / TT, lane = threadIdx.x % TT, wit = lane / 32;
   int turn = 0;
   const float rho = a.res_scale != nullptr ? __ldg(a.res_scale) : 1.0f;
   const float inv_h = 1.0f / static_cast<float>(a.H);
-  for (long long t = static_cast<long long>(blockIdx.x) * Team<W>::COUNT + team; t < a.T;
-       t += static_cast<long long>(gridDim.x) * Team<W>::COUNT) {
-    const int rank = static_cast<int>(t) / a.rows_per_rank;
-    const size_t row = static_cast<size_t>(static_cast<int>(t) - rank * a.rows_per_rank) * a.H;
-    float x1[V][8];
-    float ry = 1.0f;
-    if (a.has_y) {
-      float ys[V][8];
-      float s[1] = {0.0f};
+  const int step = gridDim.x * TEAMS;
+  auto column = [&](int v) { return (v * TT + lane) * 8; };
+  auto slot = [&](int stage, int tensor, int v) -> uint4& { return ring[((stage * 2 + tensor) * V + v) * CTA + threadIdx.x]; };
+  int queue[DEPTH];  // the ranks of the rows on their way
+  int t_a = blockIdx.x * TEAMS + team, rank_a = t_a / a.rows_per_rank, rank_end_a = (rank_a + 1) * a.rows_per_rank, fill = 0;
+  auto issue = [&] {
+#pragma unroll
+    for (int i = 0; i + 1 < DEPTH; ++i) queue[i] = queue[i + 1];
+    if (t_a < a.T) {
+      while (t_a >= rank_end_a) {
+        ++rank_a;
+        rank_end_a += a.rows_per_rank;
+      }
+      queue[DEPTH - 1] = rank_a;
+      const size_t at = static_cast<size_t>(t_a - rank_a * a.rows_per_rank) * a.H + lane * 8;
+      const uint16_t* px = static_cast<const uint16_t*>(a.x[rank_a]) + at;
+      const uint16_t* py = HAS_Y ? static_cast<const uint16_t*>(a.y[rank_a]) + at : nullptr;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int col = (v * Team<W>::THREADS + lane) * 8;
-        if (col < a.H) {
-          load8<DT>(a.y[rank], row + col, ys[v]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[0] += ys[v][i] * ys[v][i];
+        if (column(v) < a.H) {
+          if constexpr (HAS_Y) copy16_async(&slot(fill, 1, v), py + v * TT * 8);
+          copy16_async(&slot(fill, 0, v), px + v * TT * 8);
         }
       }
+      t_a = t_a > INT_MAX - step ? a.T : t_a + step;
+    }
+    copy_commit();
+    fill = fill + 1 == DEPTH ? 0 : fill + 1;
+  };
+  // slots past H hold zeros
+#pragma unroll
+  for (int s = 0; s < DEPTH; ++s)
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (column(v) >= a.H) slot(s, 0, v) = slot(s, 1, v) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; ++i) issue();
+  // weights as they are stored, ones where there are none
+  const uint32_t one = pack2<DT>(1.0f, 1.0f);
+  auto weights = [&](const void* base, size_t at, int v) {
+    if (base == nullptr || column(v) >= a.H) return make_uint4(one, one, one, one);
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at + column(v)));
+  };
+  const bool col_gate = HAS_Y && a.gate != nullptr && a.gate_cols != 1, row_gate = HAS_Y && a.gate != nullptr && a.gate_cols == 1;
+  const bool one_gate = col_gate && a.gate_per == a.T;
+  uint4 wq[HAS_Y ? V : 1], wp[V], gq[HAS_Y ? V : 1];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    wp[v] = weights(a.w_pre, 0, v);
+    if constexpr (HAS_Y) {
+      wq[v] = weights(a.w_post, 0, v);
+      gq[v] = one_gate ? weights(a.gate, 0, v) : make_uint4(one, one, one, one);
+    }
+  }
+  const f32x2 rho2 = both(rho);
+  int stage = 0;
+  for (long long tl = static_cast<long long>(blockIdx.x) * TEAMS + team; tl < a.T; tl += step) {
+    const int t = static_cast<int>(tl);
+    float g_row = 1.0f;
+    if constexpr (HAS_Y) {
+      if (row_gate) g_row = load16<DT>(a.gate, t / a.gate_per);
+      if (col_gate && !one_gate) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) gq[v] = weights(a.gate, static_cast<size_t>(t / a.gate_per) * a.H, v);
+      }
+    }
+    issue();
+    const int rank = queue[0];
+    const size_t row = static_cast<size_t>(t - rank * a.rows_per_rank) * a.H + lane * 8;
+    copy_wait<DEPTH - 1>();
+    float a1 = g_row;
+    if constexpr (HAS_Y) {
       if (a.post_norm) {
-        team_sum<W>(s, red[team], turn, team, wit);
-        ry = rsqrtf(s[0] * inv_h + a.eps);
-        if (lane == 0 && a.rstd_y != nullptr) a.rstd_y[t] = ry;
-      }
+        f32x2 s = 0;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int col = (v * Team<W>::THREADS + lane) * 8;
-        if (col < a.H) {
-          float w[8], g[8];
-          load8<DT>(a.x[rank], row + col, x1[v]);
-          load_or_one<DT>(a.w_post, col, w);
-          load_gate<DT>(a, static_cast<int>(t), col, g);
+        for (int v = 0; v < V; ++v) {
+          f32x2 y[4];
+          unpack8<DT>(slot(stage, 1, v), y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x1[v][i] = rho * x1[v][i] + g[i] * (ys[v][i] * ry * w[i]);
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_a[rank]) + row + col) = pack8<DT>(x1[v]);
+          for (int i = 0; i < 4; ++i) s = fma2(y[i], y[i], s);
         }
+        float s1[1] = {halves(s).x + halves(s).y};
+        team_sum<W>(s1, red[team], turn, team, wit);
+        const float ry = rsqrtf(s1[0] * inv_h + a.eps);
+        if (lane == 0 && a.rstd_y != nullptr) a.rstd_y[t] = ry;
+        a1 *= ry;
       }
-    } else {
+    }
+    // x' = rho x + g (y r_y w)
+    const f32x2 a12 = both(a1);
+    f32x2 x1[V][4], s = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      unpack8<DT>(slot(stage, 0, v), x1[v]);
+      if constexpr (HAS_Y) {
+        f32x2 y[4], w[4], g[4];
+        unpack8<DT>(slot(stage, 1, v), y);
+        unpack8<DT>(wq[v], w);
+        unpack8<DT>(gq[v], g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x1[v][i] = fma2(mul2(mul2(y[i], a12), w[i]), g[i], mul2(rho2, x1[v][i]));
+        if (column(v) < a.H)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_a[rank]) + row + v * TT * 8) = pack8<DT>(x1[v]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = fma2(x1[v][i], x1[v][i], s);
+    }
+    if (a.has_u) {
+      float s1[1] = {halves(s).x + halves(s).y};
+      team_sum<W>(s1, red[team], turn, team, wit);
+      const float rx = rsqrtf(s1[0] * inv_h + a.eps);
+      if (lane == 0 && a.rstd_x != nullptr) a.rstd_x[t] = rx;
+      const f32x2 rx2 = both(rx);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int col = (v * Team<W>::THREADS + lane) * 8;
-        if (col < a.H) load8<DT>(a.x[rank], row + col, x1[v]);
+        f32x2 w[4];
+        unpack8<DT>(wp[v], w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = mul2(mul2(x1[v][i], rx2), w[i]);
+        if (column(v) < a.H)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_b[rank]) + row + v * TT * 8) = pack8<DT>(w);
       }
     }
-    if (!a.has_u) continue;
-    float s[1] = {0.0f};
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int col = (v * Team<W>::THREADS + lane) * 8;
-      if (col < a.H) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] += x1[v][i] * x1[v][i];
-      }
-    }
-    team_sum<W>(s, red[team], turn, team, wit);
-    const float rx = rsqrtf(s[0] * inv_h + a.eps);
-    if (lane == 0 && a.rstd_x != nullptr) a.rstd_x[t] = rx;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int col = (v * Team<W>::THREADS + lane) * 8;
-      if (col < a.H) {
-        float w[8];
-        load_or_one<DT>(a.w_pre, col, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = x1[v][i] * rx * w[i];
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_b[rank]) + row + col) = pack8<DT>(w);
-      }
-    }
+    stage = stage + 1 == DEPTH ? 0 : stage + 1;
   }
 }
 
@@ -810,15 +849,31 @@ void fill_common(BlockNormArgs* a, int R, int T, int H, int post_norm, int gate_
   a->w_pre = w_pre;
 }
 
+// Lets a kernel use `smem` bytes of shared memory; once per kernel.
+template <typename K>
+cudaError_t allow_smem(K kernel, int smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
+template <int DT, int W, int V, bool HAS_Y>
+flux_status_t launch_fwd_form(const BlockNormArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  using S = FwdShape<W, V>;
+  constexpr auto kernel = block_norm_kernel<DT, W, V, HAS_Y>;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] { attr = allow_smem(kernel, S::SMEM); });
+  if (attr != cudaSuccess) return cuda_fail(attr);
+  const int grid = std::min((a.T + Team<W>::COUNT - 1) / Team<W>::COUNT, dev.sm_count * S::CTAS);
+  kernel<<<grid, Team<W>::CTA, S::SMEM, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
+}
+
 template <int DT>
-flux_status_t launch_fwd(const BlockNormArgs& a, cudaStream_t s) {
+flux_status_t launch_fwd(const BlockNormArgs& a, const DeviceInfo& dev, cudaStream_t s) {
   return by_width(a.H, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
-    constexpr int teams = Team<W>::COUNT;
-    const int grid = static_cast<int>(std::min<long long>((a.T + teams - 1) / teams, 1 << 20));
-    block_norm_kernel<DT, W, V><<<grid, Team<W>::CTA, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
+    return a.has_y ? launch_fwd_form<DT, W, V, true>(a, dev, s) : launch_fwd_form<DT, W, V, false>(a, dev, s);
   });
 }
 
@@ -828,7 +883,7 @@ flux_status_t launch_bwd_form(const BlockNormArgs& a, const BwdPlan& p, cudaStre
   constexpr auto kernel = block_norm_bwd_kernel<DT, W, V, HAS_Y, HAS_U>;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] { attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  std::call_once(once, [] { attr = allow_smem(kernel, smem); });
   if (attr != cudaSuccess) return cuda_fail(attr);
   kernel<<<p.ctas, Team<W>::CTA, smem, s>>>(a);
   const cudaError_t e = cudaGetLastError();
@@ -886,7 +941,7 @@ extern "C" flux_status_t flux_block_norm(int R, int T, int H, flux_dtype_t dtype
   a.rstd_x = rstd_x;
   a.eps = eps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return dtype == FLUX_BF16 ? launch_fwd<1>(a, s) : launch_fwd<0>(a, s);
+  return dtype == FLUX_BF16 ? launch_fwd<1>(a, dev, s) : launch_fwd<0>(a, dev, s);
 }
 
 extern "C" size_t flux_block_norm_workspace_size(int T, int H, int gate_rows, int gate_cols) {

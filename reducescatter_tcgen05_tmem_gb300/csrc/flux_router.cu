@@ -38,7 +38,7 @@ constexpr int RT_ITEMS = 608;       // about this many CTAs: four per SM
 // the items of a sequence, and their sums, that its last CTA joins; more are joined
 // by a second kernel
 constexpr int RT_HERE_ITEMS = 64, RT_HERE_SUMS = 2048;
-constexpr int JOIN_COLS = 32, JOIN_WARPS = 16, JOIN_THREADS = JOIN_COLS * JOIN_WARPS;
+constexpr int JOIN_THREADS = 512, JOIN_FEW = 32;  // few items of a sequence: a thread adds all of an expert's
 
 // A token's scores are held by LPT lanes, four by four: V vectors of four a
 // lane.  Vectors of a row of 4 n experts are 16-byte loads of neighbours, other
@@ -47,6 +47,7 @@ template <int LPT, int V, bool VEC>
 struct Lanes {
   static constexpr int TPW = 32 / LPT;             // tokens of a warp at a time
   static constexpr int TPC = RT_WARPS * TPW;       // of a CTA
+  static constexpr int IDS = LPT <= 4 ? 2 : 1;     // expert ids that a lane loads ahead
   static __device__ __forceinline__ int expert(int l, int v, int i) {
     return VEC ? (v * LPT + l) * 4 + i : (v * 4 + i) * LPT + l;
   }
@@ -100,7 +101,7 @@ __device__ __forceinline__ float inverse_fast(float x) {
 // How the forward pass cuts the tokens: `sub` items of `chunk` tokens per
 // sequence, one CTA each.
 struct BalancePlan {
-  int sub, chunk, items, cols;  // cols: column blocks of the joining kernel, 0 if there is none
+  int sub, chunk, items, join_cols, cols;  // cols: blocks of join_cols experts of the joining kernel, 0 if there is none
   size_t probs, counts, kept, z, bal, seq_z, arrived, total;
 };
 
@@ -219,16 +220,21 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
   // the next tokens' scores, mask and first expert are on their way while these
   // are at work
   float next[V][4];
-  int next_id = 0, next_mask = 1;
+  int next_id[L::IDS] = {}, next_mask = 1;
   auto fetch = [&](int t) {
     const size_t at = static_cast<size_t>(t < t1 ? t : t0);
     L::load(a.logits + at * E, l, E, -INFINITY, next);
-    if (l < a.topk) next_id = __ldg(a.ids + at * a.topk + l);
+#pragma unroll
+    for (int k = 0; k < L::IDS; ++k)
+      if (l + k * LPT < a.topk) next_id[k] = __ldg(a.ids + at * a.topk + l + k * LPT);
     if (a.mask != nullptr) next_mask = __ldg(a.mask + at);
   };
   if (t0 + warp * L::TPW < t1) fetch(t0 + warp * L::TPW + tg);
   for (int tw = t0 + warp * L::TPW; tw < t1; tw += L::TPC) {
-    const int t = tw + tg, first = next_id;
+    const int t = tw + tg;
+    int id[L::IDS];
+#pragma unroll
+    for (int k = 0; k < L::IDS; ++k) id[k] = next_id[k];
     const bool here = t < t1, keep = here && next_mask != 0;
     float f[V][4];
     float top = -INFINITY;
@@ -272,11 +278,14 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
         ++kept;
         if (!isinf(top)) z += lse * lse;
       }
-      for (int j = l; j < a.topk; j += LPT) {
-        const int e = j == l ? first : a.ids[static_cast<size_t>(t) * a.topk + j];
+      auto count = [&](int e) {
         if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
         else bad = true;
-      }
+      };
+#pragma unroll
+      for (int k = 0; k < L::IDS; ++k)
+        if (l + k * LPT < a.topk) count(id[k]);
+      for (int j = l + L::IDS * LPT; j < a.topk; j += LPT) count(__ldg(a.ids + static_cast<size_t>(t) * a.topk + j));
     }
   }
   // tokens side by side in a warp, then the warps
@@ -406,15 +415,19 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
   join_losses<RT_THREADS>(a, a.S, red);
 }
 
-// Joins the items' sums of 32 experts of one sequence.
+// Joins the items' sums of COLS experts of one sequence, the items dealt out to
+// JOIN_THREADS / COLS threads.
+template <int COLS>
 __global__ void __launch_bounds__(JOIN_THREADS) balance_join_kernel(const __grid_constant__ BalanceArgs a) {
-  __shared__ float probs_w[JOIN_WARPS][JOIN_COLS];
-  __shared__ int cnt_w[JOIN_WARPS][JOIN_COLS];
-  __shared__ float red[JOIN_WARPS * 3];
+  constexpr int ROWS = JOIN_THREADS / COLS;
+  __shared__ float probs_w[ROWS][COLS];
+  __shared__ int cnt_w[ROWS][COLS];
+  __shared__ float red[JOIN_THREADS / 32 * 3];
   __shared__ int kept, flag;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int seq = blockIdx.y, i0 = seq * a.sub, e = blockIdx.x * JOIN_COLS + lane;
+  const int col = threadIdx.x % COLS, row = threadIdx.x / COLS;
+  const int seq = blockIdx.y, i0 = seq * a.sub, e = blockIdx.x * COLS + col;
   if (warp == 0) {  // every block of the sequence needs its count
     int n = 0;
     float z = 0.0f;
@@ -436,19 +449,19 @@ __global__ void __launch_bounds__(JOIN_THREADS) balance_join_kernel(const __grid
   float p = 0.0f;
   int c = 0;
   if (e < a.E) {
-    for (int i1 = warp; i1 < a.sub; i1 += JOIN_WARPS * BATCH) {
+    for (int i1 = row; i1 < a.sub; i1 += ROWS * BATCH) {
       float fp[BATCH];
       int fc[BATCH];
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) {
-        const int i = i1 + b * JOIN_WARPS;
+        const int i = i1 + b * ROWS;
         const size_t at = static_cast<size_t>(i0 + i) * a.E + e;
         fp[b] = i < a.sub ? a.part_probs[at] : 0.0f;
         fc[b] = i < a.sub ? a.part_counts[at] : 0;
       }
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) {
-        const int i = i1 + b * JOIN_WARPS;
+        const int i = i1 + b * ROWS;
         const size_t at = static_cast<size_t>(i0 + i) * a.E + e;
         if (i < a.sub) {
           a.part_probs[at] = 0.0f;
@@ -459,14 +472,15 @@ __global__ void __launch_bounds__(JOIN_THREADS) balance_join_kernel(const __grid
       }
     }
   }
-  probs_w[warp][lane] = p;
-  cnt_w[warp][lane] = c;
+  probs_w[row][col] = p;
+  cnt_w[row][col] = c;
   __syncthreads();
-  float bal = 0.0f;
-  if (warp == 0 && e < a.E) {
-    for (int w = 1; w < JOIN_WARPS; ++w) {
-      p += probs_w[w][lane];
-      c += cnt_w[w][lane];
+  float bal = 0.0f, none = 0.0f;
+  int no = 0;
+  if (row == 0 && e < a.E) {
+    for (int w = 1; w < ROWS; ++w) {
+      p += probs_w[w][col];
+      c += cnt_w[w][col];
     }
     const float n = static_cast<float>(max(kept, 1));
     p /= n;
@@ -474,10 +488,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) balance_join_kernel(const __grid
     a.counts[static_cast<size_t>(seq) * a.E + e] = c;
     bal = static_cast<float>(c) / n * p;
   }
-  if (warp == 0) {
-    bal = warp_sum(bal);
-    if (lane == 0) a.part_bal[seq * gridDim.x + blockIdx.x] = bal;
-  }
+  cta_sums<JOIN_THREADS>(bal, none, no, red);
+  if (threadIdx.x == 0) a.part_bal[seq * gridDim.x + blockIdx.x] = bal;
   if (!last_to_arrive(a.arrived + a.S, gridDim.x * gridDim.y - 1, &flag)) return;
   for (int i = threadIdx.x; i < a.S * a.sub; i += JOIN_THREADS) {
     a.part_kept[i] = 0;
@@ -613,24 +625,38 @@ router_bwd_kernel(const __grid_constant__ RouterBwdArgs a) {
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// Calls f(LPT, V, VEC) for the lanes that hold a row of E scores.
-template <typename F>
+// Calls f(LPT, V, VEC) for the lanes that hold a row of E scores.  Forward: four
+// vectors a lane; what a token costs besides its scores (sums over its lanes,
+// logarithm, inverse, counts) is shared by several tokens of the warp (131072 x
+// 256: 31 us with two tokens a warp, 40 with one).  Backward has less of that
+// and wants more lanes' loads on their way: one or two vectors (53 against 58 us).
+template <bool FORWARD, typename F>
 auto by_experts(int E, F&& f) {
   auto vec = [&](auto lpt, auto v) { return E % 4 == 0 ? f(lpt, v, std::true_type{}) : f(lpt, v, std::false_type{}); };
   if (E <= 4) return vec(Int<1>{}, Int<1>{});
-  if (E <= 8) return vec(Int<2>{}, Int<1>{});
-  if (E <= 16) return vec(Int<4>{}, Int<1>{});
-  if (E <= 32) return vec(Int<8>{}, Int<1>{});
-  if (E <= 64) return vec(Int<16>{}, Int<1>{});
-  if (E <= 128) return vec(Int<32>{}, Int<1>{});
-  if (E <= 256) return vec(Int<32>{}, Int<2>{});
+  if constexpr (FORWARD) {
+    if (E <= 8) return vec(Int<1>{}, Int<2>{});
+    if (E <= 16) return vec(Int<1>{}, Int<4>{});
+    if (E <= 32) return vec(Int<2>{}, Int<4>{});
+    if (E <= 64) return vec(Int<4>{}, Int<4>{});
+    if (E <= 128) return vec(Int<8>{}, Int<4>{});
+    if (E <= 256) return vec(Int<16>{}, Int<4>{});
+  } else {
+    if (E <= 8) return vec(Int<2>{}, Int<1>{});
+    if (E <= 16) return vec(Int<4>{}, Int<1>{});
+    if (E <= 32) return vec(Int<8>{}, Int<1>{});
+    if (E <= 64) return vec(Int<16>{}, Int<1>{});
+    if (E <= 128) return vec(Int<32>{}, Int<1>{});
+    if (E <= 256) return vec(Int<32>{}, Int<2>{});
+  }
   if (E <= 512) return vec(Int<32>{}, Int<4>{});
   return vec(Int<32>{}, Int<8>{});
 }
 
 // Items of a sequence: about RT_ITEMS CTAs in all, each with work for its warps.
+template <bool FORWARD>
 void cut_tokens(int E, int per, int S, int* sub, int* chunk) {
-  const int tokens = by_experts(E, [](auto lpt, auto, auto) { return RT_WARPS * 32 / decltype(lpt)::value; });
+  const int tokens = by_experts<FORWARD>(E, [](auto lpt, auto, auto) { return RT_WARPS * 32 / decltype(lpt)::value; });
   *sub = std::max(1, std::min((RT_ITEMS + S - 1) / S, (per + tokens - 1) / tokens));
   *chunk = (per + *sub - 1) / *sub;
   *sub = (per + *chunk - 1) / *chunk;
@@ -638,9 +664,10 @@ void cut_tokens(int E, int per, int S, int* sub, int* chunk) {
 
 BalancePlan balance_plan(int T, int E, int S) {
   BalancePlan p{};
-  cut_tokens(E, T / S, S, &p.sub, &p.chunk);
+  cut_tokens<true>(E, T / S, S, &p.sub, &p.chunk);
   p.items = p.sub * S;
-  p.cols = p.sub > RT_HERE_ITEMS || (p.sub > 1 && static_cast<long long>(p.sub) * E > RT_HERE_SUMS) ? (E + JOIN_COLS - 1) / JOIN_COLS : 0;
+  p.join_cols = p.sub <= JOIN_FEW ? 256 : 32;
+  p.cols = p.sub > RT_HERE_ITEMS || (p.sub > 1 && static_cast<long long>(p.sub) * E > RT_HERE_SUMS) ? (E + p.join_cols - 1) / p.join_cols : 0;
   size_t at = WS_HEADER;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -728,7 +755,7 @@ extern "C" flux_status_t flux_moe_balance_loss(int T, int E, int topk, int seqs,
   a.cols = p.cols;
   a.balance_scale = static_cast<float>(static_cast<double>(balance_coef) * E / (static_cast<double>(topk) * seqs));
   a.z_coef = z_coef;
-  by_experts(E, [&](auto lpt, auto v, auto vec) {
+  by_experts<true>(E, [&](auto lpt, auto v, auto vec) {
     balance_kernel<decltype(lpt)::value, decltype(v)::value, decltype(vec)::value><<<p.items, RT_THREADS, 0, s>>>(a);
   });
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
@@ -742,7 +769,8 @@ extern "C" flux_status_t flux_moe_balance_loss(int T, int E, int topk, int seqs,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, balance_join_kernel, a);
+  e = p.join_cols == 256 ? cudaLaunchKernelEx(&cfg, balance_join_kernel<256>, a)
+                         : cudaLaunchKernelEx(&cfg, balance_join_kernel<32>, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
@@ -779,10 +807,10 @@ extern "C" flux_status_t flux_moe_router_bwd(int T, int E, int topk, int seqs, f
   a.topk = topk;
   a.S = seqs;
   a.per = T / seqs;
-  cut_tokens(E, a.per, seqs, &a.sub, &a.chunk);
+  cut_tokens<false>(E, a.per, seqs, &a.sub, &a.chunk);
   a.balance_coef = balance_coef;
   a.z_coef = z_coef;
-  by_experts(E, [&](auto lpt, auto v, auto vec) {
+  by_experts<false>(E, [&](auto lpt, auto v, auto vec) {
     router_bwd_kernel<decltype(lpt)::value, decltype(v)::value, decltype(vec)::value><<<a.sub * seqs, RT_THREADS, 0, s>>>(a);
   });
   const cudaError_t e = cudaGetLastError();
