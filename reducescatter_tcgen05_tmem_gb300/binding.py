@@ -10,6 +10,7 @@ raises if the compiled library is missing.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -170,10 +171,17 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_PTRS = {}  # ctypes array types by length
+
+
 def _ptrs(xs):
     if xs is None:
         return None
-    return (ctypes.c_void_p * len(xs))(*map(_ptr, xs))
+    n = len(xs)
+    make = _PTRS.get(n) or _PTRS.setdefault(n, ctypes.c_void_p * n)
+    if n == 1:
+        return make(_ptr(xs[0]))
+    return make.from_buffer(array.array("Q", [_ptr(x) or 0 for x in xs]))
 
 
 def _nbytes(t):

@@ -458,6 +458,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
   };
   float* my_post = a.part_post + static_cast<size_t>(blockIdx.x) * a.H;
   float* my_pre = a.part_pre + static_cast<size_t>(blockIdx.x) * a.H;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // block_norm_sums_kernel waits for all of this
   const f32x2 rho2 = both(rho);
 
   // slots that no copy fills hold zeros: columns past H, a gradient not given
@@ -637,7 +638,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
   }
 }
 
-constexpr int SUM_COLS = 32, SUM_WARPS = 32, SUM_BATCH = 10;
+constexpr int SUM_COLS = 32, SUM_WARPS = 8, SUM_BATCH = 20;
 
 constexpr int SUM_THREADS = SUM_COLS * SUM_WARPS;
 // blocks of block_norm_sums_kernel: dw_pre and dw_post by columns, the scalars, cut runs by columns
@@ -650,6 +651,7 @@ template <int DT>
 __global__ void __launch_bounds__(SUM_THREADS)
 block_norm_sums_kernel(const __grid_constant__ BlockNormArgs a, int col_blocks, int per_run_blocks) {
   __shared__ float part[SUM_WARPS][SUM_COLS];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x % SUM_COLS, warp = threadIdx.x / SUM_COLS;
   const bool one_row = a.gate != nullptr && a.gate_cols != 1 && a.gate_per == a.T;
   if (blockIdx.x < 2 * col_blocks) {
@@ -703,14 +705,20 @@ block_norm_sums_kernel(const __grid_constant__ BlockNormArgs a, int col_blocks, 
   }
   // the run that CTA b - 1 and CTA b share, if b is the first to continue it
   const int k = blockIdx.x - 2 * col_blocks - 1;
-  const int b = 1 + k / per_run_blocks, at = first_row(a.T, a.ctas, b), run = at / a.run_rows;
-  const int r0 = run * a.run_rows;
-  if (r0 == at) return;
-  const int c0 = cta_of_row(a.T, a.ctas, r0), c1 = cta_of_row(a.T, a.ctas, r0 + a.run_rows - 1);
-  if (c0 != b - 1) return;
-  const int first = 2 * c0 + (first_row(a.T, a.ctas, c0) == r0 ? 0 : 1);
+  __shared__ int run_s, first_s, c0_s, c1_s;
+  if (threadIdx.x == 0) {
+    const int b = 1 + k / per_run_blocks, at = first_row(a.T, a.ctas, b), r = at / a.run_rows, r0 = r * a.run_rows;
+    run_s = r;
+    c0_s = cta_of_row(a.T, a.ctas, r0);
+    c1_s = r0 == at || c0_s != b - 1 ? -1 : cta_of_row(a.T, a.ctas, r0 + a.run_rows - 1);
+    first_s = 2 * c0_s + (first_row(a.T, a.ctas, c0_s) == r0 ? 0 : 1);
+  }
+  __syncthreads();
+  const int run = run_s, first = first_s, c0 = c0_s, c1 = c1_s;
+  if (c1 < 0) return;
   auto place = [&](int i) { return i == 0 ? first : 2 * (c0 + i); };
   const int n = c1 - c0 + 1;
+  constexpr int RUN_BATCH = 8;
   if (a.gate_cols == 1) {
     if (threadIdx.x != 0 || k % per_run_blocks != 0) return;
     double s = 0.0;
@@ -724,13 +732,13 @@ block_norm_sums_kernel(const __grid_constant__ BlockNormArgs a, int col_blocks, 
   const int col = (k % per_run_blocks * SUM_THREADS + threadIdx.x) * 4;
   if (col >= a.H) return;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int i0 = 0; i0 < n; i0 += SUM_BATCH) {
-    float4 v[SUM_BATCH];
+  for (int i0 = 0; i0 < n; i0 += RUN_BATCH) {
+    float4 v[RUN_BATCH];
 #pragma unroll
-    for (int j = 0; j < SUM_BATCH; ++j)
+    for (int j = 0; j < RUN_BATCH; ++j)
       if (i0 + j < n) v[j] = *reinterpret_cast<const float4*>(a.part_gate + static_cast<size_t>(place(i0 + j)) * a.H + col);
 #pragma unroll
-    for (int j = 0; j < SUM_BATCH; ++j) {
+    for (int j = 0; j < RUN_BATCH; ++j) {
       if (i0 + j >= n) break;
       *reinterpret_cast<float4*>(a.part_gate + static_cast<size_t>(place(i0 + j)) * a.H + col) =
           make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -900,8 +908,16 @@ flux_status_t launch_bwd(const BlockNormArgs& a, const BwdPlan& p, cudaStream_t 
   if (st != FLUX_OK) return st;
   const int cols = sum_blocks(a.H), per_run = a.gate_cols == 1 ? 1 : run_blocks(a.H);
   const int cut = p.cut_runs && a.dgate != nullptr ? (p.ctas - 1) * per_run : 0;
-  block_norm_sums_kernel<DT><<<2 * cols + 1 + cut, SUM_THREADS, 0, s>>>(a, cols, per_run);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * cols + 1 + cut, 1, 1);
+  cfg.blockDim = dim3(SUM_THREADS, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, block_norm_sums_kernel<DT>, a, cols, per_run);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
