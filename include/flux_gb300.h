@@ -55,7 +55,9 @@
  *     fallback path.
  *   - Workspaces must be 256-byte aligned, at least flux_*workspace_size()
  *     bytes, and zero-filled once before first use (flux_workspace_init).
- *     Every successful call leaves its workspace zero again.  Calls that share
+ *     Every successful call leaves its workspace zero again (the MoE layers leave
+ *     their routing and staged rows in it).  The block-norm, router and 4-bit
+ *     calls need zeros in the first 256 bytes only.  Calls that share
  *     one workspace must be ordered on the GPU (same stream or events); calls
  *     that overlap on the GPU need separate workspaces.
  */

@@ -243,9 +243,10 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
 template <int W, int V>
 struct BwdShape {
   static constexpr int ROW = Team<W>::CTA * V * 64;  // bytes of four tensors' rows, all teams of the CTA
-  static constexpr int DEPTH = W <= 8 ? (V == 1 ? 4 : 3) : V == 2 ? 3 : V == 3 ? 2 : 1;
+  static constexpr int VECS = W * V * 32;  // of a row
+  static constexpr int DEPTH = W <= 8 ? (V == 1 ? 4 : 3) : VECS <= 1024 ? 3 : VECS <= 1536 ? 2 : 1;
   static constexpr int JOIN = Team<W>::COUNT > 1 ? Team<W>::CTA * V * 32 : 0;
-  static constexpr int WEIGHTS = V > 3 ? Team<W>::CTA * V * 48 : 0;  // gw in fp32, w_pre as stored
+  static constexpr int WEIGHTS = VECS > 1536 ? VECS * 48 : VECS > 1024 ? VECS * 16 : 0;  // gw in fp32, w_pre as stored
   static constexpr int SMEM = ROW * DEPTH + JOIN + WEIGHTS;
   static constexpr int CTAS = W <= 8 ? 2 : 1;  // per SM
 };
@@ -255,10 +256,10 @@ __global__ void __launch_bounds__(Team<W>::CTA, (BwdShape<W, V>::CTAS))
 block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
   constexpr int TT = Team<W>::THREADS, TEAMS = Team<W>::COUNT, CTA = Team<W>::CTA;
   constexpr int DEPTH = BwdShape<W, V>::DEPTH;
-  // up to two vectors a thread: the weights as floats and d in registers; three:
-  // w_pre as stored, d in two slots whose values have been used; four: the
-  // weights in shared memory too (reloaded from L2 they took 2/3 of the time)
-  constexpr bool ROOMY = V <= 2;
+  // up to 8192 columns: the weights as floats and d in registers; up to 12288:
+  // w_pre in shared memory, d in two slots whose values have been used; more: all
+  // weights in shared memory (reloaded from L2 they took 2/3 of the time)
+  constexpr bool ROOMY = BwdShape<W, V>::VECS <= 1024, GW_REGS = BwdShape<W, V>::VECS <= 1536;
   enum { X = 0, Y = 1, DU = 2, DX = 3 };
   extern __shared__ uint4 ring[];  // [DEPTH][tensor][V][CTA]
   float* join = reinterpret_cast<float*>(ring + BwdShape<W, V>::ROW / 16 * DEPTH);
@@ -323,10 +324,9 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
   };
 
   // the product of w_post and the gate's columns, and w_pre
-  f32x2 gw_r[V <= 3 ? V : 1][4], wp_r[ROOMY ? V : 1][4];
-  uint4 wp_q[V == 3 ? V : 1];
-  uint4* gw_s = reinterpret_cast<uint4*>(join);  // V > 3: [2][V][CTA], then w_pre [V][CTA] (JOIN is 0 there)
-  uint4* wp_s = gw_s + 2 * V * CTA;
+  f32x2 gw_r[GW_REGS ? V : 1][4], wp_r[ROOMY ? V : 1][4];
+  uint4* gw_s = reinterpret_cast<uint4*>(join);  // [2][V][CTA] if not in registers, then w_pre [V][CTA] (JOIN is 0 there)
+  uint4* wp_s = gw_s + (GW_REGS ? 0 : 2 * V * CTA);
   const uint32_t one16 = pack2<DT>(1.0f, 1.0f);
   auto weight8 = [&](const void* base, size_t at, bool inside, f32x2 (&f)[4]) {
     if (!inside) {
@@ -352,7 +352,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
   auto put_gw = [&](int run) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if constexpr (V <= 3) {
+      if constexpr (GW_REGS) {
         load_gw(v, run, gw_r[v]);
       } else {
         f32x2 gw[4];
@@ -364,7 +364,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
     }
   };
   auto get_gw = [&](int v, f32x2 (&gw)[4]) {
-    if constexpr (V <= 3) {
+    if constexpr (GW_REGS) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) gw[i] = gw_r[v][i];
     } else {
@@ -378,7 +378,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) wp[i] = wp_r[v][i];
     } else {
-      unpack8<DT>(V == 3 ? wp_q[V == 3 ? v : 0] : wp_s[v * CTA + threadIdx.x], wp);
+      unpack8<DT>(wp_s[v * CTA + threadIdx.x], wp);
     }
   };
   if constexpr (HAS_U) {
@@ -390,7 +390,6 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
                 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.w_pre) + column(v)))
                 : make_uint4(one16, one16, one16, one16);
       if constexpr (ROOMY) unpack8<DT>(q, wp_r[v]);
-      else if constexpr (V == 3) wp_q[v] = q;
       else wp_s[v * CTA + threadIdx.x] = q;
     }
   }

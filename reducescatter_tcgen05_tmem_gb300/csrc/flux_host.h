@@ -15,6 +15,10 @@ namespace flux {
 
 constexpr size_t WS_HEADER = 256;  // status header at the start of every workspace
 constexpr size_t WS_ALIGN = 256;
+// Words of that header in which the CTAs of the router and 4-bit kernels count
+// their arrivals, so that these calls need no zeros anywhere else in a workspace.
+constexpr int WS_ARRIVED = 16;  // items of a sequence; [1] sequences or blocks
+constexpr int WS_JOINED = 18;   // blocks that are done with the routing
 // Dynamic schedule of the dense kernels: at most this many regions of 4 CTAs.
 constexpr int MAX_REGIONS = 64;
 

@@ -35,8 +35,8 @@ namespace {
 
 constexpr int RT_WARPS = 8, RT_THREADS = RT_WARPS * 32;
 constexpr int RT_ITEMS = 608;       // about this many CTAs: four per SM
-// the items of a sequence, and their sums, that its last CTA joins; more are joined
-// by a second kernel
+// the items of a lone sequence, and their sums, that its last CTA joins; more are
+// joined by a second kernel
 constexpr int RT_HERE_ITEMS = 64, RT_HERE_SUMS = 2048;
 constexpr int JOIN_THREADS = 512, JOIN_FEW = 32;  // few items of a sequence: a thread adds all of an expert's
 
@@ -102,7 +102,7 @@ __device__ __forceinline__ float inverse_fast(float x) {
 // sequence, one CTA each.
 struct BalancePlan {
   int sub, chunk, items, join_cols, cols;  // cols: blocks of join_cols experts of the joining kernel, 0 if there is none
-  size_t probs, counts, kept, z, bal, seq_z, arrived, total;
+  size_t probs, counts, kept, z, bal, seq_z, total;
 };
 
 struct BalanceArgs {
@@ -122,7 +122,7 @@ struct BalanceArgs {
   float* part_z;
   float* part_bal;
   float* seq_z;
-  uint32_t* arrived;  // [S] items of a sequence, then [1] sequences (or blocks)
+  uint32_t* arrived;  // header words: items of the one sequence, then sequences or blocks
   int E, topk, S, per, sub, chunk, cols;
   float balance_scale, z_coef;
 };
@@ -194,8 +194,8 @@ __device__ __forceinline__ void join_losses(const BalanceArgs& a, int n, float* 
 // Forward.  One read of the scores: a token's maximum, exponentials and their
 // sum stay in the registers of its lanes, which add its probabilities to their
 // own experts' sums.  An item's sums are joined over its warps in shared memory,
-// a sequence's over its items by the last of their CTAs to end, or, where they
-// are many, by balance_join_kernel; all in fixed orders.
+// a sequence's over its items by balance_join_kernel, or, where there is one
+// sequence of few items, by the last of their CTAs; all in fixed orders.
 template <int LPT, int V, bool VEC>
 __global__ void __launch_bounds__(RT_THREADS)
 balance_kernel(const __grid_constant__ BalanceArgs a) {
@@ -343,7 +343,7 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
       a.part_z[item] = z_item;
     }
     if (a.cols > 0) return;  // balance_join_kernel goes on
-    if (!last_to_arrive(a.arrived + seq, a.sub - 1, &flag)) return;
+    if (!last_to_arrive(a.arrived, a.sub - 1, &flag)) return;
     const int i0 = seq * a.sub;
     if (warp == 0) {
       int n_seq = 0;
@@ -411,7 +411,7 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
       a.seq_z[seq] = z_item;
     }
   }
-  if (a.S == 1 || !last_to_arrive(a.arrived + a.S, a.S - 1, &flag)) return;
+  if (a.S == 1 || !last_to_arrive(a.arrived + 1, a.S - 1, &flag)) return;
   join_losses<RT_THREADS>(a, a.S, red);
 }
 
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) balance_join_kernel(const __grid
   }
   cta_sums<JOIN_THREADS>(bal, none, no, red);
   if (threadIdx.x == 0) a.part_bal[seq * gridDim.x + blockIdx.x] = bal;
-  if (!last_to_arrive(a.arrived + a.S, gridDim.x * gridDim.y - 1, &flag)) return;
+  if (!last_to_arrive(a.arrived + 1, gridDim.x * gridDim.y - 1, &flag)) return;
   for (int i = threadIdx.x; i < a.S * a.sub; i += JOIN_THREADS) {
     a.part_kept[i] = 0;
     a.part_z[i] = 0.0f;
@@ -667,7 +667,8 @@ BalancePlan balance_plan(int T, int E, int S) {
   cut_tokens<true>(E, T / S, S, &p.sub, &p.chunk);
   p.items = p.sub * S;
   p.join_cols = p.sub <= JOIN_FEW ? 256 : 32;
-  p.cols = p.sub > RT_HERE_ITEMS || (p.sub > 1 && static_cast<long long>(p.sub) * E > RT_HERE_SUMS) ? (E + p.join_cols - 1) / p.join_cols : 0;
+  const bool here = S == 1 && p.sub <= RT_HERE_ITEMS && static_cast<long long>(p.sub) * E <= RT_HERE_SUMS;
+  p.cols = p.sub > 1 && !here ? (E + p.join_cols - 1) / p.join_cols : 0;
   size_t at = WS_HEADER;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -681,7 +682,6 @@ BalancePlan balance_plan(int T, int E, int S) {
   p.z = take(sizeof(float) * parts);
   p.bal = take(sizeof(float) * S * static_cast<size_t>(std::max(1, p.cols)));
   p.seq_z = take(sizeof(float) * S);
-  p.arrived = take(sizeof(uint32_t) * (static_cast<size_t>(S) + 1));
   p.total = at;
   return p;
 }
@@ -745,7 +745,7 @@ extern "C" flux_status_t flux_moe_balance_loss(int T, int E, int topk, int seqs,
   a.part_z = reinterpret_cast<float*>(ws + p.z);
   a.part_bal = reinterpret_cast<float*>(ws + p.bal);
   a.seq_z = reinterpret_cast<float*>(ws + p.seq_z);
-  a.arrived = reinterpret_cast<uint32_t*>(ws + p.arrived);
+  a.arrived = static_cast<uint32_t*>(workspace) + WS_ARRIVED;
   a.E = E;
   a.topk = topk;
   a.S = seqs;

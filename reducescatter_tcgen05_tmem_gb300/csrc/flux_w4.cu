@@ -197,7 +197,9 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint16_t order[FLUX_W4_MAX_ROWS];       // slots by expert
   __shared__ W4RowTile tiles[FLUX_W4_MAX_ROWS];
-  int* hist = reinterpret_cast<int*>(ring);  // before the ring is used
+  int* hist = reinterpret_cast<int*>(ring);  // before the ring is used, as
+  int* slot_expert = hist + FLUX_MAX_EXPERTS;
+  static_assert(S::SMEM >= 4 * (FLUX_MAX_EXPERTS + FLUX_W4_MAX_ROWS), "the ring holds the routing first");
   __shared__ int scan[2][W4_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int col_tiles = (a.N + W4_COLS - 1) / W4_COLS;
@@ -215,9 +217,14 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
     __syncthreads();
     bool bad = false;
     for (int i = tid; i < a.slots; i += W4_THREADS) {
-      const int e = a.ids[i];
-      if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
-      else bad = true;
+      int e = a.ids[i];
+      if (e >= 0 && e < a.E) {
+        atomicAdd(&hist[e], 1);
+      } else {
+        bad = true;
+        e = -1;
+      }
+      slot_expert[i] = e;
     }
     if (bad) atomicCAS(a.hdr, 0u, static_cast<uint32_t>(FLUX_ERR_INVALID_ARG));
     __syncthreads();
@@ -265,8 +272,8 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
     __syncthreads();
     if (warp == 0) {
       for (int i0 = 0; i0 < a.slots; i0 += 32) {
-        const int i = i0 + lane, e = i < a.slots ? a.ids[i] : -1;
-        const bool in = e >= 0 && e < a.E;
+        const int i = i0 + lane, e = i < a.slots ? slot_expert[i] : -1;
+        const bool in = e >= 0;
         const unsigned same = __match_any_sync(0xFFFFFFFFu, in ? e : -1 - lane);
         const int at = in ? hist[e] : 0;
         __syncwarp();
@@ -618,7 +625,7 @@ w4_quantize_kernel(int K, int N, int runs, int group, int groups, const void* __
 
 // Workspace: header, arrivals, finished row tiles, partial tiles, fp32 rows.
 struct W4Ws {
-  size_t split, joined, where, parts, rows, total;
+  size_t split, where, parts, rows, total;
 };
 
 int w4_row_tiles_of_8(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
@@ -632,7 +639,6 @@ W4Ws w4_ws(int slots, int N) {
     return here;
   };
   w.split = take(sizeof(W4Split));
-  w.joined = take(sizeof(uint32_t));
   w.where = take(sizeof(W4Slot) * slots);
   w.parts = take(sizeof(float) * 2 * W4_MAX_CTAS * W4_COLS * 8 * w4_row_tiles_of_8(slots));
   w.rows = take(sizeof(float) * slots * static_cast<size_t>(N));
@@ -730,7 +736,7 @@ flux_status_t w4_run(W4Mode mode, int rows, int slots, int T, int N, int K, int 
   a.out = static_cast<uint16_t*>(out);
   a.hdr = static_cast<uint32_t*>(workspace);
   a.split = reinterpret_cast<W4Split*>(ws + w.split);
-  a.joined = reinterpret_cast<uint32_t*>(ws + w.joined);
+  a.joined = static_cast<uint32_t*>(workspace) + WS_JOINED;
   a.where = reinterpret_cast<W4Slot*>(ws + w.where);
   a.parts = reinterpret_cast<float*>(ws + w.parts);
   a.rows_f32 = reinterpret_cast<float*>(ws + w.rows);

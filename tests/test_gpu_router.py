@@ -232,3 +232,15 @@ def test_sum_over_a_long_batch_is_exact_in_the_counts():
     p = torch.softmax(logits.double(), 1).mean(0).cpu().numpy()
     check32(o["probs"].cpu().numpy(), p, p * 2, depth=700)
     assert abs(float(o["probs"].double().sum()) - 1) < 700 * U32 * 2
+
+
+@pytest.mark.parametrize("T,E,k,S", [(512, 8, 2, 1), (700, 256, 4, 1), (640, 16, 2, 64), (4096, 32, 2, 4)])
+def test_what_a_workspace_holds_past_its_header_does_not_matter(T, E, k, S):
+    # the MoE layers leave their routing in theirs
+    r = Router(T, E, k, S, "some")
+    want = r.forward()
+    r.ws[64:] = 0x7F7F7F7F
+    got = r.forward()
+    for n in want:
+        assert np.array_equal(got[n], want[n]), n
+    assert not bool(r.ws[:64].any())

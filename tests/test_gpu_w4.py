@@ -284,3 +284,22 @@ def test_another_stream():
     fx.flux_w4_gemv(M, N, K, group, fx.FLUX_F16, x, w.q, w.s, b, ws2, stream=s)
     s.synchronize()
     assert torch.equal(a, b)
+
+
+def test_what_a_workspace_holds_past_its_header_does_not_matter():
+    T, H, F, E, k, group = 5, 640, 392, 6, 2, 64
+    ids, gw = _routing(T, E, k, 81)
+    cids, cw = torch.from_numpy(ids).cuda(), torch.from_numpy(gw).cuda()
+    w2 = Weights(E, F, H, group, "bf16", 82)
+    h = to_device(gen.normal16((83, 2), (T * k, F), 1.0, "bf16"), "bf16")
+    outs = []
+    for fill in (0, 0x7F7F7F7F):
+        ws = _ws(T * k, H, F, E)
+        ws[64:] = fill
+        out = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+        fx.flux_moe_w4_layer1(T, H, F, E, k, group, fx.FLUX_BF16, h, w2.q, w2.s, cids, cw, out, ws)
+        one = torch.empty((T * k, H), dtype=torch.bfloat16, device="cuda")
+        fx.flux_w4_gemv(T * k, H, F, group, fx.FLUX_BF16, h, w2.q[:H], w2.s[0], one, ws)
+        assert not bool(ws[:64].any())
+        outs.append((out, one))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
