@@ -34,7 +34,7 @@ namespace flux {
 namespace {
 
 constexpr int RT_WARPS = 8, RT_THREADS = RT_WARPS * 32;
-constexpr int RT_ITEMS = 608;       // about this many CTAs: four per SM
+constexpr int RT_FWD_CTAS = 3 * 152, RT_BWD_CTAS = 4 * 152;  // at most this many: one wave
 // the items of a lone sequence, and their sums, that its last CTA joins; more are
 // joined by a second kernel
 constexpr int RT_HERE_ITEMS = 64, RT_HERE_SUMS = 2048;
@@ -197,7 +197,7 @@ __device__ __forceinline__ void join_losses(const BalanceArgs& a, int n, float* 
 // a sequence's over its items by balance_join_kernel, or, where there is one
 // sequence of few items, by the last of their CTAs; all in fixed orders.
 template <int LPT, int V, bool VEC>
-__global__ void __launch_bounds__(RT_THREADS)
+__global__ void __launch_bounds__(RT_THREADS, V <= 4 ? 3 : 2)
 balance_kernel(const __grid_constant__ BalanceArgs a) {
   using L = Lanes<LPT, V, VEC>;
   constexpr int WIDE = LPT * V * 4;  // experts the lanes have room for
@@ -517,7 +517,7 @@ struct RouterBwdArgs {
 // one sequence, whose counts its lanes hold; the gate's terms of a token meet
 // the others through a row of shared memory.
 template <int LPT, int V, bool VEC>
-__global__ void __launch_bounds__(RT_THREADS)
+__global__ void __launch_bounds__(RT_THREADS, V <= 4 ? 4 : 2)
 router_bwd_kernel(const __grid_constant__ RouterBwdArgs a) {
   using L = Lanes<LPT, V, VEC>;
   constexpr int WIDE = LPT * V * 4;
@@ -653,11 +653,12 @@ auto by_experts(int E, F&& f) {
   return vec(Int<32>{}, Int<8>{});
 }
 
-// Items of a sequence: about RT_ITEMS CTAs in all, each with work for its warps.
+// Items of a sequence: one wave of CTAs in all where S allows it, each with work
+// for its warps.
 template <bool FORWARD>
 void cut_tokens(int E, int per, int S, int* sub, int* chunk) {
   const int tokens = by_experts<FORWARD>(E, [](auto lpt, auto, auto) { return RT_WARPS * 32 / decltype(lpt)::value; });
-  *sub = std::max(1, std::min((RT_ITEMS + S - 1) / S, (per + tokens - 1) / tokens));
+  *sub = std::max(1, std::min((FORWARD ? RT_FWD_CTAS : RT_BWD_CTAS) / S, (per + tokens - 1) / tokens));
   *chunk = (per + *sub - 1) / *sub;
   *sub = (per + *chunk - 1) / *chunk;
 }
