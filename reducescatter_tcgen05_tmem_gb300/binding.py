@@ -164,11 +164,9 @@ _OPT_FIELDS = frozenset(name for name, _ in flux_opts_t._fields_)
 
 # ---------------------------------------------------------------- marshalling
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
-    return x.data_ptr()
+    return x.data_ptr() if hasattr(x, "data_ptr") else int(x)
 
 
 _PTRS = {}  # ctypes array types by length

@@ -34,7 +34,7 @@ namespace flux {
 namespace {
 
 constexpr int RT_WARPS = 8, RT_THREADS = RT_WARPS * 32;
-constexpr int RT_FWD_CTAS = 3 * 152, RT_BWD_CTAS = 4 * 152;  // at most this many: one wave
+constexpr int RT_FWD_CTAS = 3 * 152, RT_BWD_CTAS = 5 * 152;  // at most this many: one wave
 // the items of a lone sequence, and their sums, that its last CTA joins; more are
 // joined by a second kernel
 constexpr int RT_HERE_ITEMS = 64, RT_HERE_SUMS = 2048;
@@ -517,7 +517,7 @@ struct RouterBwdArgs {
 // one sequence, whose counts its lanes hold; the gate's terms of a token meet
 // the others through a row of shared memory.
 template <int LPT, int V, bool VEC>
-__global__ void __launch_bounds__(RT_THREADS, V <= 4 ? 4 : 2)
+__global__ void __launch_bounds__(RT_THREADS, V <= 2 ? 5 : 2)
 router_bwd_kernel(const __grid_constant__ RouterBwdArgs a) {
   using L = Lanes<LPT, V, VEC>;
   constexpr int WIDE = LPT * V * 4;

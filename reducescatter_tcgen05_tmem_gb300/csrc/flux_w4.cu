@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
   }
 }
 
-constexpr int W4_JOIN_THREADS = 128;
+constexpr int W4_JOIN_WARPS = 8;
 
 // Sums of one slot's columns n .. n + 3 in the workspace, left zero there.
 template <int MT>
@@ -515,48 +515,51 @@ struct W4Parts {
 };
 
 // The second half of a product: adds the parts of cut tiles in CTA order, for
-// layer1 the tokens' slots in slot order, and writes zeros for slots of no
-// expert.  Four columns of one row of the output per thread.  Leaves what it
-// reads of the workspace zero.
+// layer1 the tokens' slots, and writes zeros for slots of no expert.  Four
+// columns of one row of the output per thread; layer1: a warp for each of up to
+// W4_JOIN_WARPS slots of the token, which meet in shared memory (slots one after
+// the other in one thread took twice the time).  Leaves what it reads of the
+// workspace zero.
 template <int DT, int MT, bool LAYER1>
-__global__ void __launch_bounds__(W4_JOIN_THREADS) w4_join_kernel(const __grid_constant__ W4Args a) {
+__global__ void __launch_bounds__(W4_JOIN_WARPS * 32) w4_join_kernel(const __grid_constant__ W4Args a) {
   wait_for_primary();
-  const int n = (blockIdx.x * W4_JOIN_THREADS + threadIdx.x) * 4, row = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int n = (LAYER1 ? blockIdx.x * 32 + lane : blockIdx.x * blockDim.x + threadIdx.x) * 4, row = blockIdx.y;
   const int col_tiles = (a.N + W4_COLS - 1) / W4_COLS, ct = n / W4_COLS;
   W4Parts<MT> p{a, a.mode == W4_DENSE ? a.dense_split : *a.split, col_tiles, ct, n - ct * W4_COLS, 0, 0, 0, 0};
-  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float4 sum = zero;
   bool write = n < a.N;
   if constexpr (LAYER1) {
-    // four slots at a time, the first load of each in flight together
-    constexpr int SLOTS = 4;
-    for (int j0 = 0; j0 < a.topk && write; j0 += SLOTS) {
-      float4 f[SLOTS];
-      W4Slot at[SLOTS];
-      float w[SLOTS];
-#pragma unroll
-      for (int j = 0; j < SLOTS; ++j) {
-        const int slot = row * a.topk + j0 + j;
-        at[j] = j0 + j < a.topk ? a.where[slot] : W4Slot{W4_NONE, 0};
-        w[j] = at[j].tile != W4_NONE ? a.weights[slot] : 0.0f;
+    __shared__ float4 meet[W4_JOIN_WARPS][32];
+    for (int j = warp; j < a.topk && write; j += warps) {
+      const int slot = row * a.topk + j;
+      const W4Slot at = a.where[slot];
+      const float w = a.weights[slot];
+      if (at.tile == W4_NONE) continue;
+      float4 f = zero;
+      if (p.open(at)) {
+        p.template add<4>(p.c0, f);
+      } else {
+        float4* from = reinterpret_cast<float4*>(a.rows_f32 + static_cast<size_t>(slot) * a.N + n);
+        f = *from;
+        *from = zero;
       }
-#pragma unroll
-      for (int j = 0; j < SLOTS; ++j) {
-        f[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (at[j].tile == W4_NONE) continue;
-        f[j] = p.open(at[j]) ? *p.part(p.c0)
-                             : *reinterpret_cast<const float4*>(a.rows_f32 + static_cast<size_t>(row * a.topk + j0 + j) * a.N + n);
-      }
-#pragma unroll
-      for (int j = 0; j < SLOTS; ++j) {
-        if (at[j].tile == W4_NONE) continue;
-        const bool cut = p.open(at[j]);
-        float4* from = cut ? p.part(p.c0) : reinterpret_cast<float4*>(a.rows_f32 + static_cast<size_t>(row * a.topk + j0 + j) * a.N + n);
-        *from = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (cut) p.template add<2>(p.c0 + 1, f[j]);
-        sum.x += w[j] * f[j].x;
-        sum.y += w[j] * f[j].y;
-        sum.z += w[j] * f[j].z;
-        sum.w += w[j] * f[j].w;
+      sum.x += w * f.x;
+      sum.y += w * f.y;
+      sum.z += w * f.z;
+      sum.w += w * f.w;
+    }
+    meet[warp][lane] = sum;
+    __syncthreads();
+    write = write && warp == 0;
+    if (write) {
+      for (int w = 1; w < warps; ++w) {
+        const float4 f = meet[w][lane];
+        sum.x += f.x;
+        sum.y += f.y;
+        sum.z += f.z;
+        sum.w += f.w;
       }
     }
   } else if (write) {
@@ -579,7 +582,7 @@ __global__ void __launch_bounds__(W4_JOIN_THREADS) w4_join_kernel(const __grid_c
   }
   __syncthreads();
   if (last == 0) return;
-  for (int i = threadIdx.x; i < a.slots; i += W4_JOIN_THREADS) a.where[i] = W4Slot{0, 0};
+  for (int i = threadIdx.x; i < a.slots; i += blockDim.x) a.where[i] = W4Slot{0, 0};
   if (threadIdx.x == 0) {
     *a.split = W4Split{0, 0};
     *a.joined = 0u;
@@ -669,8 +672,10 @@ flux_status_t w4_launch(W4Args a, const DeviceInfo& dev, cudaStream_t s) {
   // no tile is cut if the CTAs' stretches are whole tiles
   if (a.mode == W4_DENSE && units % grid == 0 && units / grid % a.runs == 0) return FLUX_OK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.N + 4 * W4_JOIN_THREADS - 1) / (4 * W4_JOIN_THREADS), a.mode == W4_LAYER1 ? a.T : a.slots, 1);
-  cfg.blockDim = dim3(W4_JOIN_THREADS, 1, 1);
+  const int join_warps = a.mode == W4_LAYER1 ? std::min(a.topk, W4_JOIN_WARPS) : 4;
+  const int join_cols = a.mode == W4_LAYER1 ? 128 : join_warps * 128;
+  cfg.gridDim = dim3((a.N + join_cols - 1) / join_cols, a.mode == W4_LAYER1 ? a.T : a.slots, 1);
+  cfg.blockDim = dim3(join_warps * 32, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr_pdl[1];
   attr_pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
