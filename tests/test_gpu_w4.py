@@ -236,7 +236,7 @@ def test_infinities_and_nan_stay_in_their_rows_and_columns():
     assert bool(out[4].isnan().all()) and not bool(out[rows][:, 33].isfinite().any())
 
 
-@pytest.mark.parametrize("E,K,N,group,dtype", [(1, 128, 16, 32, "bf16"), (2, 200, 24, 64, "f16"), (3, 520, 136, 128, "bf16"),
+@pytest.mark.parametrize("E,K,N,group,dtype", [(1, 128, 16, 32, "bf16"), (2, 200, 24, 64, "f16"), (3, 520, 136, 128, "bf16"), (2, 264, 16, 96, "f16"),
                                                (1, 1000, 8, 1024, "f16")])
 def test_quantize(E, K, N, group, dtype):
     raw = gen.normal16((51, 1), (E, K, N), 0.02, dtype)
