@@ -16,7 +16,7 @@ the router scores (flux_moe_router_bwd).
 Decoding: the same block for a few tokens with 4-bit experts
 (flux_w4_quantize once, then flux_moe_w4_layer0 / flux_moe_w4_layer1).
 
-    python -m reducescatter_tcgen05_tmem_gb300.build && python examples/moe_block.py
+    python -c "import __graft_entry__ as g; g.build()" && python examples/moe_block.py
 """
 from __future__ import annotations
 

@@ -93,6 +93,7 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
   __shared__ alignas(16) float red[TEAMS][2 * W];
   const int team = threadIdx.x / TT, lane = threadIdx.x % TT, wit = lane / 32;
   int turn = 0;
+  wait_for_previous();
   const float rho = a.res_scale != nullptr ? __ldg(a.res_scale) : 1.0f;
   const float inv_h = 1.0f / static_cast<float>(a.H);
   const int step = gridDim.x * TEAMS;
@@ -267,6 +268,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
   __shared__ double sums[TEAMS];
   const int team = threadIdx.x / TT, lane = threadIdx.x % TT, wit = lane / 32;
   int turn1 = 0, turn2 = 0;
+  wait_for_previous();
   const float rho = a.res_scale != nullptr ? __ldg(a.res_scale) : 1.0f;
   const float inv_h = 1.0f / static_cast<float>(a.H);
   const bool row_gate = a.gate != nullptr && a.gate_cols == 1;
@@ -457,7 +459,6 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
   };
   float* my_post = a.part_post + static_cast<size_t>(blockIdx.x) * a.H;
   float* my_pre = a.part_pre + static_cast<size_t>(blockIdx.x) * a.H;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // block_norm_sums_kernel waits for all of this
   const f32x2 rho2 = both(rho);
 
   // slots that no copy fills hold zeros: columns past H, a gradient not given
@@ -650,7 +651,7 @@ template <int DT>
 __global__ void __launch_bounds__(SUM_THREADS)
 block_norm_sums_kernel(const __grid_constant__ BlockNormArgs a, int col_blocks, int per_run_blocks) {
   __shared__ float part[SUM_WARPS][SUM_COLS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   const int lane = threadIdx.x % SUM_COLS, warp = threadIdx.x / SUM_COLS;
   const bool one_row = a.gate != nullptr && a.gate_cols != 1 && a.gate_per == a.T;
   if (blockIdx.x < 2 * col_blocks) {
@@ -871,8 +872,7 @@ flux_status_t launch_fwd_form(const BlockNormArgs& a, const DeviceInfo& dev, cud
   std::call_once(once, [] { attr = allow_smem(kernel, S::SMEM); });
   if (attr != cudaSuccess) return cuda_fail(attr);
   const int grid = std::min((a.T + Team<W>::COUNT - 1) / Team<W>::COUNT, dev.sm_count * S::CTAS);
-  kernel<<<grid, Team<W>::CTA, S::SMEM, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(kernel, dim3(grid), Team<W>::CTA, S::SMEM, s, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
@@ -892,8 +892,7 @@ flux_status_t launch_bwd_form(const BlockNormArgs& a, const BwdPlan& p, cudaStre
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] { attr = allow_smem(kernel, smem); });
   if (attr != cudaSuccess) return cuda_fail(attr);
-  kernel<<<p.ctas, Team<W>::CTA, smem, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(kernel, dim3(p.ctas), Team<W>::CTA, smem, s, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
@@ -907,16 +906,7 @@ flux_status_t launch_bwd(const BlockNormArgs& a, const BwdPlan& p, cudaStream_t 
   if (st != FLUX_OK) return st;
   const int cols = sum_blocks(a.H), per_run = a.gate_cols == 1 ? 1 : run_blocks(a.H);
   const int cut = p.cut_runs && a.dgate != nullptr ? (p.ctas - 1) * per_run : 0;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * cols + 1 + cut, 1, 1);
-  cfg.blockDim = dim3(SUM_THREADS, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, block_norm_sums_kernel<DT>, a, cols, per_run);
+  const cudaError_t e = launch_behind(block_norm_sums_kernel<DT>, dim3(2 * cols + 1 + cut), SUM_THREADS, 0, s, a, cols, per_run);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 

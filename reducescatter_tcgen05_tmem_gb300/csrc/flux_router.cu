@@ -210,7 +210,7 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT, tg = lane / LPT;
   const int item = blockIdx.x, seq = item / a.sub, E = a.E;
   const int t0 = seq * a.per + (item - seq * a.sub) * a.chunk, t1 = min(t0 + a.chunk, (seq + 1) * a.per);
-  if (a.cols > 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_previous();
   for (int e = threadIdx.x; e < WIDE; e += RT_THREADS) cnt[e] = 0;
   __syncthreads();
   float sums[V][4] = {};
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) balance_join_kernel(const __grid
   __shared__ int cnt_w[ROWS][COLS];
   __shared__ float red[JOIN_THREADS / 32 * 3];
   __shared__ int kept, flag;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = threadIdx.x % COLS, row = threadIdx.x / COLS;
   const int seq = blockIdx.y, i0 = seq * a.sub, e = blockIdx.x * COLS + col;
@@ -526,6 +526,7 @@ router_bwd_kernel(const __grid_constant__ RouterBwdArgs a) {
   const int item = blockIdx.x, seq = item / a.sub, E = a.E;
   const int t0 = seq * a.per + (item - seq * a.sub) * a.chunk, t1 = min(t0 + a.chunk, (seq + 1) * a.per);
   float* g = gate[warp * L::TPW + tg];
+  wait_for_previous();
   const bool gates = a.dweights != nullptr;
   if (gates)
     for (int e = l; e < WIDE; e += LPT) g[e] = 0.0f;
@@ -757,21 +758,11 @@ extern "C" flux_status_t flux_moe_balance_loss(int T, int E, int topk, int seqs,
   a.balance_scale = static_cast<float>(static_cast<double>(balance_coef) * E / (static_cast<double>(topk) * seqs));
   a.z_coef = z_coef;
   by_experts<true>(E, [&](auto lpt, auto v, auto vec) {
-    balance_kernel<decltype(lpt)::value, decltype(v)::value, decltype(vec)::value><<<p.items, RT_THREADS, 0, s>>>(a);
+    e = launch_behind(balance_kernel<decltype(lpt)::value, decltype(v)::value, decltype(vec)::value>, dim3(p.items), RT_THREADS, 0, s, a);
   });
-  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
+  if (e != cudaSuccess) return cuda_fail(e);
   if (p.cols == 0) return FLUX_OK;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.cols, seqs, 1);
-  cfg.blockDim = dim3(JOIN_THREADS, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = p.join_cols == 256 ? cudaLaunchKernelEx(&cfg, balance_join_kernel<256>, a)
-                         : cudaLaunchKernelEx(&cfg, balance_join_kernel<32>, a);
+  e = launch_behind(p.join_cols == 256 ? balance_join_kernel<256> : balance_join_kernel<32>, dim3(p.cols, seqs), JOIN_THREADS, 0, s, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
@@ -811,9 +802,9 @@ extern "C" flux_status_t flux_moe_router_bwd(int T, int E, int topk, int seqs, f
   cut_tokens<false>(E, a.per, seqs, &a.sub, &a.chunk);
   a.balance_coef = balance_coef;
   a.z_coef = z_coef;
+  cudaError_t e = cudaSuccess;
   by_experts<false>(E, [&](auto lpt, auto v, auto vec) {
-    router_bwd_kernel<decltype(lpt)::value, decltype(v)::value, decltype(vec)::value><<<a.sub * seqs, RT_THREADS, 0, s>>>(a);
+    e = launch_behind(router_bwd_kernel<decltype(lpt)::value, decltype(v)::value, decltype(vec)::value>, dim3(a.sub * seqs), RT_THREADS, 0, s, a);
   });
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }

@@ -74,11 +74,6 @@ struct W4RowTile {
 };
 
 // d (+)= 16 x 16 . 16 x 8; A four and B two registers of two 16-bit values.
-// A kernel launched behind this one may start; and, in that kernel, the wait for
-// everything this one has written.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 template <int DT, bool FROM_ZERO>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                             uint32_t b1) {
@@ -203,6 +198,7 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
   __shared__ int scan[2][W4_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int col_tiles = (a.N + W4_COLS - 1) / W4_COLS;
+  wait_for_previous();
   int row_tiles;
   if (a.mode == W4_DENSE) {
     row_tiles = (a.slots + MT * 8 - 1) / (MT * 8);
@@ -297,7 +293,6 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
   const int units = row_tiles * col_tiles * a.runs;
   // every CTA that works has a unit: the arrivals at a cut tile are counted by CTA
   const int ctas = min(static_cast<int>(gridDim.x), units), me = blockIdx.x;
-  launch_dependents();
   if (me >= ctas) return;
   const W4Split split{units / ctas, units % ctas};
   if (me == 0 && tid == 0 && a.mode != W4_DENSE) *a.split = split;
@@ -522,7 +517,7 @@ struct W4Parts {
 // workspace zero.
 template <int DT, int MT, bool LAYER1>
 __global__ void __launch_bounds__(W4_JOIN_WARPS * 32) w4_join_kernel(const __grid_constant__ W4Args a) {
-  wait_for_primary();
+  wait_for_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int n = (LAYER1 ? blockIdx.x * 32 + lane : blockIdx.x * blockDim.x + threadIdx.x) * 4, row = blockIdx.y;
   const int col_tiles = (a.N + W4_COLS - 1) / W4_COLS, ct = n / W4_COLS;
@@ -666,24 +661,14 @@ flux_status_t w4_launch(W4Args a, const DeviceInfo& dev, cudaStream_t s) {
   const long long fill = std::min(W4Shape<MT, SR>::CTAS * dev.sm_count, W4_MAX_CTAS);
   const int grid = static_cast<int>(std::min(units, std::max(std::min(fill, units / W4_MIN_UNITS), std::min<long long>(fill, dev.sm_count))));
   a.dense_split = W4Split{static_cast<int>(units / grid), static_cast<int>(units % grid)};
-  w4_kernel<DT, MT, SR><<<grid, W4_THREADS, smem, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_behind(w4_kernel<DT, MT, SR>, dim3(grid), W4_THREADS, smem, s, a);
   if (e != cudaSuccess) return cuda_fail(e);
   // no tile is cut if the CTAs' stretches are whole tiles
   if (a.mode == W4_DENSE && units % grid == 0 && units / grid % a.runs == 0) return FLUX_OK;
-  cudaLaunchConfig_t cfg = {};
   const int join_warps = a.mode == W4_LAYER1 ? std::min(a.topk, W4_JOIN_WARPS) : 4;
   const int join_cols = a.mode == W4_LAYER1 ? 128 : join_warps * 128;
-  cfg.gridDim = dim3((a.N + join_cols - 1) / join_cols, a.mode == W4_LAYER1 ? a.T : a.slots, 1);
-  cfg.blockDim = dim3(join_warps * 32, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr_pdl[1];
-  attr_pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr_pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr_pdl;
-  cfg.numAttrs = 1;
-  e = a.mode == W4_LAYER1 ? cudaLaunchKernelEx(&cfg, w4_join_kernel<DT, MT, true>, a)
-                          : cudaLaunchKernelEx(&cfg, w4_join_kernel<DT, MT, false>, a);
+  e = launch_behind(a.mode == W4_LAYER1 ? w4_join_kernel<DT, MT, true> : w4_join_kernel<DT, MT, false>,
+                    dim3((a.N + join_cols - 1) / join_cols, a.mode == W4_LAYER1 ? a.T : a.slots), join_warps * 32, 0, s, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
