@@ -25,19 +25,19 @@ constexpr int W4_RUN = 128;  // inputs per run of 64 bytes
 
 enum W4Mode { W4_DENSE = 0, W4_LAYER0 = 1, W4_LAYER1 = 2 };
 
-constexpr int W4_WARPS = 4, W4_THREADS = W4_WARPS * 32;
+constexpr int W4_WARPS = 4, W4_THREADS = W4_WARPS * 32;  // of a team
 constexpr int W4_CA = 2;                         // A operands (16 columns each) of a warp
 constexpr int W4_COLS = W4_WARPS * 16 * W4_CA;   // columns of a tile
 constexpr int W4_MIN_UNITS = 4;
-constexpr int W4_MAX_CTAS = 5 * 160;             // at most five CTAs per SM
+constexpr int W4_MAX_TEAMS = 4 * 160;            // at most four per SM
 constexpr int W4_RUN_BYTES = W4_RUN / 2;
 constexpr int W4_NONE = 0xFFFF;                  // row tile of a slot whose expert id is out of range
 
-// Equal stretches of units: CTA i has the units [first(i), first(i + 1)).
+// Equal stretches of units: team i has the units [first(i), first(i + 1)).
 struct W4Split {
-  int each, more;  // the first `more` CTAs have one unit more
-  __device__ __forceinline__ int first(int cta) const { return cta * each + min(cta, more); }
-  __device__ __forceinline__ int cta_of(int unit) const {
+  int each, more;  // the first `more` teams have one unit more
+  __device__ __forceinline__ int first(int team) const { return team * each + min(team, more); }
+  __device__ __forceinline__ int team_of(int unit) const {
     const int big = more * (each + 1);
     return unit < big ? unit / (each + 1) : more + (unit - big) / each;
   }
@@ -62,10 +62,10 @@ struct W4Args {
   W4Split* split;
   W4Slot* where;        // [slots]
   uint32_t* joined;     // blocks of the joining kernel that are done with those
-  float* parts;         // [2 grid] sums of cut tiles: of each CTA's first and last
+  float* parts;         // [2 teams] sums of cut tiles: of each team's first and last
   float* rows_f32;      // layer1: [slots x N]
   int slots;            // rows of x . W: M, or T topk
-  int T, N, K, runs, group, groups, E, topk, mode;
+  int T, N, K, runs, group, groups, E, topk, mode, teams;
 };
 
 // Rows of one expert that one tile multiplies.
@@ -159,7 +159,15 @@ __device__ __forceinline__ void copy16_or_zero(void* smem, const void* gmem, boo
 // MT tiles of 8 rows; SR scales per run and column (a group of 128 or a multiple: 1, of 64: 2, else 4).
 template <int MT, int SR>
 struct W4Shape {
-  static constexpr int CTAS = MT == 4 ? 2 : MT == 2 ? 3 : 4;                  // per SM
+  // Warps of a scheduler come forward by age: of an SM's four CTAs of one team the
+  // first is done with its stretch after 25 us and the last after 36.  In a CTA of
+  // four teams whose four warps have four different ages all end within 3 us (layer1
+  // of 24 tokens, 6 of 64 experts, 1792 x 4096: 69 -> 66 us; one row of 4096 x 4096
+  // 8.9 -> 8.3).  Three teams that way are slower than three CTAs (13 rows of
+  // 28672 x 8192: 39.0 us, 37.4).
+  static constexpr int TEAMS = MT == 1 ? 4 : 1;                  // of a CTA
+  static constexpr int CTAS = MT == 4 ? 2 : MT == 2 ? 3 : 1;     // per SM
+  static constexpr int THREADS = TEAMS * W4_THREADS;
   static constexpr int AHEAD = 2;                               // runs of codes that a thread has on the way
   static constexpr int CHUNK = MT == 1 ? 6 : MT == 2 ? 4 : 2;   // runs whose rows of x and scales make one buffer
   static_assert(CHUNK % AHEAD == 0, "the words on the way keep their places from one buffer to the next");
@@ -172,47 +180,48 @@ struct W4Shape {
 
 // out = x . W for few rows.  The work is units of one tile of 128 columns, up
 // to 8 MT rows of one expert, and one run of 128 inputs; unit ids count the
-// runs of a tile, then the column tiles, then the row tiles, and every CTA
-// takes an equal stretch of them, so a tile may be cut between CTAs.
+// runs of a tile, then the column tiles, then the row tiles, and every team of
+// four warps takes an equal stretch of them, so a tile may be cut between teams.
 //
 // A warp multiplies 32 columns: the codes are two A operands of 16 x 8 x 16
 // tensor instructions, the rows of x the B operand (a matrix-vector product
 // leaves 7 of its 8 columns idle, which costs nothing: the kernel is bound by
 // the bytes of the codes and by the instructions that unpack them).  Every
 // thread loads the words that it will unpack itself, AHEAD runs ahead; rows of
-// x and scales are shared by the CTA, in two buffers of CHUNK runs, one filled
+// x and scales are shared by the team, in two buffers of CHUNK runs, one filled
 // while the other is used.
 //
 // The sums of a group are exact products in fp32, then scaled into the tile's
-// sums.  CTAs that share a tile leave their sums in the workspace, where
-// w4_join_kernel adds them in CTA order: repeat calls give the same bits.
+// sums.  Teams that share a tile leave their sums in the workspace, where
+// w4_join_kernel adds them in team order: repeat calls give the same bits.
 template <int DT, int MT, int SR>
-__global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel(const __grid_constant__ W4Args a) {
+__global__ void __launch_bounds__((W4Shape<MT, SR>::THREADS), (W4Shape<MT, SR>::CTAS)) w4_kernel(const __grid_constant__ W4Args a) {
   using S = W4Shape<MT, SR>;
-  extern __shared__ __align__(128) uint8_t ring[];
+  extern __shared__ __align__(128) uint8_t rings[];
   __shared__ uint16_t order[FLUX_W4_MAX_ROWS];       // slots by expert
   __shared__ W4RowTile tiles[FLUX_W4_MAX_ROWS];
-  int* hist = reinterpret_cast<int*>(ring);  // before the ring is used, as
+  int* hist = reinterpret_cast<int*>(rings);  // before the rings are used, as
   int* slot_expert = hist + FLUX_MAX_EXPERTS;
-  static_assert(S::SMEM >= 4 * (FLUX_MAX_EXPERTS + FLUX_W4_MAX_ROWS), "the ring holds the routing first");
-  __shared__ int scan[2][W4_WARPS];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  static_assert(S::TEAMS * S::SMEM >= 4 * (FLUX_MAX_EXPERTS + FLUX_W4_MAX_ROWS), "the rings hold the routing first");
+  constexpr int WARPS = S::THREADS / 32;
+  __shared__ int scan[2][WARPS];
+  const int thread = threadIdx.x, lane = thread & 31, cta_warp = thread >> 5;
   const int col_tiles = (a.N + W4_COLS - 1) / W4_COLS;
   wait_for_previous();
   int row_tiles;
   if (a.mode == W4_DENSE) {
     row_tiles = (a.slots + MT * 8 - 1) / (MT * 8);
-    for (int i = tid; i < row_tiles; i += W4_THREADS)
+    for (int i = thread; i < row_tiles; i += S::THREADS)
       tiles[i] = W4RowTile{0, static_cast<uint16_t>(i * MT * 8), static_cast<uint16_t>(min(MT * 8, a.slots - i * MT * 8))};
-    for (int i = tid; i < a.slots; i += W4_THREADS) order[i] = static_cast<uint16_t>(i);
+    for (int i = thread; i < a.slots; i += S::THREADS) order[i] = static_cast<uint16_t>(i);
     __syncthreads();
   } else {
-    // stable counting sort of the slots by expert: CTAs that share a tile have to
+    // stable counting sort of the slots by expert: teams that share a tile have to
     // agree on the order of its rows
-    for (int e = tid; e < a.E; e += W4_THREADS) hist[e] = 0;
+    for (int e = thread; e < a.E; e += S::THREADS) hist[e] = 0;
     __syncthreads();
     bool bad = false;
-    for (int i = tid; i < a.slots; i += W4_THREADS) {
+    for (int i = thread; i < a.slots; i += S::THREADS) {
       int e = a.ids[i];
       if (e >= 0 && e < a.E) {
         atomicAdd(&hist[e], 1);
@@ -225,10 +234,10 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
     if (bad) atomicCAS(a.hdr, 0u, static_cast<uint32_t>(FLUX_ERR_INVALID_ARG));
     __syncthreads();
     // exclusive sums of slots and row tiles over the experts
-    constexpr int PER = FLUX_MAX_EXPERTS / W4_THREADS;
+    constexpr int PER = (FLUX_MAX_EXPERTS + S::THREADS - 1) / S::THREADS;
     int slots = 0, rt = 0;
     for (int k = 0; k < PER; ++k) {
-      const int e = tid * PER + k, n = e < a.E ? hist[e] : 0;
+      const int e = thread * PER + k, n = e < a.E ? hist[e] : 0;
       slots += n;
       rt += (n + MT * 8 - 1) / (MT * 8);
     }
@@ -242,23 +251,23 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
       }
     }
     if (lane == 31) {
-      scan[0][warp] = s0;
-      scan[1][warp] = r0;
+      scan[0][cta_warp] = s0;
+      scan[1][cta_warp] = r0;
     }
     __syncthreads();
     s0 -= slots;
     r0 -= rt;
     row_tiles = 0;
 #pragma unroll
-    for (int w = 0; w < W4_WARPS; ++w) {
-      if (w < warp) {
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < cta_warp) {
         s0 += scan[0][w];
         r0 += scan[1][w];
       }
       row_tiles += scan[1][w];
     }
     for (int k = 0; k < PER; ++k) {
-      const int e = tid * PER + k, n = e < a.E ? hist[e] : 0;
+      const int e = thread * PER + k, n = e < a.E ? hist[e] : 0;
       if (e < a.E) hist[e] = s0;
       for (int m = 0; m < n; m += MT * 8)
         tiles[r0++] = W4RowTile{static_cast<uint16_t>(e), static_cast<uint16_t>(s0 + m),
@@ -266,7 +275,7 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
       s0 += n;
     }
     __syncthreads();
-    if (warp == 0) {
+    if (cta_warp == 0) {
       for (int i0 = 0; i0 < a.slots; i0 += 32) {
         const int i = i0 + lane, e = i < a.slots ? slot_expert[i] : -1;
         const bool in = e >= 0;
@@ -284,17 +293,21 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
     }
     __syncthreads();
     if (blockIdx.x == 0) {
-      for (int r = warp; r < row_tiles; r += W4_WARPS)
+      for (int r = cta_warp; r < row_tiles; r += WARPS)
         for (int m = lane; m < tiles[r].rows; m += 32)
           a.where[order[tiles[r].first + m]] = W4Slot{static_cast<uint16_t>(r), static_cast<uint16_t>(m)};
     }
   }
 
+  // a team: one warp of each of the four schedulers, each of another age there
+  const int warp = cta_warp % W4_WARPS, team = (cta_warp / W4_WARPS + warp) % S::TEAMS, tid = warp * 32 + lane,
+            g = lane >> 2, c = lane & 3;
+  uint8_t* const ring = rings + team * S::SMEM;
   const int units = row_tiles * col_tiles * a.runs;
-  // every CTA that works has a unit: the arrivals at a cut tile are counted by CTA
-  const int ctas = min(static_cast<int>(gridDim.x), units), me = blockIdx.x;
-  if (me >= ctas) return;
-  const W4Split split{units / ctas, units % ctas};
+  // every team that works has a unit
+  const int teams = min(a.teams, units), me = team * gridDim.x + blockIdx.x;
+  if (me >= teams) return;
+  const W4Split split{units / teams, units % teams};
   if (me == 0 && tid == 0 && a.mode != W4_DENSE) *a.split = split;
   const int u0 = split.first(me), n_units = split.first(me + 1) - u0;
   int tile = u0 / a.runs, run = u0 - tile * a.runs;
@@ -420,7 +433,7 @@ __global__ void __launch_bounds__(W4_THREADS, (W4Shape<MT, SR>::CTAS)) w4_kernel
     for (int r0 = 0; r0 < n_runs; r0 += S::CHUNK) {
       const int n = min(S::CHUNK, n_runs - r0);
       copy_wait<0>();
-      __syncthreads();  // this buffer is filled, the other one has been read
+      team_sync<W4_WARPS>(team);  // this buffer is filled, the other one has been read
       if (r0 + n < n_runs) stage(ring + (buffer ^ 1) * S::BUFFER, tile, run + r0 + n, min(S::CHUNK, n_runs - r0 - n));
       else if (next_runs > 0) stage(ring + (buffer ^ 1) * S::BUFFER, tile + 1, 0, min(S::CHUNK, next_runs));
       copy_commit();
@@ -477,19 +490,19 @@ struct W4Parts {
   int col_tiles, ct, col;
   int unit, row, c0, c1;  // of the slot
 
-  // whether several CTAs have sums of the slot's tile
+  // whether several teams have sums of the slot's tile
   __device__ __forceinline__ bool open(W4Slot at) {
     unit = (at.tile * col_tiles + ct) * a.runs;
     row = at.row;
-    c0 = split.cta_of(unit);
-    c1 = split.cta_of(unit + a.runs - 1);
+    c0 = split.team_of(unit);
+    c1 = split.team_of(unit + a.runs - 1);
     return c0 != c1;
   }
   __device__ __forceinline__ float4* part(int k) const {
-    // the tile is the first of CTA k unless it begins inside its stretch
+    // the tile is the first of team k unless it begins inside its stretch
     return reinterpret_cast<float4*>(a.parts + static_cast<size_t>(2 * k + (split.first(k) >= unit ? 0 : 1)) * PART + row * W4_COLS + col);
   }
-  // adds the parts of the CTAs from `first` on, BATCH loads in flight together
+  // adds the parts of the teams from `first` on, BATCH loads in flight together
   template <int BATCH>
   __device__ __forceinline__ void add(int first, float4& v) const {
     for (int k0 = first; k0 <= c1; k0 += BATCH) {
@@ -509,7 +522,7 @@ struct W4Parts {
   }
 };
 
-// The second half of a product: adds the parts of cut tiles in CTA order, for
+// The second half of a product: adds the parts of cut tiles in team order, for
 // layer1 the tokens' slots, and writes zeros for slots of no expert.  Four
 // columns of one row of the output per thread; layer1: a warp for each of up to
 // W4_JOIN_WARPS slots of the token, which meet in shared memory (slots one after
@@ -638,7 +651,7 @@ W4Ws w4_ws(int slots, int N) {
   };
   w.split = take(sizeof(W4Split));
   w.where = take(sizeof(W4Slot) * slots);
-  w.parts = take(sizeof(float) * 2 * W4_MAX_CTAS * W4_COLS * 8 * w4_row_tiles_of_8(slots));
+  w.parts = take(sizeof(float) * 2 * W4_MAX_TEAMS * W4_COLS * 8 * w4_row_tiles_of_8(slots));
   w.rows = take(sizeof(float) * slots * static_cast<size_t>(N));
   w.total = at;
   return w;
@@ -646,25 +659,26 @@ W4Ws w4_ws(int slots, int N) {
 
 template <int DT, int MT, int SR>
 flux_status_t w4_launch(W4Args a, const DeviceInfo& dev, cudaStream_t s) {
-  constexpr int smem = W4Shape<MT, SR>::SMEM;
+  using S = W4Shape<MT, SR>;
+  constexpr int smem = S::TEAMS * S::SMEM;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
     attr = cudaFuncSetAttribute(w4_kernel<DT, MT, SR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (attr != cudaSuccess) return cuda_fail(attr);
-  // no more CTAs than units (of as many row tiles as the slots can make)
+  // no more teams than units (of as many row tiles as the slots can make)
   const long long col_tiles = (a.N + W4_COLS - 1) / W4_COLS;
   const long long row_tiles = a.mode == W4_DENSE ? (a.slots + MT * 8 - 1) / (MT * 8) : a.slots;
   const long long units = row_tiles * col_tiles * a.runs;
   if (units > INT_MAX) return FLUX_ERR_UNSUPPORTED;
-  const long long fill = std::min(W4Shape<MT, SR>::CTAS * dev.sm_count, W4_MAX_CTAS);
-  const int grid = static_cast<int>(std::min(units, std::max(std::min(fill, units / W4_MIN_UNITS), std::min<long long>(fill, dev.sm_count))));
-  a.dense_split = W4Split{static_cast<int>(units / grid), static_cast<int>(units % grid)};
-  cudaError_t e = launch_behind(w4_kernel<DT, MT, SR>, dim3(grid), W4_THREADS, smem, s, a);
+  const long long sms = std::min(dev.sm_count, W4_MAX_TEAMS / 4), ctas = S::CTAS * sms, fill = S::TEAMS * ctas;
+  a.teams = static_cast<int>(std::min(units, std::max(std::min(fill, units / W4_MIN_UNITS), sms)));
+  a.dense_split = W4Split{static_cast<int>(units / a.teams), static_cast<int>(units % a.teams)};
+  cudaError_t e = launch_behind(w4_kernel<DT, MT, SR>, dim3(std::min<long long>(a.teams, ctas)), S::THREADS, smem, s, a);
   if (e != cudaSuccess) return cuda_fail(e);
-  // no tile is cut if the CTAs' stretches are whole tiles
-  if (a.mode == W4_DENSE && units % grid == 0 && units / grid % a.runs == 0) return FLUX_OK;
+  // no tile is cut if the teams' stretches are whole tiles
+  if (a.mode == W4_DENSE && units % a.teams == 0 && units / a.teams % a.runs == 0) return FLUX_OK;
   const int join_warps = a.mode == W4_LAYER1 ? std::min(a.topk, W4_JOIN_WARPS) : 4;
   const int join_cols = a.mode == W4_LAYER1 ? 128 : join_warps * 128;
   e = launch_behind(a.mode == W4_LAYER1 ? w4_join_kernel<DT, MT, true> : w4_join_kernel<DT, MT, false>,
