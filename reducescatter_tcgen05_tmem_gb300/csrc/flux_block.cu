@@ -28,7 +28,7 @@
 namespace flux {
 
 constexpr int BLOCK_MAX_H = FLUX_BLOCK_MAX_H;
-constexpr int BN_MAX_CTAS = 304;  // persistent backward grid: at most two CTAs on each of 152 SMs
+constexpr int BN_SMS = 152;  // the backward grid: one wave on them
 
 struct BlockNormArgs {
   const void* x[FLUX_MAX_RANKS];
@@ -56,11 +56,13 @@ struct BlockNormArgs {
 
 namespace {
 
-// A row is held by a team of W warps; a CTA has one to eight teams.
+// A row is held by a team of W warps; a CTA has one to eight teams.  Where a team
+// has three warps or more, CTAs of one team are faster than CTAs of several
+// (2^27 elements in rows of 1792: backward 278 us, two teams 339; forward 164, 212).
 template <int W>
 struct Team {
   static constexpr int THREADS = W * 32;
-  static constexpr int CTA = W <= 8 ? 256 : W * 32;
+  static constexpr int CTA = W <= 2 ? 256 : W * 32;
   static constexpr int COUNT = CTA / THREADS;
 };
 
@@ -82,7 +84,7 @@ struct FwdShape {
   static constexpr int ROW = Team<W>::CTA * V * 32;  // bytes of two tensors' rows, all teams of the CTA
   static constexpr int DEPTH = V == 4 ? 2 : 3;
   static constexpr int SMEM = ROW * DEPTH;
-  static constexpr int CTAS = W <= 8 ? 4 : V == 2 ? 2 : 1;  // per SM
+  static constexpr int CTAS = W == 3 ? 8 : W <= 8 ? 1024 / Team<W>::CTA : V == 2 ? 2 : 1;  // per SM
 };
 
 template <int DT, int W, int V, bool HAS_Y>
@@ -249,7 +251,9 @@ struct BwdShape {
   static constexpr int JOIN = Team<W>::COUNT > 1 ? Team<W>::CTA * V * 32 : 0;
   static constexpr int WEIGHTS = VECS > 1536 ? VECS * 48 : VECS > 1024 ? VECS * 16 : 0;  // gw in fp32, w_pre as stored
   static constexpr int SMEM = ROW * DEPTH + JOIN + WEIGHTS;
-  static constexpr int CTAS = W <= 8 ? 2 : 1;  // per SM
+  // per SM: with two vectors the registers of twelve warps, where eight more do not
+  // make up for the spills
+  static constexpr int CTAS = W > 8 ? 1 : W <= 2 || W == 8 ? 2 : 384 / Team<W>::CTA;
 };
 
 template <int DT, int W, int V, bool HAS_Y, bool HAS_U>
@@ -760,15 +764,25 @@ block_norm_sums_kernel(const __grid_constant__ BlockNormArgs a, int col_blocks, 
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// Calls f(W, V) for the team that holds a row of H columns.
-template <typename F>
-flux_status_t by_width(int H, F&& f) {
+// Calls f(W, V) for the team that holds a row of H columns.  The steps are close
+// enough that a third of the lanes idle at most (2^27 elements in rows of 5120:
+// backward 354 us, in teams of 16 warps 401; of 1280: 278, 4 warps 399; of 2560:
+// 287, 8 warps 373).  A warp with two vectors is fast enough forward but spills
+// backward (H 512: 456 us, two warps of one vector 266).
+template <bool BACKWARD, typename F>
+auto by_width(int H, F&& f) {
   const int nvec = H / 8;
   if (nvec <= 32) return f(Int<1>{}, Int<1>{});
-  if (nvec <= 64) return f(Int<1>{}, Int<2>{});
+  if (nvec <= 64) {
+    if constexpr (BACKWARD) return f(Int<2>{}, Int<1>{});
+    else return f(Int<1>{}, Int<2>{});
+  }
   if (nvec <= 128) return f(Int<2>{}, Int<2>{});
+  if (nvec <= 192) return f(Int<3>{}, Int<2>{});
   if (nvec <= 256) return f(Int<4>{}, Int<2>{});
+  if (nvec <= 384) return f(Int<6>{}, Int<2>{});
   if (nvec <= 512) return f(Int<8>{}, Int<2>{});
+  if (nvec <= 768) return f(Int<12>{}, Int<2>{});
   if (nvec <= 1024) return f(Int<16>{}, Int<2>{});
   if (nvec <= 1536) return f(Int<16>{}, Int<3>{});
   return f(Int<16>{}, Int<4>{});
@@ -783,9 +797,10 @@ struct BwdPlan {
 
 BwdPlan bwd_plan(int T, int H, int gate_rows, int gate_cols) {
   BwdPlan p{};
-  const int nvec = H / 8;
-  const int teams = nvec <= 64 ? 8 : nvec <= 128 ? 4 : nvec <= 256 ? 2 : 1;
-  p.ctas = std::min(nvec <= 512 ? BN_MAX_CTAS : BN_MAX_CTAS / 2, (T + teams - 1) / teams);
+  p.ctas = by_width<true>(H, [T](auto w, auto v) {
+    constexpr int W = decltype(w)::value, V = decltype(v)::value, TEAMS = Team<W>::COUNT;
+    return std::min(BwdShape<W, V>::CTAS * BN_SMS, (T + TEAMS - 1) / TEAMS);
+  });
   const int per = gate_rows > 0 ? T / gate_rows : T;
   const bool rows = gate_rows > 1 && gate_cols > 1, scalars = gate_cols == 1 && per > 1;
   p.cut_runs = rows || scalars;
@@ -878,7 +893,7 @@ flux_status_t launch_fwd_form(const BlockNormArgs& a, const DeviceInfo& dev, cud
 
 template <int DT>
 flux_status_t launch_fwd(const BlockNormArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  return by_width(a.H, [&](auto w, auto v) {
+  return by_width<false>(a.H, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
     return a.has_y ? launch_fwd_form<DT, W, V, true>(a, dev, s) : launch_fwd_form<DT, W, V, false>(a, dev, s);
   });
@@ -898,7 +913,7 @@ flux_status_t launch_bwd_form(const BlockNormArgs& a, const BwdPlan& p, cudaStre
 
 template <int DT>
 flux_status_t launch_bwd(const BlockNormArgs& a, const BwdPlan& p, cudaStream_t s) {
-  flux_status_t st = by_width(a.H, [&](auto w, auto v) {
+  flux_status_t st = by_width<true>(a.H, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
     if (!a.has_y) return launch_bwd_form<DT, W, V, false, true>(a, p, s);
     return a.has_u ? launch_bwd_form<DT, W, V, true, true>(a, p, s) : launch_bwd_form<DT, W, V, true, false>(a, p, s);
