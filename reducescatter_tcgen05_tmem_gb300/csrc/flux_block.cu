@@ -78,7 +78,8 @@ __host__ __device__ __forceinline__ int cta_of_row(int T, int ctas, int t) {
 // Forward.  A team of W warps walks rows, V vectors of 8 columns per thread; as
 // in the backward pass below every thread copies its own columns of the rows to
 // come into its own slots of shared memory, and holds x' between its two sums
-// in registers.
+// in registers.  Bound by HBM: 32768 x 4096 bf16, post and pre norm, in 8 shards,
+// 163 us, 6.6 TB/s.
 template <int W, int V>
 struct FwdShape {
   static constexpr int ROW = Team<W>::CTA * V * 32;  // bytes of two tensors' rows, all teams of the CTA
@@ -243,6 +244,10 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
 //
 // Consecutive rows for a CTA were measured against rows dealt out in turn (T
 // 32768, H 4096): 318 against 393 us.
+//
+// Bound by latency: the registers that hold the weights and column sums leave 12
+// to 16 warps on an SM, which meet twice a row.  32768 x 4096 bf16: 312 us with
+// the joining kernel, 5.2 TB/s; 4061 x 12288 f16 with 31 gate rows: 154 us, 3.9.
 template <int W, int V>
 struct BwdShape {
   static constexpr int ROW = Team<W>::CTA * V * 64;  // bytes of four tensors' rows, all teams of the CTA
@@ -650,7 +655,9 @@ inline int sum_blocks(int H) { return (H + SUM_COLS - 1) / SUM_COLS; }
 inline int run_blocks(int H) { return (H + 4 * SUM_THREADS - 1) / (4 * SUM_THREADS); }
 
 // Joins the CTAs' partial sums, each column in a fixed order, and leaves the
-// partial sums zero.
+// partial sums zero.  SUM_BATCH loads of a thread are on their way together: a few
+// MB from L2 are bound by latency (H 4096, 304 CTAs: 16 us with cold caches; one
+// load after the other took 300).
 template <int DT>
 __global__ void __launch_bounds__(SUM_THREADS)
 block_norm_sums_kernel(const __grid_constant__ BlockNormArgs a, int col_blocks, int per_run_blocks) {

@@ -196,6 +196,10 @@ __device__ __forceinline__ void join_losses(const BalanceArgs& a, int n, float* 
 // own experts' sums.  An item's sums are joined over its warps in shared memory,
 // a sequence's over its items by balance_join_kernel, or, where there is one
 // sequence of few items, by the last of their CTAs; all in fixed orders.
+//
+// Bound by issue slots next to HBM (an exponential and two sums per score):
+// 131072 x 256 in 64 masked sequences 30.3 us with the joining kernel, 4.6 TB/s
+// (sums in double precision took 462); 4096 x 8 in one launch 5.9 us.
 template <int LPT, int V, bool VEC>
 __global__ void __launch_bounds__(RT_THREADS, V <= 4 ? 3 : 2)
 balance_kernel(const __grid_constant__ BalanceArgs a) {
@@ -416,7 +420,8 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
 }
 
 // Joins the items' sums of COLS experts of one sequence, the items dealt out to
-// JOIN_THREADS / COLS threads.
+// JOIN_THREADS / COLS threads.  Latency: 3 us behind the forward kernel at 64
+// sequences of 256 experts (8.6 us with cold caches).
 template <int COLS>
 __global__ void __launch_bounds__(JOIN_THREADS) balance_join_kernel(const __grid_constant__ BalanceArgs a) {
   constexpr int ROWS = JOIN_THREADS / COLS;
@@ -515,7 +520,8 @@ struct RouterBwdArgs {
 
 // Backward: one read of the scores, one write of their gradient.  A CTA stays in
 // one sequence, whose counts its lanes hold; the gate's terms of a token meet
-// the others through a row of shared memory.
+// the others through a row of shared memory.  Bound by HBM: 131072 x 256 49 us,
+// 5.7 TB/s.
 template <int LPT, int V, bool VEC>
 __global__ void __launch_bounds__(RT_THREADS, V <= 2 ? 5 : 2)
 router_bwd_kernel(const __grid_constant__ RouterBwdArgs a) {
