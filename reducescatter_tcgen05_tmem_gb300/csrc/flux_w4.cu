@@ -604,41 +604,69 @@ __global__ void __launch_bounds__(W4_JOIN_WARPS * 32) w4_join_kernel(const __gri
   }
 }
 
-// One thread per column and group: the group's largest magnitude / 7, rounded
-// to 16 bits, is its scale; codes are the nearest multiples of it.  Run once per
-// weight; neighbouring threads read neighbouring columns, and the second reading
-// of a group comes from L1 or L2.
+// One thread per four columns and group: the group's largest magnitude / 7,
+// rounded to 16 bits, is its scale; codes are the nearest multiples of it.  Eight
+// loads of 8 bytes are on their way together; the second reading of a group comes
+// from L1 or L2.  Run once per weight, bound by its stores (words 64 bytes of a
+// column apart; a group need not be whole runs): 8 x 4096 x 14336 in groups of 128
+// 569 us, 2.1 TB/s; a column a thread took 844.
+constexpr int W4_QUANT_COLS = 4;
+
 template <int DT>
 __global__ void __launch_bounds__(128)
-w4_quantize_kernel(int K, int N, int runs, int group, int groups, const void* __restrict__ w, uint8_t* __restrict__ q,
-                   void* __restrict__ scales) {
-  const int n = blockIdx.x * 128 + threadIdx.x;
+w4_quantize_kernel(int K, int N, int runs, int group, int groups, const uint16_t* __restrict__ w, uint8_t* __restrict__ q,
+                   uint16_t* __restrict__ scales) {
+  constexpr int C = W4_QUANT_COLS;
+  const int n = (blockIdx.x * 128 + threadIdx.x) * C;
   const size_t e = blockIdx.z;
   if (n >= N) return;
-  const size_t wbase = e * K * N + n;
+  // eight inputs of the four columns
+  auto load8 = [&](int k, float (&v)[8][C]) {
+    const uint16_t* from = w + (e * K + k) * N + n;
+    uint2 raw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[i] = __ldg(reinterpret_cast<const uint2*>(from + static_cast<size_t>(i) * N));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 lo = unpack2<DT>(raw[i].x), hi = unpack2<DT>(raw[i].y);
+      v[i][0] = lo.x, v[i][1] = lo.y, v[i][2] = hi.x, v[i][3] = hi.y;
+    }
+  };
   for (int g = blockIdx.y; g < groups; g += gridDim.y) {
     const int k0 = g * group, k1 = min(k0 + group, K);
-    float top = 0.0f;
-    for (int k = k0; k < k1; ++k) top = fmaxf(top, fabsf(load16<DT>(w, wbase + static_cast<size_t>(k) * N)));
-    const uint32_t s16 = pack2<DT>(top / 7.0f, 0.0f);
-    const float scale = unpack2<DT>(s16).x;
-    static_cast<uint16_t*>(scales)[(e * groups + g) * N + n] = static_cast<uint16_t>(s16);
+    float top[C] = {}, v[8][C];
+    for (int k = k0; k < k1; k += 8) {
+      load8(k, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < C; ++c) top[c] = fmaxf(top[c], fabsf(v[i][c]));
+    }
+    const uint32_t s01 = pack2<DT>(top[0] / 7.0f, top[1] / 7.0f), s23 = pack2<DT>(top[2] / 7.0f, top[3] / 7.0f);
+    *reinterpret_cast<uint2*>(scales + (e * groups + g) * N + n) = make_uint2(s01, s23);
+    const float scale[C] = {unpack2<DT>(s01).x, unpack2<DT>(s01).y, unpack2<DT>(s23).x, unpack2<DT>(s23).y};
     // the last group also fills its run of 128 inputs
     const int kend = g == groups - 1 ? runs * W4_RUN : k1;
     for (int k = k0; k < kend; k += 8) {
-      uint32_t word = 0x88888888u;
-      if (k < K && scale > 0.0f) {
-        word = 0;
+      uint32_t word[C] = {0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u};
+      if (k < K) {
+        load8(k, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float v = load16<DT>(w, wbase + static_cast<size_t>(k + i) * N);
-          const int code = min(max(static_cast<int>(rintf(v / scale)) + 8, 0), 15);
-          word |= static_cast<uint32_t>(code) << (i / 2 * 4 + i % 2 * 16);
+        for (int c = 0; c < C; ++c) {
+          if (!(scale[c] > 0.0f)) continue;
+          word[c] = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int code = min(max(static_cast<int>(rintf(v[i][c] / scale[c])) + 8, 0), 15);
+            word[c] |= static_cast<uint32_t>(code) << (i / 2 * 4 + i % 2 * 16);
+          }
         }
       }
       const int r = k % W4_RUN;
-      *reinterpret_cast<uint32_t*>(q + ((e * N + n) * runs + k / W4_RUN) * (W4_RUN / 2) + r % 32 / 8 * 16 + r / 32 * 4) =
-          word;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        *reinterpret_cast<uint32_t*>(q + ((e * N + n + c) * runs + k / W4_RUN) * W4_RUN_BYTES + r % 32 / 8 * 16 + r / 32 * 4) =
+            word[c];
     }
   }
 }
@@ -792,12 +820,15 @@ extern "C" flux_status_t flux_w4_quantize(int E, int K, int N, int group, flux_d
   flux_status_t st = current_device(&dev);
   if (st != FLUX_OK) return st;
   const int runs = (K + W4_RUN - 1) / W4_RUN, groups = (K + group - 1) / group;
-  const dim3 grid((N + 127) / 128, std::min(groups, 65535), E);
+  const int cols = 128 * W4_QUANT_COLS;
+  const dim3 grid((N + cols - 1) / cols, std::min(groups, 65535), E);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == FLUX_BF16)
-    w4_quantize_kernel<1><<<grid, 128, 0, s>>>(K, N, runs, group, groups, w, static_cast<uint8_t*>(q), scales);
+    w4_quantize_kernel<1><<<grid, 128, 0, s>>>(K, N, runs, group, groups, static_cast<const uint16_t*>(w),
+                                               static_cast<uint8_t*>(q), static_cast<uint16_t*>(scales));
   else
-    w4_quantize_kernel<0><<<grid, 128, 0, s>>>(K, N, runs, group, groups, w, static_cast<uint8_t*>(q), scales);
+    w4_quantize_kernel<0><<<grid, 128, 0, s>>>(K, N, runs, group, groups, static_cast<const uint16_t*>(w),
+                                               static_cast<uint8_t*>(q), static_cast<uint16_t*>(scales));
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
