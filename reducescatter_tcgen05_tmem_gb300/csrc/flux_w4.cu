@@ -671,7 +671,7 @@ w4_quantize_kernel(int K, int N, int runs, int group, int groups, const uint16_t
   }
 }
 
-// Workspace: header, arrivals, finished row tiles, partial tiles, fp32 rows.
+// Workspace: header, how the units were cut, the slots' tiles, sums of cut tiles, fp32 rows (layer1).
 struct W4Ws {
   size_t split, where, parts, rows, total;
 };
