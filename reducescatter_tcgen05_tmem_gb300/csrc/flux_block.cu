@@ -557,7 +557,9 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
         if constexpr (ROOMY) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) d_r[v][i] = d[i];
-        } else {
+        } else if (column(v) < a.H) {
+          // slots past H stay zero: no copy fills them again, and there d of a row that
+          // is not finite is NaN
           const ulonglong2 lo = make_ulonglong2(d[0], d[1]), hi = make_ulonglong2(d[2], d[3]);
           slot(stage, X, v) = *reinterpret_cast<const uint4*>(&lo);
           slot(stage, DU, v) = *reinterpret_cast<const uint4*>(&hi);
