@@ -531,8 +531,9 @@ struct W4Parts {
 // The second half of a product: adds the parts of cut tiles in team order, for
 // layer1 the tokens' slots, and writes zeros for slots of no expert.  Four
 // columns of one row of the output per thread; layer1: a warp for each of up to
-// W4_JOIN_WARPS slots of the token, which meet in shared memory (slots one after
-// the other in one thread took twice the time).  Leaves what it reads of the
+// W4_JOIN_WARPS slots of the token at a time, which meet in shared memory and are
+// added in slot order (slots one after the other in one thread took twice the
+// time).  Leaves what it reads of the
 // workspace zero.  A chain of latencies: 8192 columns of 13 rows 5 us with cold
 // caches, 4096 of 24 rows and 6 slots 8 us behind the products.
 template <int DT, int MT, bool LAYER1>
@@ -547,36 +548,42 @@ __global__ void __launch_bounds__(W4_JOIN_WARPS * 32) w4_join_kernel(const __gri
   bool write = n < a.N;
   if constexpr (LAYER1) {
     __shared__ float4 meet[W4_JOIN_WARPS][32];
-    for (int j = warp; j < a.topk && write; j += warps) {
-      const int slot = row * a.topk + j;
-      const W4Slot at = a.where[slot];
-      const float w = a.weights[slot];
-      if (at.tile == W4_NONE) continue;
+    for (int j0 = 0; j0 < a.topk; j0 += warps) {
+      const int j = j0 + warp;
       float4 f = zero;
-      if (p.open(at)) {
-        p.template add<4>(p.c0, f);
-      } else {
-        float4* from = reinterpret_cast<float4*>(a.rows_f32 + static_cast<size_t>(slot) * a.N + n);
-        f = *from;
-        *from = zero;
+      if (j < a.topk && write) {
+        const int slot = row * a.topk + j;
+        const W4Slot at = a.where[slot];
+        const float w = a.weights[slot];
+        if (at.tile != W4_NONE) {
+          if (p.open(at)) {
+            p.template add<4>(p.c0, f);
+          } else {
+            float4* from = reinterpret_cast<float4*>(a.rows_f32 + static_cast<size_t>(slot) * a.N + n);
+            f = *from;
+            *from = zero;
+          }
+          f = make_float4(__fmul_rn(w, f.x), __fmul_rn(w, f.y), __fmul_rn(w, f.z), __fmul_rn(w, f.w));
+        }
       }
-      sum.x += w * f.x;
-      sum.y += w * f.y;
-      sum.z += w * f.z;
-      sum.w += w * f.w;
-    }
-    meet[warp][lane] = sum;
-    __syncthreads();
-    write = write && warp == 0;
-    if (write) {
-      for (int w = 1; w < warps; ++w) {
-        const float4 f = meet[w][lane];
+      if (j0 > 0) __syncthreads();  // the slots before have been added
+      meet[warp][lane] = f;
+      __syncthreads();
+      if (warp == 0) {
         sum.x += f.x;
         sum.y += f.y;
         sum.z += f.z;
         sum.w += f.w;
+        for (int w = 1; w < min(warps, a.topk - j0); ++w) {
+          const float4 o = meet[w][lane];
+          sum.x += o.x;
+          sum.y += o.y;
+          sum.z += o.z;
+          sum.w += o.w;
+        }
       }
     }
+    write = write && warp == 0;
   } else if (write) {
     const W4Slot at = a.mode == W4_DENSE ? W4Slot{static_cast<uint16_t>(row / (MT * 8)), static_cast<uint16_t>(row % (MT * 8))}
                                          : a.where[row];
