@@ -164,22 +164,24 @@ _OPT_FIELDS = frozenset(name for name, _ in flux_opts_t._fields_)
 
 # ---------------------------------------------------------------- marshalling
 def _ptr(x):
-    if x is None or x.__class__ is int:
+    if x is None or isinstance(x, int):
         return x
-    return x.data_ptr() if hasattr(x, "data_ptr") else int(x)
+    return x.data_ptr()
 
 
 _PTRS = {}  # ctypes array types by length
 
 
 def _ptrs(xs):
-    if xs is None:
-        return None
     n = len(xs)
     make = _PTRS.get(n) or _PTRS.setdefault(n, ctypes.c_void_p * n)
     if n == 1:
         return make(_ptr(xs[0]))
     return make.from_buffer(array.array("Q", [_ptr(x) or 0 for x in xs]))
+
+
+def _optional_ptrs(xs):
+    return None if xs is None else _ptrs(xs)
 
 
 def _nbytes(t):
@@ -387,9 +389,9 @@ def flux_block_norm_workspace_size(T: int, H: int, gate_rows: int = 0, gate_cols
 def flux_block_norm(R, T, H, dtype, post_norm, gate_rows, gate_cols, eps, x_shards, y_shards, w_post, gate,
                     res_scale, w_pre, x_out, u_out, rstd_y=None, rstd_x=None, stream=None) -> None:
     """Post-norm, gate, residual and the next block's pre-norm in one pass."""
-    _check(_lib.flux_block_norm(R, T, H, dtype, post_norm, gate_rows, gate_cols, eps, _ptrs(x_shards),
-                                _ptrs(y_shards), _ptr(w_post), _ptr(gate), _ptr(res_scale), _ptr(w_pre),
-                                _ptrs(x_out), _ptrs(u_out), _ptr(rstd_y), _ptr(rstd_x), _stream(stream)),
+    _check(_lib.flux_block_norm(R, T, H, dtype, post_norm, gate_rows, gate_cols, eps, _optional_ptrs(x_shards),
+                                _optional_ptrs(y_shards), _ptr(w_post), _ptr(gate), _ptr(res_scale), _ptr(w_pre),
+                                _optional_ptrs(x_out), _optional_ptrs(u_out), _ptr(rstd_y), _ptr(rstd_x), _stream(stream)),
            "flux_block_norm")
 
 
@@ -398,9 +400,9 @@ def flux_block_norm_bwd(R, T, H, dtype, post_norm, gate_rows, gate_cols, x_shard
                         dw_pre, workspace, stream=None) -> None:
     """Gradients of flux_block_norm."""
     _check(_lib.flux_block_norm_bwd(
-        R, T, H, dtype, post_norm, gate_rows, gate_cols, _ptrs(x_shards), _ptrs(y_shards), _ptr(w_post),
-        _ptr(gate), _ptr(res_scale), _ptr(w_pre), _ptr(rstd_y), _ptr(rstd_x), _ptrs(dx_out), _ptrs(du),
-        _ptrs(dx), _ptrs(dy), _ptr(dw_post), _ptr(dgate), _ptr(dres_scale), _ptr(dw_pre), _ptr(workspace),
+        R, T, H, dtype, post_norm, gate_rows, gate_cols, _optional_ptrs(x_shards), _optional_ptrs(y_shards), _ptr(w_post),
+        _ptr(gate), _ptr(res_scale), _ptr(w_pre), _ptr(rstd_y), _ptr(rstd_x), _optional_ptrs(dx_out), _optional_ptrs(du),
+        _optional_ptrs(dx), _optional_ptrs(dy), _ptr(dw_post), _ptr(dgate), _ptr(dres_scale), _ptr(dw_pre), _ptr(workspace),
         _nbytes(workspace), _stream(stream)), "flux_block_norm_bwd")
 
 
