@@ -19,7 +19,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 #include "flux_host.h"
@@ -881,7 +880,7 @@ void fill_common(BlockNormArgs* a, int R, int T, int H, int post_norm, int gate_
   a->w_pre = w_pre;
 }
 
-// Lets a kernel use `smem` bytes of shared memory; once per kernel.
+// Lets a kernel use `smem` bytes of shared memory on the current device.
 template <typename K>
 cudaError_t allow_smem(K kernel, int smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -891,9 +890,8 @@ template <int DT, int W, int V, bool HAS_Y>
 flux_status_t launch_fwd_form(const BlockNormArgs& a, const DeviceInfo& dev, cudaStream_t s) {
   using S = FwdShape<W, V>;
   constexpr auto kernel = block_norm_kernel<DT, W, V, HAS_Y>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] { attr = allow_smem(kernel, S::SMEM); });
+  static OncePerDevice once;
+  const cudaError_t attr = once(dev.device, [] { return allow_smem(kernel, S::SMEM); });
   if (attr != cudaSuccess) return cuda_fail(attr);
   const int grid = std::min((a.T + Team<W>::COUNT - 1) / Team<W>::COUNT, dev.sm_count * S::CTAS);
   const cudaError_t e = launch_behind(kernel, dim3(grid), Team<W>::CTA, S::SMEM, s, a);
@@ -909,23 +907,22 @@ flux_status_t launch_fwd(const BlockNormArgs& a, const DeviceInfo& dev, cudaStre
 }
 
 template <int DT, int W, int V, bool HAS_Y, bool HAS_U>
-flux_status_t launch_bwd_form(const BlockNormArgs& a, const BwdPlan& p, cudaStream_t s) {
+flux_status_t launch_bwd_form(const BlockNormArgs& a, const BwdPlan& p, const DeviceInfo& dev, cudaStream_t s) {
   constexpr int smem = BwdShape<W, V>::SMEM;
   constexpr auto kernel = block_norm_bwd_kernel<DT, W, V, HAS_Y, HAS_U>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] { attr = allow_smem(kernel, smem); });
+  static OncePerDevice once;
+  const cudaError_t attr = once(dev.device, [] { return allow_smem(kernel, smem); });
   if (attr != cudaSuccess) return cuda_fail(attr);
   const cudaError_t e = launch_behind(kernel, dim3(p.ctas), Team<W>::CTA, smem, s, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
 template <int DT>
-flux_status_t launch_bwd(const BlockNormArgs& a, const BwdPlan& p, cudaStream_t s) {
+flux_status_t launch_bwd(const BlockNormArgs& a, const BwdPlan& p, const DeviceInfo& dev, cudaStream_t s) {
   flux_status_t st = by_width<true>(a.H, [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, V = decltype(v)::value;
-    if (!a.has_y) return launch_bwd_form<DT, W, V, false, true>(a, p, s);
-    return a.has_u ? launch_bwd_form<DT, W, V, true, true>(a, p, s) : launch_bwd_form<DT, W, V, true, false>(a, p, s);
+    if (!a.has_y) return launch_bwd_form<DT, W, V, false, true>(a, p, dev, s);
+    return a.has_u ? launch_bwd_form<DT, W, V, true, true>(a, p, dev, s) : launch_bwd_form<DT, W, V, true, false>(a, p, dev, s);
   });
   if (st != FLUX_OK) return st;
   const int cols = sum_blocks(a.H), per_run = a.gate_cols == 1 ? 1 : run_blocks(a.H);
@@ -1046,5 +1043,5 @@ extern "C" flux_status_t flux_block_norm_bwd(int R, int T, int H, flux_dtype_t d
   a.part_scalar = reinterpret_cast<double*>(ws + p.scalar);
   a.ctas = p.ctas;
   a.run_rows = p.run_rows;
-  return dtype == FLUX_BF16 ? launch_bwd<1>(a, p, s) : launch_bwd<0>(a, p, s);
+  return dtype == FLUX_BF16 ? launch_bwd<1>(a, p, dev, s) : launch_bwd<0>(a, p, dev, s);
 }

@@ -20,9 +20,8 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 cudaError_t g_encode_err = cudaSuccess;
 
-constexpr int kMaxDevices = 64;
-DeviceInfo g_dev[kMaxDevices];
-bool g_dev_ok[kMaxDevices];
+DeviceInfo g_dev[MAX_DEVICES];
+bool g_dev_ok[MAX_DEVICES];
 std::mutex g_dev_mu;
 
 CUtensorMapDataType map_type(flux_dtype_t dt) {
@@ -59,7 +58,7 @@ flux_status_t current_device(DeviceInfo* info) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
-  if (dev < 0 || dev >= kMaxDevices) return FLUX_ERR_NO_DEVICE;
+  if (dev < 0 || dev >= MAX_DEVICES) return FLUX_ERR_NO_DEVICE;
   std::lock_guard<std::mutex> lk(g_dev_mu);
   if (!g_dev_ok[dev]) {
     DeviceInfo d{};

@@ -8,6 +8,8 @@
 #include <stdint.h>
 
 #include <array>
+#include <atomic>
+#include <mutex>
 
 #include "../../include/flux_gb300.h"
 
@@ -27,6 +29,29 @@ struct DeviceInfo {
   int sm_count;
   int cc_major, cc_minor;
   size_t max_smem_optin;
+};
+
+constexpr int MAX_DEVICES = 64;  // ordinals that current_device accepts
+
+// Function attributes belong to the device that is current when they are set.
+// Runs `set`, which returns a cudaError_t, until it has succeeded once on
+// `device`; one static object for each kernel.
+class OncePerDevice {
+ public:
+  template <typename F>
+  cudaError_t operator()(int device, F&& set) {
+    std::atomic<bool>& done = done_[device];
+    if (done.load(std::memory_order_acquire)) return cudaSuccess;
+    std::lock_guard<std::mutex> lock(mutex_);
+    if (done.load(std::memory_order_relaxed)) return cudaSuccess;
+    const cudaError_t e = set();
+    if (e == cudaSuccess) done.store(true, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<bool> done_[MAX_DEVICES] = {};
+  std::mutex mutex_;
 };
 
 // Current device's properties (cached); FLUX_ERR_NO_DEVICE if it has no tcgen05.

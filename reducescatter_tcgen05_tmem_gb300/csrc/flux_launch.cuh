@@ -1,11 +1,10 @@
 // Host-side launch of one instantiation of the fused kernel: sets the shared
-// memory attribute once, sizes CTA-pair grids to the clusters that fit at
+// memory attribute once per device, sizes CTA-pair grids to the clusters that fit at
 // once, and launches on the caller's stream.
 #pragma once
 
 #include <cstdio>
 #include <cstdlib>
-#include <mutex>
 
 #include "flux_host.h"
 #include "flux_kernels.cuh"
@@ -25,16 +24,15 @@ template <int MODE, int DT, int CL>
 struct Launcher {
   // Largest grid (CTAs) that is resident at once; 0 on error.
   static int max_ctas(const DeviceInfo& dev) {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    static int ctas = 0;
-    std::call_once(once, [&dev] {
-      err = cudaFuncSetAttribute(fused_gemm_kernel<MODE, DT, CL>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-      if (err != cudaSuccess) return;
+    static OncePerDevice once;
+    static int ctas[MAX_DEVICES] = {};
+    const cudaError_t err = once(dev.device, [&dev] {
+      cudaError_t e = cudaFuncSetAttribute(fused_gemm_kernel<MODE, DT, CL>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+      if (e != cudaSuccess) return e;
       if (CL == 1) {
-        ctas = dev.sm_count;
-        return;
+        ctas[dev.device] = dev.sm_count;
+        return e;
       }
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(CL * (dev.sm_count / CL), 1, 1);
@@ -48,17 +46,18 @@ struct Launcher {
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int clusters = 0;
-      err = cudaOccupancyMaxActiveClusters(&clusters, fused_gemm_kernel<MODE, DT, CL>, &cfg);
-      ctas = clusters * CL;
+      e = cudaOccupancyMaxActiveClusters(&clusters, fused_gemm_kernel<MODE, DT, CL>, &cfg);
+      ctas[dev.device] = clusters * CL;
       if (debug_enabled())
         std::fprintf(stderr, "[flux] mode %d dtype %d cluster %d: %d clusters resident at once\n",
                      MODE, DT, CL, clusters);
+      return e;
     });
     if (err != cudaSuccess) {
       cuda_fail(err);
       return 0;
     }
-    return ctas;
+    return ctas[dev.device];
   }
 
   // Dynamic schedule (dense CL = 4 kernels): the grid when clusters are CTA
@@ -67,9 +66,9 @@ struct Launcher {
   static int max_ctas_dyn(const DeviceInfo& dev) {
     static_assert(CL == 4 || CL == 8, "regions of two or four CTA pairs");
     if (max_ctas(dev) <= 0) return 0;  // sets the shared memory attribute
-    static std::once_flag once;
-    static int ctas = 0;
-    std::call_once(once, [&dev] {
+    static OncePerDevice once;
+    static int ctas[MAX_DEVICES] = {};
+    once(dev.device, [&dev] {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * (dev.sm_count / 2), 1, 1);
       cfg.blockDim = dim3(KernelShape<MODE, DT, CL>::THREADS, 1, 1);
@@ -90,12 +89,13 @@ struct Launcher {
       int g = clusters * 2;
       g -= g % CL;
       if (g > CL * MAX_REGIONS) g = CL * MAX_REGIONS;
-      ctas = g;
+      ctas[dev.device] = g;
       if (debug_enabled())
         std::fprintf(stderr, "[flux] mode %d dtype %d: %d CTA pairs resident at once (dynamic grid %d)\n",
                      MODE, DT, clusters, g);
+      return cudaSuccess;
     });
-    return ctas;
+    return ctas[dev.device];
   }
 
   static flux_status_t launch_dyn(const KParams& p, int grid, cudaStream_t stream) {

@@ -10,7 +10,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 #include "flux_host.h"
@@ -705,10 +704,9 @@ template <int DT, int MT, int SR>
 flux_status_t w4_launch(W4Args a, const DeviceInfo& dev, cudaStream_t s) {
   using S = W4Shape<MT, SR>;
   constexpr int smem = S::TEAMS * S::SMEM;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(w4_kernel<DT, MT, SR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static OncePerDevice once;
+  const cudaError_t attr = once(dev.device, [] {
+    return cudaFuncSetAttribute(w4_kernel<DT, MT, SR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (attr != cudaSuccess) return cuda_fail(attr);
   // no more teams than units (of as many row tiles as the slots can make)
