@@ -39,6 +39,7 @@ constexpr int RT_FWD_CTAS = 3 * 152, RT_BWD_CTAS = 5 * 152;  // at most this man
 // joined by a second kernel
 constexpr int RT_HERE_ITEMS = 64, RT_HERE_SUMS = 2048;
 constexpr int JOIN_THREADS = 512, JOIN_FEW = 32;  // few items of a sequence: a thread adds all of an expert's
+constexpr int JOIN_WIDE = 256, JOIN_NARROW = 32;  // experts of a joining block: few items, many
 
 // A token's scores are held by LPT lanes, four by four: V vectors of four a
 // lane.  Vectors of a row of 4 n experts are 16-byte loads of neighbours, other
@@ -660,12 +661,18 @@ auto by_experts(int E, F&& f) {
   return vec(Int<32>{}, Int<8>{});
 }
 
-// Items of a sequence: one wave of CTAs in all where S allows it, each with work
-// for its warps.
+// Items of a sequence before its tokens are dealt out evenly: one wave of CTAs in
+// all where S allows it, each with work for its warps.  Never fewer for more tokens.
+template <bool FORWARD>
+int most_items(int E, int per, int S) {
+  const int tokens = by_experts<FORWARD>(E, [](auto lpt, auto, auto) { return RT_WARPS * 32 / decltype(lpt)::value; });
+  return std::max(1, std::min((FORWARD ? RT_FWD_CTAS : RT_BWD_CTAS) / S, (per + tokens - 1) / tokens));
+}
+
+// Items of a sequence, equal but for the last.
 template <bool FORWARD>
 void cut_tokens(int E, int per, int S, int* sub, int* chunk) {
-  const int tokens = by_experts<FORWARD>(E, [](auto lpt, auto, auto) { return RT_WARPS * 32 / decltype(lpt)::value; });
-  *sub = std::max(1, std::min((FORWARD ? RT_FWD_CTAS : RT_BWD_CTAS) / S, (per + tokens - 1) / tokens));
+  *sub = most_items<FORWARD>(E, per, S);
   *chunk = (per + *sub - 1) / *sub;
   *sub = (per + *chunk - 1) / *chunk;
 }
@@ -674,7 +681,7 @@ BalancePlan balance_plan(int T, int E, int S) {
   BalancePlan p{};
   cut_tokens<true>(E, T / S, S, &p.sub, &p.chunk);
   p.items = p.sub * S;
-  p.join_cols = p.sub <= JOIN_FEW ? 256 : 32;
+  p.join_cols = p.sub <= JOIN_FEW ? JOIN_WIDE : JOIN_NARROW;
   const bool here = S == 1 && p.sub <= RT_HERE_ITEMS && static_cast<long long>(p.sub) * E <= RT_HERE_SUMS;
   p.cols = p.sub > 1 && !here ? (E + p.join_cols - 1) / p.join_cols : 0;
   size_t at = WS_HEADER;
@@ -683,12 +690,16 @@ BalancePlan balance_plan(int T, int E, int S) {
     at += round_up(bytes, WS_ALIGN);
     return here;
   };
-  const size_t parts = p.sub > 1 ? static_cast<size_t>(p.items) : 0;
+  // sizes by the items before they are made even, so that the workspace of a batch
+  // is enough for every smaller one: 8664 tokens of 256 experts have 456 items, 9000 have 450
+  const int most = most_items<true>(E, T / S, S);
+  const size_t parts = most > 1 ? static_cast<size_t>(most) * S : 0;
+  const int cols = most > 1 ? (E + JOIN_NARROW - 1) / JOIN_NARROW : 1;
   p.probs = take(sizeof(float) * parts * E);
   p.counts = take(sizeof(int) * parts * E);
   p.kept = take(sizeof(int) * parts);
   p.z = take(sizeof(float) * parts);
-  p.bal = take(sizeof(float) * S * static_cast<size_t>(std::max(1, p.cols)));
+  p.bal = take(sizeof(float) * S * static_cast<size_t>(cols));
   p.seq_z = take(sizeof(float) * S);
   p.total = at;
   return p;
@@ -768,7 +779,7 @@ extern "C" flux_status_t flux_moe_balance_loss(int T, int E, int topk, int seqs,
   });
   if (e != cudaSuccess) return cuda_fail(e);
   if (p.cols == 0) return FLUX_OK;
-  e = launch_behind(p.join_cols == 256 ? balance_join_kernel<256> : balance_join_kernel<32>, dim3(p.cols, seqs), JOIN_THREADS, 0, s, a);
+  e = launch_behind(p.join_cols == JOIN_WIDE ? balance_join_kernel<JOIN_WIDE> : balance_join_kernel<JOIN_NARROW>, dim3(p.cols, seqs), JOIN_THREADS, 0, s, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
