@@ -79,6 +79,8 @@ flux_status_t encode_3d(CUtensorMap* map, flux_dtype_t dt, const void* base, uin
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+// n / d rounded up, where n + d may be past 32 bits.
+inline int ceil_div(int n, int d) { return n / d + (n % d != 0); }
 
 // Validate a workspace pointer and size.
 flux_status_t check_workspace(const void* ws, size_t have, size_t need);

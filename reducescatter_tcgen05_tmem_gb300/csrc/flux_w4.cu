@@ -639,7 +639,7 @@ w4_quantize_kernel(int K, int N, int runs, int group, int groups, const uint16_t
     }
   };
   for (int g = blockIdx.y; g < groups; g += gridDim.y) {
-    const int k0 = g * group, k1 = min(k0 + group, K);
+    const int k0 = g * group, k1 = K - k0 > group ? k0 + group : K;
     float top[C] = {}, v[8][C];
     for (int k = k0; k < k1; k += 8) {
       load8(k, v);
@@ -792,7 +792,7 @@ flux_status_t w4_run(W4Mode mode, int rows, int slots, int T, int N, int K, int 
   a.K = K;
   a.runs = (K + W4_RUN - 1) / W4_RUN;
   a.group = group;
-  a.groups = (K + group - 1) / group;
+  a.groups = ceil_div(K, group);
   a.E = E;
   a.topk = topk;
   a.mode = mode;
@@ -824,7 +824,7 @@ extern "C" flux_status_t flux_w4_quantize(int E, int K, int N, int group, flux_d
   DeviceInfo dev;
   flux_status_t st = current_device(&dev);
   if (st != FLUX_OK) return st;
-  const int runs = (K + W4_RUN - 1) / W4_RUN, groups = (K + group - 1) / group;
+  const int runs = (K + W4_RUN - 1) / W4_RUN, groups = ceil_div(K, group);
   const int cols = 128 * W4_QUANT_COLS;
   const dim3 grid((N + cols - 1) / cols, std::min(groups, 65535), E);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
