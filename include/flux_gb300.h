@@ -646,7 +646,8 @@ flux_status_t flux_moe_router_bwd(int T, int E, int topk, int seqs, float balanc
  *            and 32 j + 8 c + 2 (i - 4) + 1 for i >= 4.  Codes past K are ignored.
  *   scales   device [E x ceil(K / group) x N] in dtype
  * Sums in fp32, the scale of a group applied to its exact sum of x (code - 8).
- * Requires N % 8 == 0, K % 8 == 0, group % 32 == 0 (FLUX_ERR_UNSUPPORTED).  More
+ * Requires N % 8 == 0, K % 8 == 0, group % 32 == 0, N and K at most 2^31 - 1024
+ * (FLUX_ERR_UNSUPPORTED).  More
  * than FLUX_W4_MAX_ROWS rows (M, or T topk) return FLUX_ERR_UNSUPPORTED: such
  * products are bound by arithmetic and belong to the 16-bit GEMMs. */
 

@@ -30,6 +30,7 @@ constexpr int W4_COLS = W4_WARPS * 16 * W4_CA;   // columns of a tile
 constexpr int W4_MIN_UNITS = 4;
 constexpr int W4_MAX_TEAMS = 4 * 160;            // at most four per SM
 constexpr int W4_RUN_BYTES = W4_RUN / 2;
+constexpr int W4_MAX_SIZE = INT_MAX - 1023;      // of N and K: rounded up to tiles, runs and blocks they still are ints
 constexpr int W4_NONE = 0xFFFF;                  // row tile of a slot whose expert id is out of range
 
 // Equal stretches of units: team i has the units [first(i), first(i + 1)).
@@ -754,7 +755,7 @@ flux_status_t w4_run(W4Mode mode, int rows, int slots, int T, int N, int K, int 
                      flux_dtype_t dtype, const void* x, const void* q, const void* scales, const int32_t* ids,
                      const float* weights, void* out, void* workspace, size_t workspace_bytes, void* stream) {
   if (T < 0 || !w4_common_ok(N, K, group, E, dtype) || topk < 1 || topk > E) return FLUX_ERR_INVALID_ARG;
-  if (N % 8 != 0 || K % 8 != 0 || group % 32 != 0) return FLUX_ERR_UNSUPPORTED;
+  if (N % 8 != 0 || K % 8 != 0 || N > W4_MAX_SIZE || K > W4_MAX_SIZE || group % 32 != 0) return FLUX_ERR_UNSUPPORTED;
   if (static_cast<long long>(T) * topk > FLUX_W4_MAX_ROWS) return FLUX_ERR_UNSUPPORTED;
   if (rows == 0 || N == 0) return FLUX_OK;
   if (out == nullptr || (K > 0 && (x == nullptr || q == nullptr || scales == nullptr)) ||
@@ -805,19 +806,21 @@ flux_status_t w4_run(W4Mode mode, int rows, int slots, int T, int N, int K, int 
 using namespace flux;
 
 extern "C" size_t flux_w4_weight_bytes(int E, int K, int N) {
-  if (E < 1 || K < 0 || N < 0) return 0;
+  if (E < 1 || K < 0 || N < 0 || K > W4_MAX_SIZE || N > W4_MAX_SIZE) return 0;
   return static_cast<size_t>(E) * N * ((K + W4_RUN - 1) / W4_RUN) * (W4_RUN / 2);
 }
 
 extern "C" size_t flux_w4_workspace_size(int rows, int N, int K, int E) {
-  if (rows < 0 || rows > FLUX_W4_MAX_ROWS || N < 0 || K < 0 || E < 1 || E > FLUX_MAX_EXPERTS) return 0;
+  if (rows < 0 || rows > FLUX_W4_MAX_ROWS || N < 0 || K < 0 || N > W4_MAX_SIZE || K > W4_MAX_SIZE || E < 1 ||
+      E > FLUX_MAX_EXPERTS)
+    return 0;
   return w4_ws(rows, N).total;
 }
 
 extern "C" flux_status_t flux_w4_quantize(int E, int K, int N, int group, flux_dtype_t dtype, const void* w, void* q,
                                           void* scales, void* stream) {
   if (!w4_common_ok(N, K, group, E, dtype)) return FLUX_ERR_INVALID_ARG;
-  if (N % 8 != 0 || K % 8 != 0 || group % 32 != 0) return FLUX_ERR_UNSUPPORTED;
+  if (N % 8 != 0 || K % 8 != 0 || N > W4_MAX_SIZE || K > W4_MAX_SIZE || group % 32 != 0) return FLUX_ERR_UNSUPPORTED;
   if (N == 0 || K == 0) return FLUX_OK;
   if (w == nullptr || q == nullptr || scales == nullptr) return FLUX_ERR_INVALID_ARG;
   if (!aligned16(w) || !aligned16(q) || !aligned16(scales)) return FLUX_ERR_UNSUPPORTED;
