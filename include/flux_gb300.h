@@ -604,7 +604,7 @@ flux_status_t flux_block_norm_bwd(int R, int T, int H, flux_dtype_t dtype, int p
  * Odd rows follow the gate: a NaN score counts as -inf; where the largest score
  * is infinite, the scores equal to it share p equally, and the token has no z
  * term.  Deterministic.  Requires 1 <= topk <= E <= FLUX_MAX_EXPERTS, seqs >= 1,
- * T % seqs == 0, finite coefficients.
+ * T % seqs == 0, T at most 2^31 - 512, T topk below 2^31, finite coefficients.
  * Workspace: flux_moe_balance_workspace_size(). */
 flux_status_t flux_moe_balance_loss(int T, int E, int topk, int seqs, float balance_coef,
                                     float z_coef, const float* logits, const int32_t* topk_ids,

@@ -21,6 +21,7 @@
 // largest score is infinite the scores equal to it share p equally (all -inf:
 // every expert).  Such a token has no z term and its scores get no gradient (p
 // is constant around it).
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -214,7 +215,7 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
   __shared__ int flag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT, tg = lane / LPT;
   const int item = blockIdx.x, seq = item / a.sub, E = a.E;
-  const int t0 = seq * a.per + (item - seq * a.sub) * a.chunk, t1 = min(t0 + a.chunk, (seq + 1) * a.per);
+  const int t0 = seq * a.per + (item - seq * a.sub) * a.chunk, t1 = t0 + min(a.chunk, (seq + 1) * a.per - t0);
   wait_for_previous();
   for (int e = threadIdx.x; e < WIDE; e += RT_THREADS) cnt[e] = 0;
   __syncthreads();
@@ -531,7 +532,7 @@ router_bwd_kernel(const __grid_constant__ RouterBwdArgs a) {
   __shared__ alignas(16) float gate[RT_WARPS * L::TPW][WIDE];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT, tg = lane / LPT;
   const int item = blockIdx.x, seq = item / a.sub, E = a.E;
-  const int t0 = seq * a.per + (item - seq * a.sub) * a.chunk, t1 = min(t0 + a.chunk, (seq + 1) * a.per);
+  const int t0 = seq * a.per + (item - seq * a.sub) * a.chunk, t1 = t0 + min(a.chunk, (seq + 1) * a.per - t0);
   float* g = gate[warp * L::TPW + tg];
   wait_for_previous();
   const bool gates = a.dweights != nullptr;
@@ -666,15 +667,15 @@ auto by_experts(int E, F&& f) {
 template <bool FORWARD>
 int most_items(int E, int per, int S) {
   const int tokens = by_experts<FORWARD>(E, [](auto lpt, auto, auto) { return RT_WARPS * 32 / decltype(lpt)::value; });
-  return std::max(1, std::min((FORWARD ? RT_FWD_CTAS : RT_BWD_CTAS) / S, (per + tokens - 1) / tokens));
+  return std::max(1, std::min((FORWARD ? RT_FWD_CTAS : RT_BWD_CTAS) / S, ceil_div(per, tokens)));
 }
 
 // Items of a sequence, equal but for the last.
 template <bool FORWARD>
 void cut_tokens(int E, int per, int S, int* sub, int* chunk) {
   *sub = most_items<FORWARD>(E, per, S);
-  *chunk = (per + *sub - 1) / *sub;
-  *sub = (per + *chunk - 1) / *chunk;
+  *chunk = ceil_div(per, *sub);
+  *sub = ceil_div(per, *chunk);
 }
 
 BalancePlan balance_plan(int T, int E, int S) {
@@ -705,8 +706,11 @@ BalancePlan balance_plan(int T, int E, int S) {
   return p;
 }
 
+// the kernels count tokens in ints up to a CTA's group past the last one
+constexpr int RT_MAX_TOKENS = INT_MAX - 2 * RT_THREADS + 1;
+
 bool router_sizes_ok(int T, int E, int topk, int seqs) {
-  return T >= 0 && E >= 1 && E <= FLUX_MAX_EXPERTS && topk >= 1 && topk <= E && seqs >= 1 && T % seqs == 0 &&
+  return T >= 0 && T <= RT_MAX_TOKENS && E >= 1 && E <= FLUX_MAX_EXPERTS && topk >= 1 && topk <= E && seqs >= 1 && T % seqs == 0 &&
          static_cast<long long>(T) * topk < (1ll << 31);
 }
 
@@ -738,7 +742,7 @@ extern "C" flux_status_t flux_moe_balance_loss(int T, int E, int topk, int seqs,
     if ((e = cudaMemsetAsync(loss, 0, 2 * sizeof(float), s)) != cudaSuccess ||
         (e = cudaMemsetAsync(counts, 0, n * sizeof(int32_t), s)) != cudaSuccess ||
         (e = cudaMemsetAsync(probs, 0, n * sizeof(float), s)) != cudaSuccess ||
-        (e = cudaMemsetAsync(tokens, 0, (seqs + 1) * sizeof(int32_t), s)) != cudaSuccess)
+        (e = cudaMemsetAsync(tokens, 0, (static_cast<size_t>(seqs) + 1) * sizeof(int32_t), s)) != cudaSuccess)
       return cuda_fail(e);
     return FLUX_OK;
   }
