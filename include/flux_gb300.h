@@ -573,7 +573,8 @@ size_t flux_block_norm_workspace_size(int T, int H, int gate_rows, int gate_cols
  *   dres_scale   device float             dw_pre device float[H]
  *                written in fp32; NULL = not wanted
  * The sums over tokens are taken in a fixed order: repeat calls give the same
- * bits.  Workspace: flux_block_norm_workspace_size(). */
+ * bits.  T above 2^31 - 512 returns FLUX_ERR_UNSUPPORTED.
+ * Workspace: flux_block_norm_workspace_size(). */
 flux_status_t flux_block_norm_bwd(int R, int T, int H, flux_dtype_t dtype, int post_norm,
                                   int gate_rows, int gate_cols, const void* const* x_shards,
                                   const void* const* y_shards, const void* w_post, const void* gate,

@@ -28,6 +28,7 @@ namespace flux {
 
 constexpr int BLOCK_MAX_H = FLUX_BLOCK_MAX_H;
 constexpr int BN_SMS = 152;  // the backward grid: one wave on them
+constexpr int BWD_MAX_ROWS = INT_MAX - 511;  // the backward pass counts rows in ints up to the teams of a CTA past the last one
 
 struct BlockNormArgs {
   const void* x[FLUX_MAX_RANKS];
@@ -893,7 +894,7 @@ flux_status_t launch_fwd_form(const BlockNormArgs& a, const DeviceInfo& dev, cud
   static OncePerDevice once;
   const cudaError_t attr = once(dev.device, [] { return allow_smem(kernel, S::SMEM); });
   if (attr != cudaSuccess) return cuda_fail(attr);
-  const int grid = std::min((a.T + Team<W>::COUNT - 1) / Team<W>::COUNT, dev.sm_count * S::CTAS);
+  const int grid = std::min(ceil_div(a.T, Team<W>::COUNT), dev.sm_count * S::CTAS);
   const cudaError_t e = launch_behind(kernel, dim3(grid), Team<W>::CTA, S::SMEM, s, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
@@ -971,7 +972,7 @@ extern "C" flux_status_t flux_block_norm(int R, int T, int H, flux_dtype_t dtype
 }
 
 extern "C" size_t flux_block_norm_workspace_size(int T, int H, int gate_rows, int gate_cols) {
-  if (T < 0 || H < 0 || H % 8 != 0 || H > BLOCK_MAX_H || gate_rows < 0 || gate_cols < 0) return 0;
+  if (T < 0 || T > BWD_MAX_ROWS || H < 0 || H % 8 != 0 || H > BLOCK_MAX_H || gate_rows < 0 || gate_cols < 0) return 0;
   if (gate_rows > 0 && gate_cols > 0 && (T % gate_rows != 0 || (gate_cols != 1 && gate_cols != H))) return 0;
   if (T == 0 || H == 0) return WS_HEADER;
   return bwd_plan(T, H, gate_cols > 0 ? gate_rows : 0, gate_cols).total;
@@ -987,6 +988,7 @@ extern "C" flux_status_t flux_block_norm_bwd(int R, int T, int H, flux_dtype_t d
   flux_status_t st = check_common(R, T, H, dtype, post_norm, gate_rows, gate_cols, y_shards != nullptr,
                                   du != nullptr, w_post, gate, res_scale, w_pre);
   if (st != FLUX_OK) return st;
+  if (T > BWD_MAX_ROWS) return FLUX_ERR_UNSUPPORTED;
   const bool has_y = y_shards != nullptr;
   if (has_y != (dy != nullptr)) return FLUX_ERR_INVALID_ARG;
   // a gradient that is asked for needs what it is the gradient of
