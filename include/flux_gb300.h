@@ -648,9 +648,12 @@ flux_status_t flux_moe_router_bwd(int T, int E, int topk, int seqs, float balanc
  *   scales   device [E x ceil(K / group) x N] in dtype
  * Sums in fp32, the scale of a group applied to its exact sum of x (code - 8).
  * Requires N % 8 == 0, K % 8 == 0, group % 32 == 0, N and K at most 2^31 - 1024
- * (FLUX_ERR_UNSUPPORTED).  More
- * than FLUX_W4_MAX_ROWS rows (M, or T topk) return FLUX_ERR_UNSUPPORTED: such
- * products are bound by arithmetic and belong to the 16-bit GEMMs. */
+ * (FLUX_ERR_UNSUPPORTED), and at most FLUX_W4_MAX_ROWS rows (M, or T topk; else
+ * FLUX_ERR_UNSUPPORTED).  Made for few rows: past 32 rows of one matrix its codes
+ * are read again for each 32 of them, and flux_gemm with 16-bit weights is faster
+ * from somewhere between 64 (K 28672, N 8192) and 512 rows (4096 x 4096).
+ * These calls take whole matrices and rows; unlike the layers above they know no
+ * ranks and do no ReduceScatter. */
 
 /* Bytes of q for E experts of K inputs and N outputs; 0 for invalid sizes. */
 size_t flux_w4_weight_bytes(int E, int K, int N);

@@ -79,7 +79,7 @@ __host__ __device__ __forceinline__ int cta_of_row(int T, int ctas, int t) {
 // in the backward pass below every thread copies its own columns of the rows to
 // come into its own slots of shared memory, and holds x' between its two sums
 // in registers.  Bound by HBM: 32768 x 4096 bf16, post and pre norm, in 8 shards,
-// 163 us, 6.6 TB/s.
+// 162 us, 6.6 TB/s.
 template <int W, int V>
 struct FwdShape {
   static constexpr int ROW = Team<W>::CTA * V * 32;  // bytes of two tensors' rows, all teams of the CTA
@@ -247,7 +247,11 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
 //
 // Bound by latency: the registers that hold the weights and column sums leave 12
 // to 16 warps on an SM, which meet twice a row.  32768 x 4096 bf16: 312 us with
-// the joining kernel, 5.2 TB/s; 4061 x 12288 f16 with 31 gate rows: 154 us, 3.9.
+// the joining kernel, 5.2 TB/s; 4061 x 12288 f16 with 31 gate rows: 152 us, 4.0.
+// Where every row or every few rows have a gate row of their own, the runs' ends
+// cost more than their rows: 32768 x 4096 with as many gate rows 730 us, 131072 x
+// 1024, four teams a CTA of which one works at a time, 1890 (floor 356 each); with
+// a gate row for eight rows 393 and 437.
 template <int W, int V>
 struct BwdShape {
   static constexpr int ROW = Team<W>::CTA * V * 64;  // bytes of four tensors' rows, all teams of the CTA
@@ -773,11 +777,12 @@ block_norm_sums_kernel(const __grid_constant__ BlockNormArgs a, int col_blocks, 
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// Calls f(W, V) for the team that holds a row of H columns.  The steps are close
-// enough that a third of the lanes idle at most (2^27 elements in rows of 5120:
-// backward 354 us, in teams of 16 warps 401; of 1280: 278, 4 warps 399; of 2560:
-// 287, 8 warps 373).  A warp with two vectors is fast enough forward but spills
-// backward (H 512: 456 us, two warps of one vector 266).
+// Calls f(W, V) for the team that holds a row of H columns.  From 1032 columns on
+// the steps are close enough that a third of the lanes idle at most (2^27 elements
+// in rows of 5120: backward 353 us, in teams of 16 warps 401; of 1280: 278, 4 warps
+// 399; of 2560: 287, 8 warps 373); just past 256 and 512 columns half of them do.
+// A warp with two vectors is fast enough forward but spills backward (H 512: 456
+// us, two warps of one vector 266).
 template <bool BACKWARD, typename F>
 auto by_width(int H, F&& f) {
   const int nvec = H / 8;

@@ -82,8 +82,9 @@ struct Lanes {
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
-// The hardware's 2^x, log2 x and 1 / x (relative error about 2^-22; results below
-// 2^-126 are 0).
+// The hardware's 2^x and 1 / x (relative error about 2^-22; results below 2^-126
+// are 0) and log2 x, whose error near x = 1 is about 2^-22 absolute: it is added to
+// the largest score.
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -199,8 +200,8 @@ __device__ __forceinline__ void join_losses(const BalanceArgs& a, int n, float* 
 // a sequence's over its items by balance_join_kernel, or, where there is one
 // sequence of few items, by the last of their CTAs; all in fixed orders.
 //
-// Bound by issue slots next to HBM (an exponential and two sums per score):
-// 131072 x 256 in 64 masked sequences 30.3 us with the joining kernel, 4.6 TB/s
+// Bound by latency, with one group of tokens ahead in registers (issue slots 58 %,
+// DRAM 65 %): 131072 x 256 in 64 masked sequences 30.6 us with the joining kernel, 4.6 TB/s
 // (sums in double precision took 462); 4096 x 8 in one launch 5.9 us.
 template <int LPT, int V, bool VEC>
 __global__ void __launch_bounds__(RT_THREADS, V <= 4 ? 3 : 2)
@@ -523,7 +524,7 @@ struct RouterBwdArgs {
 // Backward: one read of the scores, one write of their gradient.  A CTA stays in
 // one sequence, whose counts its lanes hold; the gate's terms of a token meet
 // the others through a row of shared memory.  Bound by HBM: 131072 x 256 49 us,
-// 5.7 TB/s.
+// 5.8 TB/s.
 template <int LPT, int V, bool VEC>
 __global__ void __launch_bounds__(RT_THREADS, V <= 2 ? 5 : 2)
 router_bwd_kernel(const __grid_constant__ RouterBwdArgs a) {

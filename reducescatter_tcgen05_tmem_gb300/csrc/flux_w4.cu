@@ -101,7 +101,8 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t b
 
 // The eight codes of a word less 8 as pairs of 16-bit values: nibbles i and
 // i + 4 in pair i.  A code in the low bits of a power of two's significand is
-// that power plus the code; the difference is exact.
+// that power plus the code; the difference is exact (the method is published, in
+// Kim et al., "Who Says Elephants Can't Run", 2022).
 template <int DT>
 __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&p)[4]) {
   if constexpr (DT == 1) {
@@ -614,9 +615,9 @@ __global__ void __launch_bounds__(W4_JOIN_WARPS * 32) w4_join_kernel(const __gri
 // One thread per four columns and group: the group's largest magnitude / 7,
 // rounded to 16 bits, is its scale; codes are the nearest multiples of it.  Eight
 // loads of 8 bytes are on their way together; the second reading of a group comes
-// from L1 or L2.  Run once per weight, bound by its stores (words 64 bytes of a
-// column apart; a group need not be whole runs): 8 x 4096 x 14336 in groups of 128
-// 569 us, 2.1 TB/s; a column a thread took 844.
+// from L1 or L2.  Run once per weight; its stores are words 64 bytes of a column
+// apart, which fill 4 bytes of a sector each: 8 x 4096 x 14336 in groups of 128
+// 571 us, 2.1 TB/s; a column a thread took 844.
 constexpr int W4_QUANT_COLS = 4;
 
 template <int DT>
@@ -678,7 +679,8 @@ w4_quantize_kernel(int K, int N, int runs, int group, int groups, const uint16_t
   }
 }
 
-// Workspace: header, how the units were cut, the slots' tiles, sums of cut tiles, fp32 rows (layer1).
+// Workspace: header, how the units were cut, the slots' tiles, sums of cut tiles, fp32
+// rows (used by layer1; the size is the same for all three products).
 struct W4Ws {
   size_t split, where, parts, rows, total;
 };
