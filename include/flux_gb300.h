@@ -22,6 +22,9 @@
  *     norms before and after a block, gate, residual         flux_block_norm(_bwd)
  *     the router's losses, counts and score gradient         flux_moe_balance_loss, flux_moe_router_bwd
  *     products of few rows with 4-bit weights                flux_w4_gemv, flux_moe_w4_layer0 / _layer1
+ *     layer norm, dropout and residual around a block        flux_layer_norm(_bwd)
+ *     routing with expert groups, and its gradient           flux_moe_group_gate(_bwd)
+ *     products in 8-bit integers                             flux_q8_quantize, flux_q8_gemm
  * plus the plain non-split GEMM that the effective-communication-time metric
  * ECT = OverallTime - GEMM_non-split is measured against (paper review,
  * section 三, "核心公式"): flux_gemm.  The operator list is the one the Flux
@@ -56,7 +59,8 @@
  *   - Workspaces must be 256-byte aligned, at least flux_*workspace_size()
  *     bytes, and zero-filled once before first use (flux_workspace_init).
  *     Every successful call leaves its workspace zero again (the MoE layers leave
- *     their routing and staged rows in it).  The block-norm, router and 4-bit
+ *     their routing and staged rows in it, flux_q8_gemm of more than 32 rows its
+ *     widened operands).  The block-norm, layer-norm, router, 4-bit and 8-bit
  *     calls need zeros in the first 256 bytes only.  Calls that share
  *     one workspace must be ordered on the GPU (same stream or events); calls
  *     that overlap on the GPU need separate workspaces.
@@ -73,7 +77,8 @@ extern "C" {
 
 #define FLUX_MAX_RANKS 16
 #define FLUX_MAX_EXPERTS 1024
-#define FLUX_BLOCK_MAX_H 16384 /* widest row of flux_block_norm */
+#define FLUX_MAX_GROUPS 32     /* most expert groups of flux_moe_group_gate */
+#define FLUX_BLOCK_MAX_H 16384 /* widest row of flux_block_norm and flux_layer_norm */
 #define FLUX_W4_MAX_ROWS 1024  /* most rows (tokens x topk) of a product with 4-bit weights */
 
 typedef enum {
@@ -87,6 +92,9 @@ typedef enum {
 } flux_status_t;
 
 typedef enum { FLUX_F16 = 0, FLUX_BF16 = 1 } flux_dtype_t;
+
+/* Score functions of flux_moe_group_gate. */
+typedef enum { FLUX_SCORE_SOFTMAX = 0, FLUX_SCORE_SIGMOID = 1 } flux_score_t;
 
 typedef enum {
   FLUX_OP_GEMM = 0,
@@ -694,6 +702,152 @@ flux_status_t flux_moe_w4_layer1(int T, int H, int F, int E, int topk, int group
                                  const void* h, const void* q2, const void* scales2,
                                  const int32_t* topk_ids, const float* topk_weights, void* out,
                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- layer norm and dropout around a block
+ *
+ * One pass over the residual stream between two blocks: the finished block's
+ * output y is dropped out and added to the residual stream x, and the sum is
+ * normalised for the next block.  Per token, means over the H columns, in fp32:
+ *     x' = x + drop(y)
+ *     u  = (x' - m) r weight + bias,   m = mean(x'), r = 1 / sqrt(mean((x' - m)^2) + eps)
+ * x' and u are rounded once each; u is computed from the unrounded x'.
+ * drop(y) keeps an element with probability keep / 65536, where keep is
+ * (1 - p) 65536 to the nearest integer, and multiplies it by 65536 / keep; the
+ * others are 0, whatever they held.  Element i = t H + h (t over all shards) is
+ * kept where its 16 bits are below keep: those of the Philox4x32-10 block with
+ * key (seed, low word first) and counter (i / 8 in the first two words, the offset
+ * in the others, low words first), of which word (i % 8) / 2 holds element i in
+ * its low (i even) or high half.  The backward pass makes the same bits again; no
+ * mask is stored.  A program takes another offset for every call (layer, step). */
+
+/*   p            share to drop, 0 <= p < 1; 0 (then rng is NULL) = none.  A p so
+ *                near 1 that keep is 0 returns FLUX_ERR_INVALID_ARG.
+ *   x_shards[s]  device, [T/R x H]: the rows of the residual stream owned by rank s;
+ *                the array NULL = zeros (only with y)
+ *   y_shards     [T/R x H] each: the block's output; the array NULL = no block
+ *                before this norm (x' = x; then p is 0 and x_out NULL)
+ *   rng          device uint64[2], 16-byte aligned: seed, offset.  On the device, so
+ *                that a captured step replays with the numbers it finds there.
+ *   weight, bias device [H] in dtype, or NULL = ones, zeros
+ *   x_out[s]     x' [T/R x H]; may be x_shards[s] or y_shards[s]
+ *   u_out[s]     u  [T/R x H]; may be y_shards[s], or x_shards[s] without y; the array
+ *                NULL = no next norm (then weight, bias, mean and rstd are NULL too)
+ *   mean, rstd   device float[T]: m and r for the backward pass, or NULL
+ * Requires T % R == 0, H % 8 == 0 and H <= FLUX_BLOCK_MAX_H (else
+ * FLUX_ERR_UNSUPPORTED), eps finite and >= 0.  A call with neither y nor u, or
+ * with an argument of a part that it leaves out, returns FLUX_ERR_INVALID_ARG.
+ * Needs no workspace; deterministic. */
+flux_status_t flux_layer_norm(int R, int T, int H, flux_dtype_t dtype, float p, float eps,
+                              const void* const* x_shards, const void* const* y_shards,
+                              const uint64_t* rng, const void* weight, const void* bias,
+                              void* const* x_out, void* const* u_out, float* mean, float* rstd,
+                              void* stream);
+
+/* Bytes of workspace flux_layer_norm_bwd needs; 0 for invalid sizes. */
+size_t flux_layer_norm_workspace_size(int T, int H);
+
+/* Gradients of flux_layer_norm from those of x' and u, with the norm taken of the
+ * stored x':  g = weight du, n = (x' - m) r,
+ *     d = dx_out + r (g - mean(g) - n mean(g n)),   dx = d,   dy = drop(d)
+ *   p, rng       as the forward call had them (the offset too); both are needed for
+ *                dy only, but have to fit together always
+ *   x_out[s]     x' [T/R x H] as the forward call wrote it (x itself without y)
+ *   weight       as the forward call had it;  mean, rstd  as it wrote them
+ *   dx_out[s]    gradient of x' [T/R x H]; the array NULL = zeros
+ *   du[s]        gradient of u [T/R x H]; the array NULL = the call had no u (then
+ *                x_out, weight, mean, rstd, dweight and dbias are NULL too)
+ *   dx[s], dy[s] device [T/R x H] in dtype: gradients of x and y; either array may be
+ *                NULL (without dropout dy is dx).  Each may be x_out[s], dx_out[s] or
+ *                du[s], but not the other.
+ *   dweight, dbias  device float[H], written in fp32; NULL = not wanted
+ * The sums over tokens are taken in a fixed order: repeat calls give the same
+ * bits.  T above 2^31 - 512 returns FLUX_ERR_UNSUPPORTED.
+ * Workspace: flux_layer_norm_workspace_size(). */
+flux_status_t flux_layer_norm_bwd(int R, int T, int H, flux_dtype_t dtype, float p,
+                                  const void* const* x_out, const uint64_t* rng, const void* weight,
+                                  const float* mean, const float* rstd, const void* const* dx_out,
+                                  const void* const* du, void* const* dx, void* const* dy,
+                                  float* dweight, float* dbias, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- routing with expert groups
+ *
+ * Top-k routing of T tokens over E experts in `groups` groups of neighbours
+ * (experts g E/groups ..), as flux_moe_topk_gate but with
+ *     s = sigmoid(logits) or softmax(logits) over all E          (score)
+ *     c = s + bias, or the logits themselves without a bias: what the choice goes by
+ * A group's rank is the sum of its group_top (1 or 2) largest c (of the scores
+ * without a bias and with group_top 2; all of them where a group has fewer
+ * experts).  The topk_groups groups of highest rank are kept, then the topk
+ * largest c of their experts are chosen, largest first; ties go to the lowest
+ * index, of groups and of experts.  The weights are
+ *     scale s[id_j], or scale s[id_j] / (sum of the chosen s) with renorm
+ * The choice is that of s, c and the ranks in double precision (the logits, the
+ * bias and the rounding of 64-bit arithmetic as given); the weights are fp32. */
+
+/*   logits       device float32[T x E]
+ *   bias         device float32[E], or NULL: moves the choice, not the weights; no NaN
+ *   topk_ids     device int32[T x topk]     topk_weights  device float32[T x topk]
+ * Odd rows: a NaN logit counts as -inf; softmax where the largest logit is infinite:
+ * the logits equal to it share equally.  Renormalised softmax weights go by the
+ * chosen logits alone: with an infinite one among them, those equal to the largest
+ * share equally; renormalised sigmoid weights share equally where all chosen
+ * logits are -inf.  Deterministic; needs no workspace.
+ * Requires 1 <= topk <= topk_groups E / groups, E <= FLUX_MAX_EXPERTS, groups <=
+ * FLUX_MAX_GROUPS, E % groups == 0, 1 <= topk_groups <= groups, a finite scale;
+ * else, or with a NULL buffer (T > 0), FLUX_ERR_INVALID_ARG. */
+flux_status_t flux_moe_group_gate(int T, int E, int topk, int score, int groups, int topk_groups,
+                                  int group_top, int renorm, float scale, const float* logits,
+                                  const float* bias, int32_t* topk_ids, float* topk_weights,
+                                  void* stream);
+
+/* Gradient of the logits from that of the weights (the choice is constant, and the
+ * bias has no gradient).
+ *   topk_ids     as flux_moe_group_gate wrote them: no expert twice in a token; an id
+ *                outside [0, E) adds nothing
+ *   dweights     device float32[T x topk]: gradient of topk_weights
+ *   accumulate   nonzero: added to what dlogits holds (the gradient of a loss of
+ *                flux_moe_router_bwd, for instance)
+ *   dlogits      device float32[T x E]; without accumulate written whole, zeros where
+ *                nothing arrives
+ * Where weights are shared equally by one of the rules for odd rows they do not
+ * depend on the logits: no gradient.  Deterministic; needs no workspace. */
+flux_status_t flux_moe_group_gate_bwd(int T, int E, int topk, int score, int renorm, float scale,
+                                      const float* logits, const int32_t* topk_ids,
+                                      const float* dweights, int accumulate, float* dlogits,
+                                      void* stream);
+
+/* ---------------------------------------------------------------- products in 8-bit integers
+ *
+ * out[m, n] = x_scales[m] w_scales[n] sum_k x[m, k] w[n, k] (+ bias[n]): a linear
+ * layer whose weights are held in 8 bits with a scale for each output channel and
+ * whose inputs are quantised token by token as they come.
+ * Requires K % 16 == 0, K < 131072, N % 8 == 0, N <= 2^30 (FLUX_ERR_UNSUPPORTED).
+ * These calls take whole matrices and rows; they know no ranks. */
+
+/* 8-bit codes and the scale of each of `rows` rows of 16-bit numbers:
+ *   x      device [rows x K] in dtype: tokens, or the weights of a layer row by
+ *          output channel
+ *   q      device int8[rows x K]        scales  device float[rows]
+ * scale = largest magnitude of the row / 127 in fp32; code = the nearest integer to
+ * x / scale (the quotient of the real numbers, ties to even), 0 where the scale is
+ * 0.  A row that holds a NaN or an infinity gets that as its scale and codes of
+ * zero, so that its products are NaN. */
+flux_status_t flux_q8_quantize(int rows, int K, flux_dtype_t dtype, const void* x, int8_t* q,
+                               float* scales, void* stream);
+
+/* Bytes of workspace flux_q8_gemm needs; 0 for invalid sizes. */
+size_t flux_q8_workspace_size(int M, int N, int K);
+
+/*   x  device int8[M x K]   x_scales  device float[M]
+ *   w  device int8[N x K]   w_scales  device float[N]   bias  device [N] in dtype, or NULL
+ *   out  device [M x N] in dtype
+ * The integer sums are exact for M <= 32; for more rows as long as they stay below
+ * 2^24, past that to 24 bits.  K = 0 writes the bias, or zeros. */
+flux_status_t flux_q8_gemm(int M, int N, int K, flux_dtype_t dtype, const int8_t* x,
+                           const float* x_scales, const int8_t* w, const float* w_scales,
+                           const void* bias, void* out, void* workspace, size_t workspace_bytes,
+                           void* stream);
 
 /* ---------------------------------------------------------------- tuning
  *

@@ -8,3 +8,4 @@ product path.
 """
 from .flux_oracle import *  # noqa: F401,F403
 from .block_oracle import *  # noqa: F401,F403
+from .edge_oracle import *  # noqa: F401,F403

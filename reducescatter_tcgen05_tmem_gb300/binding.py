@@ -39,6 +39,9 @@ FLUX_ERR_NO_DEVICE = 6
 FLUX_F16 = 0
 FLUX_BF16 = 1
 
+FLUX_SCORE_SOFTMAX = 0
+FLUX_SCORE_SIGMOID = 1
+
 FLUX_OP_GEMM = 0
 FLUX_OP_AG_GEMM = 1
 FLUX_OP_GEMM_RS = 2
@@ -52,6 +55,7 @@ FLUX_OP_AG_GEMM_PUSH = 9
 
 FLUX_MAX_RANKS = 16
 FLUX_MAX_EXPERTS = 1024
+FLUX_MAX_GROUPS = 32
 FLUX_BLOCK_MAX_H = 16384
 FLUX_W4_MAX_ROWS = 1024
 FLUX_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -149,6 +153,15 @@ _SIGS = {
     "flux_w4_gemv": ([_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
     "flux_moe_w4_layer0": ([_i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
     "flux_moe_w4_layer1": ([_i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
+    "flux_layer_norm": ([_i, _i, _i, _i, _f, _f, _vpp, _vpp, _vp, _vp, _vp, _vpp, _vpp, _vp, _vp, _vp], _i),
+    "flux_layer_norm_workspace_size": ([_i, _i], _sz),
+    "flux_layer_norm_bwd": ([_i, _i, _i, _i, _f, _vpp, _vp, _vp, _vp, _vp, _vpp, _vpp, _vpp, _vpp, _vp, _vp, _vp,
+                             _sz, _vp], _i),
+    "flux_moe_group_gate": ([_i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp], _i),
+    "flux_moe_group_gate_bwd": ([_i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _i, _vp, _vp], _i),
+    "flux_q8_quantize": ([_i, _i, _i, _vp, _vp, _vp, _vp], _i),
+    "flux_q8_workspace_size": ([_i, _i, _i], _sz),
+    "flux_q8_gemm": ([_i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -462,6 +475,57 @@ def flux_moe_w4_layer1(T, H, F, E, topk, group, dtype, h, q2, scales2, topk_ids,
     _check(_lib.flux_moe_w4_layer1(T, H, F, E, topk, group, dtype, _ptr(h), _ptr(q2), _ptr(scales2),
                                    _ptr(topk_ids), _ptr(topk_weights), _ptr(out), _ptr(workspace),
                                    _nbytes(workspace), _stream(stream)), "flux_moe_w4_layer1")
+
+
+def flux_layer_norm_workspace_size(T: int, H: int) -> int:
+    return int(_lib.flux_layer_norm_workspace_size(T, H))
+
+
+def flux_layer_norm(R, T, H, dtype, p, eps, x_shards, y_shards, rng, weight, bias, x_out, u_out, mean=None, rstd=None,
+                    stream=None) -> None:
+    """Dropout, residual and the next block's layer norm in one pass."""
+    _check(_lib.flux_layer_norm(R, T, H, dtype, p, eps, _optional_ptrs(x_shards), _optional_ptrs(y_shards), _ptr(rng),
+                                _ptr(weight), _ptr(bias), _optional_ptrs(x_out), _optional_ptrs(u_out), _ptr(mean),
+                                _ptr(rstd), _stream(stream)), "flux_layer_norm")
+
+
+def flux_layer_norm_bwd(R, T, H, dtype, p, x_out, rng, weight, mean, rstd, dx_out, du, dx, dy, dweight, dbias,
+                        workspace, stream=None) -> None:
+    """Gradients of flux_layer_norm."""
+    _check(_lib.flux_layer_norm_bwd(
+        R, T, H, dtype, p, _optional_ptrs(x_out), _ptr(rng), _ptr(weight), _ptr(mean), _ptr(rstd), _optional_ptrs(dx_out),
+        _optional_ptrs(du), _optional_ptrs(dx), _optional_ptrs(dy), _ptr(dweight), _ptr(dbias), _ptr(workspace),
+        _nbytes(workspace), _stream(stream)), "flux_layer_norm_bwd")
+
+
+def flux_moe_group_gate(T, E, topk, score, groups, topk_groups, group_top, renorm, scale, logits, bias, topk_ids,
+                        topk_weights, stream=None) -> None:
+    """Expert ids and weights of routing with groups."""
+    _check(_lib.flux_moe_group_gate(T, E, topk, score, groups, topk_groups, group_top, renorm, scale, _ptr(logits),
+                                    _ptr(bias), _ptr(topk_ids), _ptr(topk_weights), _stream(stream)),
+           "flux_moe_group_gate")
+
+
+def flux_moe_group_gate_bwd(T, E, topk, score, renorm, scale, logits, topk_ids, dweights, accumulate, dlogits,
+                            stream=None) -> None:
+    """Gradient of the logits from the gradient of flux_moe_group_gate's weights."""
+    _check(_lib.flux_moe_group_gate_bwd(T, E, topk, score, renorm, scale, _ptr(logits), _ptr(topk_ids), _ptr(dweights),
+                                        accumulate, _ptr(dlogits), _stream(stream)), "flux_moe_group_gate_bwd")
+
+
+def flux_q8_quantize(rows, K, dtype, x, q, scales, stream=None) -> None:
+    """8-bit codes and a scale for each row of 16-bit numbers."""
+    _check(_lib.flux_q8_quantize(rows, K, dtype, _ptr(x), _ptr(q), _ptr(scales), _stream(stream)), "flux_q8_quantize")
+
+
+def flux_q8_workspace_size(M: int, N: int, K: int) -> int:
+    return int(_lib.flux_q8_workspace_size(M, N, K))
+
+
+def flux_q8_gemm(M, N, K, dtype, x, x_scales, w, w_scales, bias, out, workspace, stream=None) -> None:
+    """out = x . w^T of 8-bit codes, times the rows' and the channels' scales."""
+    _check(_lib.flux_q8_gemm(M, N, K, dtype, _ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(bias), _ptr(out),
+                             _ptr(workspace), _nbytes(workspace), _stream(stream)), "flux_q8_gemm")
 
 
 def _tuned(st, what, best):

@@ -22,13 +22,12 @@
 #include <type_traits>
 
 #include "flux_host.h"
+#include "flux_norm.cuh"
 #include "flux_rows.cuh"
 
 namespace flux {
 
 constexpr int BLOCK_MAX_H = FLUX_BLOCK_MAX_H;
-constexpr int BN_SMS = 152;  // the backward grid: one wave on them
-constexpr int BWD_MAX_ROWS = INT_MAX - 511;  // the backward pass counts rows in ints up to the teams of a CTA past the last one
 
 struct BlockNormArgs {
   const void* x[FLUX_MAX_RANKS];
@@ -56,20 +55,6 @@ struct BlockNormArgs {
 
 namespace {
 
-// A row is held by a team of W warps; a CTA has one to eight teams.  Where a team
-// has three warps or more, CTAs of one team are faster than CTAs of several
-// (2^27 elements in rows of 1792: backward 278 us, two teams 339; forward 164, 212).
-template <int W>
-struct Team {
-  static constexpr int THREADS = W * 32;
-  static constexpr int CTA = W <= 2 ? 256 : W * 32;
-  static constexpr int COUNT = CTA / THREADS;
-};
-
-// CTA c of `ctas` takes the rows [first_row(c), first_row(c + 1)).
-__host__ __device__ __forceinline__ int first_row(int T, int ctas, int c) {
-  return static_cast<int>(static_cast<long long>(c) * T / ctas);
-}
 // The CTA that has row t.
 __host__ __device__ __forceinline__ int cta_of_row(int T, int ctas, int t) {
   return static_cast<int>(((t + 1ll) * ctas - 1) / T);
@@ -653,17 +638,11 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
   }
 }
 
-constexpr int SUM_COLS = 32, SUM_WARPS = 8, SUM_BATCH = 20;
-
-constexpr int SUM_THREADS = SUM_COLS * SUM_WARPS;
 // blocks of block_norm_sums_kernel: dw_pre and dw_post by columns, the scalars, cut runs by columns
-inline int sum_blocks(int H) { return (H + SUM_COLS - 1) / SUM_COLS; }
 inline int run_blocks(int H) { return (H + 4 * SUM_THREADS - 1) / (4 * SUM_THREADS); }
 
 // Joins the CTAs' partial sums, each column in a fixed order, and leaves the
-// partial sums zero.  SUM_BATCH loads of a thread are on their way together: a few
-// MB from L2 are bound by latency (H 4096, 304 CTAs: 16 us with cold caches; one
-// load after the other took 300).
+// partial sums zero (H 4096, 304 CTAs: 16 us with cold caches).
 template <int DT>
 __global__ void __launch_bounds__(SUM_THREADS)
 block_norm_sums_kernel(const __grid_constant__ BlockNormArgs a, int col_blocks, int per_run_blocks) {
@@ -676,30 +655,8 @@ block_norm_sums_kernel(const __grid_constant__ BlockNormArgs a, int col_blocks, 
     if (is_pre ? !a.has_u : !a.has_y) return;
     float* src = is_pre ? a.part_pre : a.part_post;
     const int col = (is_pre ? blockIdx.x : blockIdx.x - col_blocks) * SUM_COLS + lane;
-    float s = 0.0f;
-    if (col < a.H) {
-      // the loads of a batch are in flight together: one after another, each
-      // behind the store of the last, they cost more than all the rest
-      for (int i0 = warp; i0 < a.ctas; i0 += SUM_WARPS * SUM_BATCH) {
-        float v[SUM_BATCH];
-#pragma unroll
-        for (int j = 0; j < SUM_BATCH; ++j) {
-          const int i = i0 + j * SUM_WARPS;
-          v[j] = i < a.ctas ? src[static_cast<size_t>(i) * a.H + col] : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < SUM_BATCH; ++j) {
-          const int i = i0 + j * SUM_WARPS;
-          if (i < a.ctas) src[static_cast<size_t>(i) * a.H + col] = 0.0f;
-          s += v[j];
-        }
-      }
-    }
-    part[warp][lane] = s;
-    __syncthreads();
+    const float s = column_sum(src, a.ctas, a.H, col, warp, lane, part);
     if (warp != 0 || col >= a.H) return;
-#pragma unroll
-    for (int w = 1; w < SUM_WARPS; ++w) s += part[w][lane];
     if (is_pre) {
       if (a.dw_pre != nullptr) a.dw_pre[col] = s;
     } else {
@@ -774,34 +731,6 @@ block_norm_sums_kernel(const __grid_constant__ BlockNormArgs a, int col_blocks, 
   *reinterpret_cast<float4*>(a.dgate + static_cast<size_t>(run) * a.H + col) = s;
 }
 
-template <int N>
-using Int = std::integral_constant<int, N>;
-
-// Calls f(W, V) for the team that holds a row of H columns.  From 1032 columns on
-// the steps are close enough that a third of the lanes idle at most (2^27 elements
-// in rows of 5120: backward 353 us, in teams of 16 warps 401; of 1280: 278, 4 warps
-// 399; of 2560: 287, 8 warps 373); just past 256 and 512 columns half of them do.
-// A warp with two vectors is fast enough forward but spills backward (H 512: 456
-// us, two warps of one vector 266).
-template <bool BACKWARD, typename F>
-auto by_width(int H, F&& f) {
-  const int nvec = H / 8;
-  if (nvec <= 32) return f(Int<1>{}, Int<1>{});
-  if (nvec <= 64) {
-    if constexpr (BACKWARD) return f(Int<2>{}, Int<1>{});
-    else return f(Int<1>{}, Int<2>{});
-  }
-  if (nvec <= 128) return f(Int<2>{}, Int<2>{});
-  if (nvec <= 192) return f(Int<3>{}, Int<2>{});
-  if (nvec <= 256) return f(Int<4>{}, Int<2>{});
-  if (nvec <= 384) return f(Int<6>{}, Int<2>{});
-  if (nvec <= 512) return f(Int<8>{}, Int<2>{});
-  if (nvec <= 768) return f(Int<12>{}, Int<2>{});
-  if (nvec <= 1024) return f(Int<16>{}, Int<2>{});
-  if (nvec <= 1536) return f(Int<16>{}, Int<3>{});
-  return f(Int<16>{}, Int<4>{});
-}
-
 // The backward pass's grid and workspace.
 struct BwdPlan {
   int ctas, run_rows;
@@ -832,21 +761,6 @@ BwdPlan bwd_plan(int T, int H, int gate_rows, int gate_cols) {
   p.scalar = take(scalars ? sizeof(double) * 2 * p.ctas : 0);
   p.total = at;
   return p;
-}
-
-template <typename P>
-bool shards_ok(int R, P const* shards, flux_status_t* st) {
-  for (int r = 0; r < R; ++r) {
-    if (shards[r] == nullptr) {
-      *st = FLUX_ERR_INVALID_ARG;
-      return false;
-    }
-    if (!aligned16(shards[r])) {
-      *st = FLUX_ERR_UNSUPPORTED;
-      return false;
-    }
-  }
-  return true;
 }
 
 // The rules both directions share; FLUX_OK if the call can go on.
@@ -884,12 +798,6 @@ void fill_common(BlockNormArgs* a, int R, int T, int H, int post_norm, int gate_
   a->gate_cols = gate != nullptr ? gate_cols : 0;
   a->res_scale = res_scale;
   a->w_pre = w_pre;
-}
-
-// Lets a kernel use `smem` bytes of shared memory on the current device.
-template <typename K>
-cudaError_t allow_smem(K kernel, int smem) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 template <int DT, int W, int V, bool HAS_Y>

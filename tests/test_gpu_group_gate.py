@@ -1,0 +1,240 @@
+"""GPU parity of the routing with expert groups (flux_moe_group_gate,
+flux_moe_group_gate_bwd) with its float64 definition, through the C ABI."""
+import numpy as np
+import pytest
+
+import oracle
+from tests.rounding import check32
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import reducescatter_tcgen05_tmem_gb300 as fx  # noqa: E402
+
+SCORE = {"softmax": fx.FLUX_SCORE_SOFTMAX, "sigmoid": fx.FLUX_SCORE_SIGMOID}
+
+
+class Gate:
+    def __init__(self, T, E, k, score, groups=1, kept=1, top=1, renorm=True, scale=1.0, bias=True, seed=0, logits=None):
+        r = np.random.default_rng(seed)
+        self.args = (T, E, k, SCORE[score], groups, kept, top, int(renorm), scale)
+        self.ref = (k, score, groups, kept, top, renorm, scale)
+        self.logits = r.standard_normal((T, E)).astype(np.float32) if logits is None else logits
+        if bias is True:
+            bias = (r.standard_normal(E) * (0.1 if score == "sigmoid" else 0.1 / E)).astype(np.float32)
+        self.bias = None if bias is None or bias is False else bias
+        self.cu = torch.from_numpy(self.logits).cuda()
+        self.cb = None if self.bias is None else torch.from_numpy(self.bias).cuda()
+        self.T, self.E, self.k = T, E, k
+
+    def run(self, stream=None):
+        ids = torch.full((self.T * self.k + 8,), -7, dtype=torch.int32, device="cuda")
+        w = torch.full((self.T * self.k + 8,), 7.0, device="cuda")
+        fx.flux_moe_group_gate(*self.args, self.cu, self.cb, ids, w, stream=stream)
+        torch.cuda.synchronize()
+        assert bool((ids[-8:] == -7).all()) and bool((w[-8:] == 7.0).all())
+        n = self.T * self.k
+        return ids[:n].view(self.T, self.k).cpu().numpy(), w[:n].view(self.T, self.k).double().cpu().numpy()
+
+    def check(self):
+        ids, w = self.run()
+        want_ids, want_w = oracle.group_gate(self.logits, None if self.bias is None else self.bias.astype(np.float64), *self.ref)
+        assert np.array_equal(ids, want_ids)
+        # exponentials, their sum and quotients, the arguments' rounding (up to 20 ulps of scores at most 20)
+        check32(w, want_w, np.abs(want_w), depth=128, what="weights")
+        return ids
+
+
+CASES = [
+    # T, E, k, score, groups, kept, top, renorm, scale, bias
+    (1, 1, 1, "sigmoid", 1, 1, 1, True, 1.0, True),
+    (5, 2, 1, "softmax", 2, 1, 1, False, 1.0, True),
+    (13, 256, 8, "sigmoid", 8, 4, 2, True, 2.5, True),
+    (1000, 256, 8, "sigmoid", 8, 4, 2, True, 2.5, True),
+    (333, 256, 8, "softmax", 8, 3, 1, False, 16.0, False),
+    (77, 160, 6, "softmax", 8, 3, 1, False, 1.0, True),
+    (100, 64, 6, "softmax", 8, 3, 2, True, 1.0, False),
+    (100, 64, 64, "sigmoid", 1, 1, 1, True, 1.0, True),     # every expert
+    (50, 63, 5, "sigmoid", 9, 2, 2, False, 1.0, True),      # odd sizes
+    (50, 33, 3, "softmax", 11, 4, 2, True, 1.0, True),
+    (41, 7, 3, "softmax", 7, 5, 2, True, 1.0, True),        # groups of one
+    (41, 96, 4, "sigmoid", 32, 7, 2, True, 1.0, True),      # more groups than lanes of a token... of 64 experts
+    (19, 64, 4, "sigmoid", 32, 9, 2, True, 1.0, True),
+    (29, 1024, 16, "sigmoid", 16, 16, 1, True, 1.0, True),
+    (29, 1024, 40, "softmax", 32, 11, 2, False, 1.0, True),
+    (64, 1021, 33, "softmax", 1, 1, 1, True, 1.0, True),    # prime
+    (300, 384, 8, "sigmoid", 1, 1, 1, True, 2.5, True),
+    (4099, 8, 2, "softmax", 1, 1, 1, True, 1.0, False),
+    (129, 128, 8, "sigmoid", 4, 2, 2, True, 1.0, False),    # ranks of scores, choice of logits
+    (129, 66, 8, "sigmoid", 2, 1, 1, True, 1.0, False),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(v) for v in c))
+def test_choice_and_weights(case):
+    Gate(*case, seed=3).check()
+
+
+def test_as_the_plain_gate():
+    g = Gate(500, 40, 4, "softmax", bias=None, seed=5)
+    ids, w = g.run()
+    i2, w2 = torch.empty(500, 4, dtype=torch.int32, device="cuda"), torch.empty(500, 4, device="cuda")
+    fx.flux_moe_topk_gate(500, 40, 4, g.cu, i2, w2)
+    assert np.array_equal(ids, i2.cpu().numpy())
+    np.testing.assert_allclose(w, w2.cpu().numpy(), rtol=1e-6)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("groups,kept,top", [(1, 1, 1), (8, 3, 1), (8, 3, 2)])
+@pytest.mark.parametrize("E", [64, 256])
+def test_values_closer_than_fp32(score, groups, kept, top, E):
+    # biases that bring every s + bias to within 2^-25 of one value: only 64 bits order them
+    r = np.random.default_rng(8)
+    row = r.standard_normal(E).astype(np.float32)
+    s = oracle.gate_scores(row[None], score)[0]
+    bias = (0.75 - s).astype(np.float32)
+    logits = np.tile(row, (37, 1))
+    logits[1::2] = r.standard_normal((18, E))
+    c = s + bias
+    assert np.unique(np.sort(c)).size > E // 2 and np.ptp(c) < 2.0 ** -23
+    Gate(37, E, 6, score, groups, kept, top, True, 1.0, bias=bias, logits=logits).check()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("bias", ["zero", "own", None])
+@pytest.mark.parametrize("groups,kept,top", [(1, 1, 1), (8, 2, 1), (8, 2, 2)])
+def test_equal_scores(score, bias, groups, kept, top):
+    # scores of a 16-bit router: many are equal; then rows that are equal throughout
+    r = np.random.default_rng(9)
+    logits = (np.round(r.standard_normal((200, 128)) * 8) / 8).astype(np.float32)
+    logits[::10] = 0.0
+    logits[5] = -0.0
+    logits[6, ::2] = -0.0
+    logits[6, 1::2] = 0.0
+    b = {"zero": np.zeros(128, np.float32), "own": (r.standard_normal(128) * 1e-3).astype(np.float32), None: None}[bias]
+    Gate(200, 128, 9, score, groups, kept, top, True, 1.0, bias=b, logits=logits).check()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("groups,kept", [(1, 1), (4, 2)])
+def test_odd_rows(score, renorm, bias, groups, kept):
+    r = np.random.default_rng(10)
+    z = r.standard_normal((14, 32)).astype(np.float32)
+    z[0] = np.nan
+    z[1] = -np.inf
+    z[2, 3] = np.inf
+    z[3, [5, 9]] = np.inf
+    z[4, ::3] = np.nan
+    z[5, 1:] = -np.inf
+    z[6] = -200.0 - np.arange(32)     # sigmoids below fp32's least number still have shares
+    z[7] = 100.0 + np.arange(32)      # sigmoids of 1
+    z[8] = 1e30
+    z[9] = -3e38
+    z[10, 0] = 3e38
+    z[11] = 45.0                      # equal 64-bit sigmoids from equal and from unequal scores
+    z[12] = 40.0 + np.arange(32) % 3
+    g = Gate(14, 32, 4, score, groups, kept, 2, renorm, 1.5, bias=bias, logits=z)
+    ids, w = g.run()
+    want_ids, want_w = oracle.group_gate(z, None if g.bias is None else g.bias.astype(np.float64), *g.ref)
+    assert np.array_equal(ids, want_ids)
+    check32(w, want_w, np.abs(want_w), depth=1024, what="weights")  # arguments up to 200 round by 200 ulps of 1
+
+
+def test_infinite_bias():
+    b = np.zeros(64, np.float32)
+    b[::3] = -np.inf  # experts that are switched off
+    b[7] = np.inf
+    ids = Gate(100, 64, 8, "sigmoid", bias=b, seed=12).check()
+    assert (ids[:, 0] == 7).all() and not np.isin(ids[ids != 7] % 3, 0).any()
+    Gate(20, 64, 40, "sigmoid", bias=b, seed=13).check()  # some of them have to be taken
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(v) for v in c))
+@pytest.mark.parametrize("accumulate", [0, 1])
+def test_backward(case, accumulate):
+    g = Gate(*case, seed=4)
+    ids, _ = g.run()
+    T, E, k = g.T, g.E, g.k
+    r = np.random.default_rng(1)
+    dw = r.standard_normal((T, k)).astype(np.float32)
+    before = r.standard_normal((T, E)).astype(np.float32)
+    buf = torch.full((T * E + 8,), 3.0, device="cuda")
+    buf[:T * E] = torch.from_numpy(before).cuda().view(-1) if accumulate else float("nan")
+    fx.flux_moe_group_gate_bwd(T, E, k, g.args[3], g.args[7], g.args[8], g.cu, torch.from_numpy(ids).cuda(),
+                               torch.from_numpy(dw).cuda(), accumulate, buf)
+    want, mag = oracle.group_gate_bwd(g.logits, ids, dw.astype(np.float64), case[3], case[7], case[8])
+    got = buf[:T * E].view(T, E).double().cpu().numpy()
+    assert bool((buf[T * E:] == 3.0).all())
+    if accumulate:
+        check32(got, want + before, mag + np.abs(before) / 64, depth=128, what="dlogits")
+    else:
+        check32(got, want, mag, depth=128, what="dlogits")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [0, 1])
+def test_backward_of_odd_rows(score, renorm):
+    z = np.random.default_rng(3).standard_normal((9, 16)).astype(np.float32)
+    z[0] = np.nan
+    z[1] = -np.inf
+    z[2, 3] = np.inf
+    z[3] = -200.0 - np.arange(16)
+    z[4] = 100.0 + np.arange(16)
+    z[5, 2:] = -np.inf
+    ids, _ = oracle.group_gate(z, None, 3, score, 1, 1, 1, bool(renorm), 1.0)
+    ids[6, 1] = -1
+    ids[7, 0] = 16
+    dw = np.random.default_rng(4).standard_normal((9, 3)).astype(np.float32)
+    dl = torch.full((9, 16), float("nan"), device="cuda")
+    fx.flux_moe_group_gate_bwd(9, 16, 3, SCORE[score], renorm, 1.0, torch.from_numpy(z).cuda(), torch.from_numpy(ids).cuda(),
+                               torch.from_numpy(dw).cuda(), 0, dl)
+    want, mag = oracle.group_gate_bwd(z, ids, dw.astype(np.float64), score, bool(renorm), 1.0)
+    # (numbers below fp32's least normal one may be 0)
+    check32(dl.double().cpu().numpy(), want, mag + 2.0 ** -100, depth=1024, what="dlogits")
+
+
+def test_dot_of_zero():
+    # the chosen experts' terms cancel: the sum over them is 0
+    z = np.zeros((1, 8), np.float32)
+    ids = np.array([[0, 1]], np.int32)
+    dw = np.array([[1.0, -1.0]], np.float32)
+    dl = torch.empty(1, 8, device="cuda")
+    fx.flux_moe_group_gate_bwd(1, 8, 2, fx.FLUX_SCORE_SOFTMAX, 0, 1.0, torch.from_numpy(z).cuda(), torch.from_numpy(ids).cuda(),
+                               torch.from_numpy(dw).cuda(), 0, dl)
+    np.testing.assert_allclose(dl.cpu().numpy(), [[0.125, -0.125] + [0.0] * 6], rtol=1e-6)
+
+
+def test_sum_with_the_router_losses():
+    # the balance loss's gradient, then the gate's added to it
+    T, E, k = 300, 32, 4
+    g = Gate(T, E, k, "softmax", bias=None, seed=6)
+    ids, w = g.run()
+    cu = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    i, wt = cu(ids), cu(w.astype(np.float32))
+    ws = torch.zeros(max(64, fx.flux_moe_balance_workspace_size(T, E, k, 1) // 4), dtype=torch.int32, device="cuda")
+    loss, probs, lse = torch.empty(2, device="cuda"), torch.empty(E, device="cuda"), torch.empty(T, device="cuda")
+    counts, tokens = torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    fx.flux_moe_balance_loss(T, E, k, 1, 0.1, 0.01, g.cu, i, None, loss, counts, probs, tokens, lse, ws)
+    dw = torch.randn(T, k, device="cuda")
+    a, b = torch.empty(T, E, device="cuda"), torch.empty(T, E, device="cuda")
+    fx.flux_moe_router_bwd(T, E, k, 1, 0.1, 0.01, g.cu, i, wt, None, lse, counts, tokens, None, dw, a)
+    fx.flux_moe_router_bwd(T, E, k, 1, 0.1, 0.01, g.cu, i, None, None, lse, counts, tokens, None, None, b)
+    fx.flux_moe_group_gate_bwd(T, E, k, fx.FLUX_SCORE_SOFTMAX, 1, 1.0, g.cu, i, dw, 1, b)
+    assert float((a - b).abs().max()) < 1e-5 * float(a.abs().max())
+
+
+def test_long_batch_repeats():
+    g = Gate(70001, 256, 8, "sigmoid", 8, 4, 2, True, 2.5, seed=20)
+    a = g.run()
+    side = torch.cuda.Stream()
+    b = g.run(stream=side)
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+    rows = np.random.default_rng(0).integers(0, 70001, 500)
+    ids, w = oracle.group_gate(g.logits[rows], g.bias.astype(np.float64), *g.ref)
+    assert np.array_equal(a[0][rows], ids)
+    check32(a[1][rows], w, np.abs(w), depth=128)
