@@ -23,6 +23,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "flux_host.h"
 #include "flux_rows.cuh"
@@ -45,18 +46,17 @@ struct GroupGateArgs {
   float* dlogits;
   int T, E, topk, G, kept, top;
   int n, pad;          // experts of a group; words between groups in shared memory
-  int lpg;             // lanes that rank one group
+  int lpg, log_lpg;    // lanes that rank one group
+  int vecs, trips, rivals;  // wide form: vectors of a lane; of a lane in its group; groups that a lane compares
   uint32_t div_n;      // ceil(2^20 / n): e / n = e div_n >> 20 for e < 1024
   int row;             // values of a token's row in shared memory
   int softmax, renorm, accumulate;
   float scale;
 };
 
-// What a token needs in shared memory: its values (room for doubles), the picked
-// experts, the groups' ranks, the ranks in order, the kept groups.
-__host__ __device__ inline size_t gate_token_bytes(int row, int topk) {
-  return static_cast<size_t>(row) * 8 + ((topk * 4 + 7) & ~7) + 32 * 8 * 2 + 32 * 4;
-}
+// What a token needs in shared memory: its values, the picked experts, the groups'
+// ranks, the ranks in order, the kept groups.
+__host__ __device__ inline size_t gate_token_bytes(int row, int topk) { return static_cast<size_t>(row + topk + 3 * 32) * 4; }
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -132,35 +132,49 @@ __device__ __forceinline__ void each_logit(const float* row, int E, int l, F&& f
 // A token's places in shared memory.
 struct Rows {
   float* val;
-  double* val64;
   int32_t* pick;
   float *rank, *sorted;
-  double *rank64;
   int32_t* kept;
   __device__ __forceinline__ Rows(char* base, int row, int topk) {
-    val64 = reinterpret_cast<double*>(base);
     val = reinterpret_cast<float*>(base);
-    pick = reinterpret_cast<int32_t*>(base + static_cast<size_t>(row) * 8);
-    rank64 = reinterpret_cast<double*>(base + static_cast<size_t>(row) * 8 + ((topk * 4 + 7) & ~7));
-    rank = reinterpret_cast<float*>(rank64);
+    pick = reinterpret_cast<int32_t*>(val + row);
+    rank = reinterpret_cast<float*>(pick + topk);
     sorted = rank + 32;
-    kept = reinterpret_cast<int32_t*>(rank64 + 64);
+    kept = reinterpret_cast<int32_t*>(sorted + 32);
   }
 };
 
 __device__ __forceinline__ int group_of(const GroupGateArgs& a, int e) { return static_cast<int>((e * a.div_n) >> 20); }
 __device__ __forceinline__ int place(const GroupGateArgs& a, int e) { return a.pad == 0 ? e : e + group_of(a, e) * a.pad; }
 // The expert at place p of the kept groups' experts in order.
-__device__ __forceinline__ int expert_at(const GroupGateArgs& a, const Rows& r, int p) {
+__device__ __forceinline__ int expert_at(const GroupGateArgs& a, const int32_t* kept, int p) {
   if (a.kept == a.G) return p;
   const int q = group_of(a, p);
-  return r.kept[q] * a.n + (p - q * a.n);
+  return kept[q] * a.n + (p - q * a.n);
 }
 
-// The choice in doubles, by the LPT lanes of one token (mask).  Rare.
-template <int LPT, int NC>
-__device__ __noinline__ void choose64(const GroupGateArgs& a, const float* row, const Rows& r, int l, uint32_t mask) {
-  auto shfl = [&](double v, int o) { return __shfl_xor_sync(mask, v, o); };
+// Doubles as numbers in their order, for maxima over lanes in halves of 32 bits.
+__device__ __forceinline__ unsigned long long order_of(double v) {
+  const unsigned long long u = __double_as_longlong(v + 0.0);
+  return u >> 63 ? ~u : u | 1ull << 63;
+}
+__device__ __forceinline__ double value_of(unsigned long long k) { return __longlong_as_double(k >> 63 ? k & ~(1ull << 63) : ~k); }
+__device__ __forceinline__ unsigned long long largest_of(uint32_t mask, unsigned long long v) {
+  const uint32_t hi = __reduce_max_sync(mask, static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = __reduce_max_sync(mask, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  return static_cast<unsigned long long>(hi) << 32 | lo;
+}
+
+// The choice in doubles, by the LPT lanes of one token (mask).  Writes the kept groups
+// and, as pick, the places of the chosen ones among the kept groups'
+// experts.  One token in a thousand comes here, and the last one holds up the launch:
+// a token of 256 experts took 60 us with double comparisons and shuffles of doubles.
+template <int LPT>
+__device__ __noinline__ void choose64(const GroupGateArgs& a, const float* row, int32_t* kept, int32_t* pick, int l,
+                                      uint32_t some) {
+  constexpr int MINE = LPT == 32 ? FLUX_MAX_EXPERTS / 32 : 64 / LPT;
+  constexpr unsigned long long LEAST = 0x000FFFFFFFFFFFFFull;  // order_of(-inf)
+  const uint32_t mask = LPT == 32 ? 0xFFFFFFFFu : some;
   auto logit = [&](int e) {
     const float x = __ldg(row + e);
     return static_cast<double>(x != x ? -INFINITY : x);
@@ -168,77 +182,98 @@ __device__ __noinline__ void choose64(const GroupGateArgs& a, const float* row, 
   double top = -INFINITY, total = 0.0;
   if (a.softmax) {
     for (int e = l; e < a.E; e += LPT) top = fmax(top, logit(e));
-#pragma unroll
-    for (int o = LPT / 2; o > 0; o >>= 1) top = fmax(top, shfl(top, o));
+    top = value_of(largest_of(mask, order_of(top)));
     for (int e = l; e < a.E; e += LPT) total += isinf(top) ? (logit(e) == top ? 1.0 : 0.0) : exp(logit(e) - top);
 #pragma unroll
-    for (int o = LPT / 2; o > 0; o >>= 1) total += shfl(total, o);
+    for (int o = LPT / 2; o > 0; o >>= 1) total += __shfl_xor_sync(mask, total, o);
   }
   auto score = [&](double x) {
     if (!a.softmax) return 1.0 / (1.0 + exp(-x));
     return (isinf(top) ? (x == top ? 1.0 : 0.0) : exp(x - top)) / total;
   };
-  __syncwarp(mask);
-  for (int e = l; e < a.E; e += LPT) {
-    const double x = logit(e), c = a.bias != nullptr ? score(x) + static_cast<double>(__ldg(a.bias + e)) : x;
-    r.val64[place(a, e)] = c != c ? -INFINITY : c;
+  unsigned long long c[MINE];  // experts l, l + LPT, ...
+#pragma unroll 1
+  for (int e = l, i = 0; e < a.E; e += LPT, ++i) {
+    const double x = logit(e), v = a.bias != nullptr ? score(x) + static_cast<double>(__ldg(a.bias + e)) : x;
+    c[i] = v != v ? LEAST : order_of(v);
   }
-  __syncwarp(mask);
+  uint32_t in = 0xFFFFFFFFu;
   if (a.kept < a.G) {
-    double mine[32 / LPT];
-    for (int g = l, i = 0; g < a.G; g += LPT, ++i) {
-      double m1 = -INFINITY, m2 = -INFINITY;
-      for (int m = 0; m < a.n; ++m) {
-        const double v = r.val64[g * (a.n + a.pad) + m];
-        m2 = fmax(m2, fmin(m1, v));
-        m1 = fmax(m1, v);
+    unsigned long long mine[32 / LPT];  // ranks of groups l, l + LPT, ...
+#pragma unroll 1
+    for (int g = 0; g < a.G; ++g) {
+      // the group's two largest: a lane's own first, then over the lanes
+      unsigned long long m1 = 0, m2 = 0;
+      const int from = g * a.n, to = from + a.n;
+#pragma unroll 1
+      for (int i = from / LPT; i * LPT < to; ++i) {
+        const int e = i * LPT + l;
+        if (e < from || e >= to) continue;
+        m2 = max(m2, min(m1, c[i]));
+        m1 = max(m1, c[i]);
       }
-      if (a.top == 2 && a.n > 1) m1 = a.bias != nullptr ? m1 + m2 : score(m1) + score(m2);
-      r.rank64[g] = m1 != m1 ? -INFINITY : m1;
+      const unsigned long long best = largest_of(mask, m1);
+      double r = value_of(best);
+      if (a.top == 2 && a.n > 1) {
+        const uint32_t all = __ballot_sync(mask, m1 == best);
+        const int owner = (__ffs(all) - 1) % LPT;
+        const double second = value_of(largest_of(mask, l == owner ? m2 : m1));
+        r = a.bias != nullptr ? r + second : score(r) + score(second);
+      }
+      if (g % LPT == l) mine[g / LPT] = r != r ? LEAST : order_of(r);
     }
-    __syncwarp(mask);
-    for (int g = l, i = 0; g < a.G; g += LPT, ++i) mine[i] = r.rank64[g];
-    uint32_t in = 0;
-    for (int g = l, i = 0; g < a.G; g += LPT, ++i) {
-      int pos = 0;
-      for (int o = 0; o < a.G; ++o) pos += r.rank64[o] > mine[i] || (r.rank64[o] == mine[i] && o < g);
-      if (pos < a.kept) in |= 1u << g;
+    // the kept ones one after the other, the first of equal ones first
+    uint32_t left = 0;
+    for (int g = l, i = 0; g < a.G; g += LPT, ++i) left |= 1u << i;
+    in = 0;
+#pragma unroll 1
+    for (int k = 0; k < a.kept; ++k) {
+      unsigned long long m = 0;
+      for (int i = 0; i < 32 / LPT; ++i)
+        if (left >> i & 1u) m = max(m, mine[i]);
+      const unsigned long long best = largest_of(mask, m);
+      uint32_t g = 0xFFFFFFFFu;
+      for (int i = 32 / LPT - 1; i >= 0; --i)
+        if ((left >> i & 1u) && mine[i] == best) g = i * LPT + l;
+      g = __reduce_min_sync(mask, g);
+      if (g % LPT == static_cast<uint32_t>(l)) left &= ~(1u << g / LPT);
+      in |= 1u << g;
     }
-#pragma unroll
-    for (int o = LPT / 2; o > 0; o >>= 1) in |= __shfl_xor_sync(mask, in, o);
-    __syncwarp(mask);
     for (int g = l; g < a.G; g += LPT)
-      if (in >> g & 1u) r.kept[__popc(in & ((1u << g) - 1u))] = g;
+      if (in >> g & 1u) kept[__popc(in & ((1u << g) - 1u))] = g;
+#pragma unroll 1
+    for (int e = l, i = 0; e < a.E; e += LPT, ++i)
+      if (!(in >> group_of(a, e) & 1u)) c[i] = 0;
     __syncwarp(mask);
   }
-  const int count = a.kept * a.n;
-  uint32_t taken = 0;
+  // a lane's best, looked for again when it has been taken
+  unsigned long long m;
+  int at;
+  auto look = [&] {
+    m = 0;
+    at = 0;
+#pragma unroll 1
+    for (int e = l, i = 0; e < a.E; e += LPT, ++i)
+      if (c[i] > m) {
+        m = c[i];
+        at = i;
+      }
+  };
+  look();
+#pragma unroll 1
   for (int j = 0; j < a.topk; ++j) {
-    double best = -INFINITY;
-    int at = 1 << 20;
-    for (int i = 0; i < NC; ++i) {
-      const int p = i * LPT + l;
-      if (p >= count || (taken >> i & 1u)) continue;
-      const int e = expert_at(a, r, p);
-      const double v = r.val64[place(a, e)];
-      if (at == 1 << 20 || v > best) {
-        best = v;
-        at = p;
-      }
+    const unsigned long long best = largest_of(mask, m);
+    const int e = __reduce_min_sync(mask, m == best ? static_cast<uint32_t>(at * LPT + l) : 0xFFFFFFFFu);
+    if (e % LPT == l) {
+      c[at] = 0;
+      look();
     }
-#pragma unroll
-    for (int o = LPT / 2; o > 0; o >>= 1) {
-      const double ov = shfl(best, o);
-      const int oat = __shfl_xor_sync(mask, at, o);
-      if (oat != 1 << 20 && (at == 1 << 20 || ov > best || (ov == best && oat < at))) {
-        best = ov;
-        at = oat;
-      }
+    if (l == 0) {
+      const int g = group_of(a, e);
+      pick[j] = a.kept < a.G ? __popc(in & ((1u << g) - 1u)) * a.n + e - g * a.n : e;
     }
-    if (at % LPT == l) taken |= 1u << at / LPT;
-    if (l == 0) r.pick[j] = expert_at(a, r, at);
+    __syncwarp(mask);
   }
-  __syncwarp(mask);
 }
 
 // One token to LPT lanes, NC candidates each.  The lanes put the values into a row
@@ -248,7 +283,7 @@ template <int LPT, int NC>
 __global__ void __launch_bounds__(GG_THREADS, NC <= 8 ? 5 : 2)
 group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
   constexpr int TPW = 32 / LPT;
-  extern __shared__ double smem[];
+  extern __shared__ uint4 smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT, sub = lane / LPT;
   using O = Over<LPT>;
   const Rows r(reinterpret_cast<char*>(smem) + (warp * TPW + sub) * gate_token_bytes(a.row, a.topk), a.row, a.topk);
@@ -359,7 +394,7 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int p = i * LPT + l;
-      key[i] = p < count ? order_of(r.val[place(a, expert_at(a, r, p))]) : 0u;
+      key[i] = p < count ? order_of(r.val[place(a, expert_at(a, r.kept, p))]) : 0u;
     }
     for (int j = 0; j < a.topk; ++j) {
       uint32_t m = key[0];
@@ -374,38 +409,39 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
 #pragma unroll
       for (int i = 0; i < NC; ++i)
         if (at == static_cast<uint32_t>(i * LPT + l)) key[i] = 0u;
-      if (l == 0) r.pick[j] = expert_at(a, r, static_cast<int>(at));
+      if (l == 0) r.pick[j] = static_cast<int>(at);
     }
     uint32_t m = key[0];
 #pragma unroll
     for (int i = 1; i < NC; ++i) m = max(m, key[i]);
     m = O::max(m);  // the best one left, 0 if none is
     __syncwarp();
+    auto expert = [&](int j) { return expert_at(a, r.kept, r.pick[j]); };
     if (biased) {
       auto apart = [&](float hi, float lo) { return hi - lo > unsure + 0x1p-23f * (fabsf(hi) + fabsf(lo)); };
       auto same = [&](int e, int f) { return __ldg(row + e) == __ldg(row + f) && __ldg(a.bias + e) == __ldg(a.bias + f); };
-      const float last = r.val[place(a, r.pick[a.topk - 1])];
+      const float last = r.val[place(a, expert(a.topk - 1))];
       uint32_t close = m != 0u && !apart(last, value_of(m));
-      for (int j = l; j + 1 < a.topk; j += LPT) close |= !apart(r.val[place(a, r.pick[j])], r.val[place(a, r.pick[j + 1])]);
+      for (int j = l; j + 1 < a.topk; j += LPT) close |= !apart(r.val[place(a, expert(j))], r.val[place(a, expert(j + 1))]);
       if (O::any(close)) {
         // equal inputs have equal values: their order is that of the indexes
         uint32_t wrong = 0;
         for (int j = l; j + 1 < a.topk; j += LPT) {
-          const int e = r.pick[j], f = r.pick[j + 1];
+          const int e = expert(j), f = expert(j + 1);
           wrong |= !apart(r.val[place(a, e)], r.val[place(a, f)]) && !same(e, f);
         }
 #pragma unroll
         for (int i = 0; i < NC; ++i)
           if (key[i] != 0u && !apart(last, value_of(key[i])))
-            wrong |= !same(r.pick[a.topk - 1], expert_at(a, r, i * LPT + l));
+            wrong |= !same(expert(a.topk - 1), expert_at(a, r.kept, i * LPT + l));
         doubt |= wrong;
       }
     }
     doubt = O::any(doubt);
-    if (doubt) choose64<LPT, NC>(a, row, r, l, LPT == 32 ? 0xFFFFFFFFu : ((1u << LPT % 32) - 1u) << (sub * LPT));
+    if (doubt) choose64<LPT>(a, row, r.kept, r.pick, l, LPT == 32 ? 0xFFFFFFFFu : ((1u << LPT % 32) - 1u) << (sub * LPT));
     __syncwarp();
     // the weights
-    auto chosen = [&](int j) { return fmaxf(__ldg(row + r.pick[j]), -INFINITY); };
+    auto chosen = [&](int j) { return fmaxf(__ldg(row + expert(j)), -INFINITY); };
     float peak = -INFINITY;
     if (a.renorm) {
       for (int j = l; j < a.topk; j += LPT) peak = fmaxf(peak, chosen(j));
@@ -425,11 +461,334 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
     }
     if (here) {
       for (int j = l; j < a.topk; j += LPT) {
-        a.ids[t * a.topk + j] = r.pick[j];
+        a.ids[t * a.topk + j] = expert(j);
         a.weights[t * a.topk + j] = a.scale * (weight(chosen(j)) / sum);
       }
     }
   }
+}
+
+// The largest of the lanes' numbers; a NaN counts only where there is nothing else.
+__device__ __forceinline__ float warp_largest(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// A token's words in shared memory, wide form: its logits as they come and those of
+// the next token (rows of whole vectors for every lane), its values (with groups),
+// the picked places, the kept groups, the lists and the order of what they hold.
+__host__ __device__ inline int wide_words(int vecs, int row, int topk, int lists) {
+  return 2 * 128 * vecs + row + ((topk + 3) & ~3) + 32 + lists * 32 * 6;
+}
+
+// One token to a warp, vectors of four experts to a lane, the next token's logits on
+// their way while this one's are at work.  The candidates (all experts, or the kept
+// groups') lie in LISTS sorted lists of four a lane, so that a round of the choice
+// is a maximum over the lists' heads and over the warp, and a shift of the winner's
+// list.
+template <int VECS, int LISTS, bool GROUPED, bool SOFT, bool BIASED>
+__global__ void __launch_bounds__(GG_THREADS, LISTS <= 2 ? 4 : 3)
+group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
+  extern __shared__ uint4 smem[];
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), vecs = VECS > 0 ? VECS : a.vecs, wide = 128 * vecs;
+  float* bias = reinterpret_cast<float*>(smem);
+  float* raw2 = bias + (BIASED ? wide : 0) + warp * wide_words(vecs, a.row, a.topk, LISTS);
+  float* val = raw2 + 2 * wide;
+  int32_t* pick = reinterpret_cast<int32_t*>(val + a.row);
+  int32_t* kept = pick + ((a.topk + 3) & ~3);
+  float* list = reinterpret_cast<float*>(kept + 32);
+  uint32_t* order = reinterpret_cast<uint32_t*>(list + LISTS * 32 * 5);
+  const bool two = a.top == 2 && a.n > 1;
+  const bool soft_row = SOFT && (BIASED || !a.renorm || (GROUPED && two));
+  // what lies past the last expert is -inf everywhere
+  for (int e = a.E + lane; e < wide; e += 32) raw2[e] = raw2[wide + e] = -INFINITY;
+  for (int q = 0; q < LISTS; ++q) list[(q * 32 + lane) * 5 + 4] = NAN;
+  wait_for_previous();
+  if constexpr (BIASED) {
+    for (int e = threadIdx.x; e < wide; e += GG_THREADS) bias[e] = e < a.E ? __ldg(a.bias + e) : -INFINITY;
+    __syncthreads();
+  }
+  auto fetch = [&](long long at, float* dst) {
+    if (at < a.T) {
+      const float* src = a.logits + static_cast<size_t>(at) * a.E;
+#pragma unroll
+      for (int v = 0; v < vecs; ++v) {
+        const int e = v * 128 + lane * 4;
+        if (e < a.E) copy16_async(dst + e, src + e);
+      }
+    }
+    copy_commit();
+  };
+  // the CTA's warps go round together, the last time perhaps without a token
+  const long long step = static_cast<long long>(gridDim.x) * GG_WARPS;
+  long long first = static_cast<long long>(blockIdx.x) * GG_WARPS;
+  fetch(first + warp, raw2);
+  for (int turn = 0; first < a.T; first += step, turn ^= 1) {
+    const bool token = first + warp < a.T;
+    const long long t = token ? first + warp : a.T - 1;
+    float* raw = raw2 + turn * wide;
+    __syncwarp();  // the other row's readers are done
+    fetch(first + warp + step, raw2 + (turn ^ 1) * wide);
+    copy_wait<1>();
+    auto four = [&](int e) {
+      float4 x = *reinterpret_cast<const float4*>(raw + e);
+      x.x = fmaxf(x.x, -INFINITY), x.y = fmaxf(x.y, -INFINITY), x.z = fmaxf(x.z, -INFINITY), x.w = fmaxf(x.w, -INFINITY);
+      return x;
+    };
+    float top = -INFINITY, inv = 1.0f, total = 1.0f;
+    auto soft = [&](float x) { return isinf(top) ? (x == top ? 1.0f : 0.0f) : ex2((x - top) * G_LOG2E); };
+    auto score = [&](float x) {
+      if constexpr (SOFT) return soft(x) * inv;
+      else return rcp(1.0f + ex2(-x * G_LOG2E));
+    };
+    if (soft_row) {
+      for (int v = 0; v < vecs; ++v) {
+        const float4 x = four(v * 128 + lane * 4);
+        top = fmaxf(top, fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)));
+      }
+      top = warp_largest(top);
+      total = 0.0f;
+      for (int v = 0; v < vecs; ++v) {
+        const float4 x = four(v * 128 + lane * 4);
+        total += (soft(x.x) + soft(x.y)) + (soft(x.z) + soft(x.w));
+      }
+      total = top == -INFINITY ? static_cast<float>(a.E) : warp_sum(total);
+      inv = rcp(total);
+    }
+    // the values: the logits without a bias, else s + bias
+    auto values = [&](int e) {
+      float4 x = four(e);
+      if constexpr (BIASED) {
+        const float4 b = *reinterpret_cast<const float4*>(bias + e);
+        x.x = score(x.x) + b.x, x.y = score(x.y) + b.y, x.z = score(x.z) + b.z, x.w = score(x.w) + b.w;
+      }
+      return x;
+    };
+    // (how far apart: as in group_gate_kernel)
+    const float unsure = SOFT ? 0x1p-16f * inv : 0x1p-20f;
+    bool doubt = false;
+    if constexpr (GROUPED) {
+#pragma unroll 2
+      for (int v = 0; v < vecs; ++v) {
+        const int e = v * 128 + lane * 4;
+        *reinterpret_cast<float4*>(val + e + group_of(a, e) * a.pad) = values(e);
+      }
+      __syncwarp();
+      // lpg lanes a group
+      const int g = lane >> a.log_lpg, sub = lane & (a.lpg - 1);
+      float m1 = -INFINITY, m2 = -INFINITY;
+      const float* mine = val + g * (a.n + a.pad);
+#pragma unroll 2
+      for (int k = 0; k < a.trips; ++k) {
+        const int i = (k * a.lpg + sub) * 4;
+        float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (g < a.G && i < a.n) q = *reinterpret_cast<const float4*>(mine + i);
+        const float p = fmaxf(q.x, q.y), s = fminf(q.x, q.y), u = fmaxf(q.z, q.w), w = fminf(q.z, q.w);
+        m2 = fmaxf(fmaxf(m2, fminf(m1, fmaxf(p, u))), fmaxf(fminf(p, u), fmaxf(s, w)));
+        m1 = fmaxf(m1, fmaxf(p, u));
+      }
+      for (int o = a.lpg >> 1; o > 0; o >>= 1) {
+        const float o1 = __shfl_xor_sync(0xFFFFFFFFu, m1, o), o2 = __shfl_xor_sync(0xFFFFFFFFu, m2, o);
+        m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+        m1 = fmaxf(m1, o1);
+      }
+      if (!two) m2 = 0.0f;
+      else if (!BIASED) m1 = score(m1), m2 = score(m2);
+      // the groups before this one in the order, counted by its lanes
+      const float rank = g < a.G ? fmaxf(m1 + m2, -INFINITY) : -INFINITY;
+      int before = 0;
+      for (int k = 0; k < a.rivals; ++k) {
+        const int o = k * a.lpg + sub;
+        const float other = __shfl_sync(0xFFFFFFFFu, rank, o << a.log_lpg);
+        before += o < a.G && (other > rank || (other == rank && o < g));
+      }
+      for (int o = a.lpg >> 1; o > 0; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+      const bool in = g < a.G && before < a.kept;
+      const uint32_t set = __ballot_sync(0xFFFFFFFFu, in && sub == 0);
+      if (in && sub == 0) kept[__popc(set & ((1u << lane) - 1u))] = g;
+      if (BIASED || two) {
+        const float big = g < a.G ? (isinf(m1) ? 0.0f : fabsf(m1)) + (isinf(m2) ? 0.0f : fabsf(m2)) : 0.0f;
+        const float last = -warp_largest(in ? -rank : NAN), next = warp_largest(in || g >= a.G ? NAN : rank);
+        doubt = !(last - next > 2.0f * unsure + 0x1p-21f * warp_largest(big));
+      }
+      __syncwarp();
+    }
+    // lists of four, largest first, equal ones in order; their numbers in the bytes of a
+    // word, and a NaN at their end
+    const int count = a.kept * a.n;
+    float h[LISTS];  // the heads
+    int at[LISTS];   // and their places
+#pragma unroll
+    for (int q = 0; q < LISTS; ++q) {
+      const int p = q * 128 + lane * 4;
+      float4 x = make_float4(NAN, NAN, NAN, NAN);
+      if constexpr (GROUPED) {
+        if (p < count) {
+          const int g = group_of(a, p);
+          x = *reinterpret_cast<const float4*>(val + kept[g] * (a.n + a.pad) + (p - g * a.n));
+        }
+      } else if (q < vecs) {
+        const float4 y = values(p);
+        if (p < count) x = y;
+      }
+      float v[4] = {x.x, x.y, x.z, x.w};
+      uint32_t id[4] = {0, 1, 2, 3};
+      auto sort2 = [&](int i) {  // neighbours, if out of order: equal ones stay in theirs
+        const bool swap = v[i] < v[i + 1];
+        const float hi = fmaxf(v[i], v[i + 1]), lo = fminf(v[i], v[i + 1]);
+        const uint32_t first = swap ? id[i + 1] : id[i], second = swap ? id[i] : id[i + 1];
+        v[i] = hi, v[i + 1] = lo, id[i] = first, id[i + 1] = second;
+      };
+      sort2(0), sort2(1), sort2(2), sort2(0), sort2(1), sort2(0);
+      at[q] = (q * 32 + lane) * 5;
+#pragma unroll
+      for (int i = 1; i < 4; ++i) list[at[q] + i] = v[i];
+      list[at[q]] = h[q] = v[0];
+      order[q * 32 + lane] = id[0] | id[1] << 8 | id[2] << 16 | id[3] << 24;
+    }
+    auto head = [&] {
+      float m = h[0];
+#pragma unroll
+      for (int q = 1; q < LISTS; ++q) m = fmaxf(m, h[q]);
+      return m;
+    };
+    // the place among the candidates of what a list holds at `where`
+    auto candidate = [&](int where) {
+      const int of = static_cast<int>(static_cast<uint32_t>(where) * 52429u >> 18);  // / 5
+      return of * 4 + (order[of] >> (where - of * 5) * 8 & 3u);
+    };
+    // One round after the other.  Where the largest is in several lists, the one with the
+    // first expert has it.  To see that costs half a round, so all of them take it; more
+    // taken than rounds tell, and the rounds are gone through again with care.
+    for (int j0 = 0; j0 < a.topk; j0 += 8) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (j0 + u >= a.topk) break;
+        const float best = warp_largest(head());
+#pragma unroll
+        for (int q = 0; q < LISTS; ++q) {
+          if (h[q] == best) {
+            pick[j0 + u] = at[q];
+            h[q] = list[++at[q]];
+          }
+        }
+      }
+    }
+    int taken = 0;
+#pragma unroll
+    for (int q = 0; q < LISTS; ++q) taken += at[q] - (q * 32 + lane) * 5;
+    if (__reduce_add_sync(0xFFFFFFFFu, taken) != a.topk) {
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < LISTS; ++q) {
+        at[q] = (q * 32 + lane) * 5;
+        h[q] = list[at[q]];
+      }
+      for (int j = 0; j < a.topk; ++j) {
+        const float best = warp_largest(head());
+        uint32_t first = 0xFFFFFFFFu;
+#pragma unroll
+        for (int q = LISTS - 1; q >= 0; --q)
+          if (h[q] == best) first = candidate(at[q]);
+        const uint32_t p = __reduce_min_sync(0xFFFFFFFFu, first);
+#pragma unroll
+        for (int q = 0; q < LISTS; ++q) {
+          if (h[q] == best && p == first && p / 128 == q) {
+            pick[j] = at[q];
+            h[q] = list[++at[q]];
+          }
+        }
+      }
+    }
+    __syncwarp();
+    const bool few = a.topk <= 32;
+    auto expert = [&](int p) { return GROUPED ? expert_at(a, kept, p) : p; };
+    int own = few && lane < a.topk ? candidate(pick[lane]) : 0;
+    if (!few) {
+      for (int j = lane; j < a.topk; j += 32) pick[j] = candidate(pick[j]);
+      __syncwarp();
+    }
+    own = expert(own);
+    if constexpr (BIASED) {
+      const float next = warp_largest(head());  // the best one left, NaN if none is
+      auto value = [&](int e) { return GROUPED ? val[place(a, e)] : score(fmaxf(raw[e], -INFINITY)) + bias[e]; };
+      auto apart = [&](float hi, float lo) { return hi - lo > unsure + 0x1p-23f * (fabsf(hi) + fabsf(lo)); };
+      bool close = false;
+      if (few) {
+        const float hi = value(own), after = __shfl_down_sync(0xFFFFFFFFu, hi, 1);
+        const float lo = lane + 1 < a.topk ? after : next;
+        close = lane < a.topk && lo == lo && !apart(hi, lo);
+      } else {
+        for (int j = lane; j < a.topk; j += 32) {
+          const float lo = j + 1 < a.topk ? value(expert(pick[j + 1])) : next;
+          close |= lo == lo && !apart(value(expert(pick[j])), lo);
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, close)) {
+        // equal inputs have equal values: their order is that of the indexes
+        auto same = [&](int e, int f) { return raw[e] == raw[f] && bias[e] == bias[f]; };
+        auto picked = [&](int j) { return expert(few ? candidate(pick[j]) : pick[j]); };
+        const int end = picked(a.topk - 1);
+        for (int j = lane; j + 1 < a.topk; j += 32) {
+          const int e = picked(j), f = picked(j + 1);
+          if (!apart(value(e), value(f))) doubt |= !same(e, f);
+        }
+#pragma unroll
+        for (int q = 0; q < LISTS; ++q)
+          for (int i = at[q]; i < (q * 32 + lane) * 5 + 4; ++i)  // what is left
+            if (list[i] == list[i] && !apart(value(end), list[i])) doubt |= !same(end, expert(candidate(i)));
+      }
+    }
+    if ((BIASED || GROUPED) && __any_sync(0xFFFFFFFFu, doubt)) {
+      choose64<32>(a, a.logits + static_cast<size_t>(t) * a.E, kept, pick, lane, 0xFFFFFFFFu);
+      if (few && lane < a.topk) own = expert(pick[lane]);
+    }
+    // The weights, with the rules of group_gate_kernel.  rcp: to one unit in the last
+    // place, where a rounded quotient costs eight times as much.
+    auto logit = [&](int e) { return fmaxf(raw[e], -INFINITY); };
+    float peak = 0.0f;
+    auto weight = [&](float x) {
+      if constexpr (SOFT) {
+        if (a.renorm) return isinf(peak) ? (x == peak ? 1.0f : 0.0f) : expf(x - peak);
+        return isinf(top) ? (x == top ? 1.0f : 0.0f) : expf(x - top);
+      } else {
+        if (!a.renorm || peak > -64.0f) return rcp(1.0f + expf(-x));
+        if (peak == -INFINITY) return 1.0f;
+        return expf(x - peak);  // so low that 1 + e^x is 1
+      }
+    };
+    int32_t* ids = a.ids + static_cast<size_t>(t) * a.topk;
+    float* weights = a.weights + static_cast<size_t>(t) * a.topk;
+    if (few) {
+      const bool here = lane < a.topk;
+      const float x = here ? logit(own) : -INFINITY;
+      if (a.renorm) peak = warp_largest(x);
+      float w = weight(x);
+      w = here ? w : 0.0f;
+      const float sum = a.renorm ? warp_sum(w) : total;
+      if (here && token) {
+        ids[lane] = own;
+        weights[lane] = a.scale * w * rcp(sum);
+      }
+    } else {
+      float sum = total;
+      if (a.renorm) {
+        peak = -INFINITY;
+        for (int j = lane; j < a.topk; j += 32) peak = fmaxf(peak, logit(expert(pick[j])));
+        peak = warp_largest(peak);
+        sum = 0.0f;
+        for (int j = lane; j < a.topk; j += 32) sum += weight(logit(expert(pick[j])));
+        sum = warp_sum(sum);
+      }
+      for (int j = lane; token && j < a.topk; j += 32) {
+        const int e = expert(pick[j]);
+        ids[j] = e;
+        weights[j] = a.scale * weight(logit(e)) * rcp(sum);
+      }
+    }
+  }
+  copy_wait<0>();
 }
 
 // Gradient of the scores.  The row of a token is made in shared memory (zeros but
@@ -438,7 +797,7 @@ template <int LPT>
 __global__ void __launch_bounds__(GG_THREADS, 4)
 group_gate_bwd_kernel(const __grid_constant__ GroupGateArgs a) {
   constexpr int TPW = 32 / LPT;
-  extern __shared__ double smem[];
+  extern __shared__ uint4 smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT, sub = lane / LPT;
   using O = Over<LPT>;
   const int pitch = (a.E + 3) & ~3;
@@ -562,6 +921,42 @@ flux_status_t launch_gate(const GroupGateArgs& a, const DeviceInfo& dev, cudaStr
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
+template <int VECS, int LISTS, bool GROUPED, bool SOFT, bool BIASED>
+flux_status_t launch_wide(const GroupGateArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  constexpr auto kernel = group_gate_wide_kernel<VECS, LISTS, GROUPED, SOFT, BIASED>;
+  const size_t smem = sizeof(float) * (GG_WARPS * wide_words(a.vecs, a.row, a.topk, LISTS) + (BIASED ? 128 * a.vecs : 0));
+  static OncePerDevice once;
+  const cudaError_t attr = once(dev.device, [&dev] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dev.max_smem_optin));
+  });
+  if (attr != cudaSuccess) return cuda_fail(attr);
+  const int per_sm = static_cast<int>(std::max<size_t>(1, std::min<size_t>(LISTS <= 2 ? 4 : 3, (227u << 10) / (smem + 1024))));
+  const int grid = std::min(ceil_div(a.T, GG_WARPS), GG_SMS * per_sm);
+  const cudaError_t e = launch_behind(kernel, dim3(grid), GG_THREADS, smem, s, a);
+  return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
+}
+
+template <int VECS, int LISTS, bool GROUPED>
+flux_status_t launch_wide(const GroupGateArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  if (a.softmax) return a.bias ? launch_wide<VECS, LISTS, GROUPED, true, true>(a, dev, s) : launch_wide<VECS, LISTS, GROUPED, true, false>(a, dev, s);
+  return a.bias ? launch_wide<VECS, LISTS, GROUPED, false, true>(a, dev, s) : launch_wide<VECS, LISTS, GROUPED, false, false>(a, dev, s);
+}
+
+// Rows of up to 256 experts have their loops unrolled.
+template <bool GROUPED>
+flux_status_t launch_wide(const GroupGateArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  const int lists = ceil_div(a.kept * a.n, 128);
+  if (a.vecs == 1) return launch_wide<1, 1, GROUPED>(a, dev, s);
+  if (a.vecs == 2 && lists == 2) return launch_wide<2, 2, GROUPED>(a, dev, s);
+  if constexpr (GROUPED) {
+    if (a.vecs == 2) return launch_wide<2, 1, true>(a, dev, s);
+    if (lists == 1) return launch_wide<0, 1, true>(a, dev, s);
+    if (lists == 2) return launch_wide<0, 2, true>(a, dev, s);
+  }
+  if (lists <= 4) return launch_wide<0, 4, GROUPED>(a, dev, s);
+  return launch_wide<0, 8, GROUPED>(a, dev, s);
+}
+
 template <int LPT>
 flux_status_t launch_gate_bwd(const GroupGateArgs& a, cudaStream_t s) {
   constexpr int TPC = GG_WARPS * (32 / LPT);
@@ -610,9 +1005,17 @@ extern "C" flux_status_t flux_moe_group_gate(int T, int E, int topk, int score, 
   const int lpt = E <= 64 ? 8 : 32;
   a.lpg = lpt;  // lanes of a group: as many as let all groups be ranked at once, at least one
   while (a.lpg > 1 && a.lpg * groups > lpt) a.lpg /= 2;
-  a.pad = topk_groups < groups ? a.lpg : 0;
-  a.row = E + groups * a.pad;
+  while (1 << a.log_lpg < a.lpg) ++a.log_lpg;
+  const bool grouped = topk_groups < groups, wide = lpt == 32 && a.n % 4 == 0;
+  // words between the groups' rows: lanes of neighbouring groups read other banks
+  a.pad = !grouped ? 0 : !wide ? a.lpg : a.lpg >= 8 ? 0 : (4 * a.lpg - a.n % 32 + 32) % 32;
+  a.vecs = ceil_div(E, 128);
+  a.trips = ceil_div(a.n, 4 * a.lpg);
+  a.rivals = ceil_div(groups, a.lpg);
+  // (the wide form has values past the last expert too)
+  a.row = !wide ? E + groups * a.pad : !grouped ? 0 : 128 * a.vecs + (128 * a.vecs - 4) / a.n * a.pad;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (wide) return grouped ? launch_wide<true>(a, dev, s) : launch_wide<false>(a, dev, s);
   const int each = ceil_div(topk_groups * a.n, lpt);  // candidates of a lane
   if (lpt == 8) {
     if (each <= 1) return launch_gate<8, 1>(a, dev, s);
