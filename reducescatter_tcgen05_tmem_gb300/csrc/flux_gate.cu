@@ -791,109 +791,175 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
   copy_wait<0>();
 }
 
-// Gradient of the scores.  The row of a token is made in shared memory (zeros but
-// for the chosen experts, or the whole softmax) and written once.
-template <int LPT>
-__global__ void __launch_bounds__(GG_THREADS, 4)
+// Gradient of the scores where only the chosen ones have one (sigmoid, or weights
+// that are renormalised).  A token's slots lie in SLOTS neighbouring lanes, so that a
+// warp works on 32 / SLOTS tokens at once; it writes their rows, which lie behind one
+// another, with zeros, and then the slots' gradients over them.  Bound by the writes.
+template <int SLOTS>
+__global__ void __launch_bounds__(GG_THREADS)
+group_gate_bwd_chosen_kernel(const __grid_constant__ GroupGateArgs a) {
+  constexpr int TPW = 32 / SLOTS;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % SLOTS;
+  auto sum = [](float v) {
+#pragma unroll
+    for (int o = SLOTS / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+  };
+  auto largest = [](float v) {
+#pragma unroll
+    for (int o = SLOTS / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+  };
+  wait_for_previous();
+  for (long long t0 = (static_cast<long long>(blockIdx.x) * GG_WARPS + warp) * TPW; t0 < a.T; t0 += static_cast<long long>(gridDim.x) * GG_WARPS * TPW) {
+    const long long t = t0 + lane / SLOTS;
+    const int tokens = static_cast<int>(min(static_cast<long long>(TPW), a.T - t0));
+    int id = -1;
+    float g = 0.0f, x = -INFINITY;
+    if (t < a.T && l < a.topk) {
+      id = __ldg(a.ids_in + t * a.topk + l);
+      if (id >= a.E) id = -1;
+      g = a.scale * __ldg(a.dweights + t * a.topk + l);
+      if (id >= 0) x = fmaxf(__ldg(a.logits + t * a.E + id), -INFINITY);
+    }
+    if (!a.accumulate) {
+      float* rows = a.dlogits + t0 * a.E;
+      const int n = tokens * a.E;
+      if (a.E % 4 == 0 || TPW % 4 == 0) {  // rows begin on 16 bytes
+        for (int i = lane * 4; i + 3 < n; i += 128) *reinterpret_cast<float4*>(rows + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (lane < n % 4) rows[n - n % 4 + lane] = 0.0f;
+      } else {
+        for (int i = lane; i < n; i += 32) rows[i] = 0.0f;
+      }
+      __syncwarp();  // the gradients come over the zeros
+    }
+    // the weights, as the forward pass has them
+    float d;
+    const float small = expf(-fabsf(x)), left = (x > 0.0f ? small : 1.0f) / (1.0f + small);  // 1 - sigmoid
+    if (a.renorm) {
+      const float peak = largest(x);
+      const bool constant = a.softmax ? isinf(peak) : peak == -INFINITY;  // no weight depends on a score
+      float v = 0.0f;
+      if (id >= 0 && !constant) v = a.softmax ? expf(x - peak) : expf(fminf(x, 0.0f) - fminf(peak, 0.0f)) / (1.0f + small);
+      const float total = sum(v), dot = sum(v * g) / total;
+      d = constant ? 0.0f : v / total * (g - dot) * (a.softmax ? 1.0f : left);
+    } else {
+      d = (x > 0.0f ? 1.0f : small) / (1.0f + small) * left * g;
+    }
+    if (id >= 0) {
+      float* at = a.dlogits + t * a.E + id;
+      *at = a.accumulate ? *at + d : d;
+    }
+  }
+}
+
+// The same for tokens of more than 32 slots, and the softmax that is not renormalised:
+// every score has a gradient, -p sum_i p_i g_i, and the chosen ones p g more.  LPT lanes
+// hold a token's scores in V vectors of four (or, for rows that do not begin on 16
+// bytes, scores one by one).
+template <int LPT, int V>
+__global__ void __launch_bounds__(GG_THREADS)
 group_gate_bwd_kernel(const __grid_constant__ GroupGateArgs a) {
   constexpr int TPW = 32 / LPT;
-  extern __shared__ uint4 smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT, sub = lane / LPT;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT;
   using O = Over<LPT>;
-  const int pitch = (a.E + 3) & ~3;
-  float* out = reinterpret_cast<float*>(smem) + (warp * TPW + sub) * pitch;
-  const bool every = a.softmax && !a.renorm;
-  const bool sparse = a.accumulate && !every;  // only the chosen experts' gradients change
+  const bool every = a.softmax && !a.renorm, vec = a.E % 4 == 0;
   wait_for_previous();
-  for (int e = l; e < a.E; e += LPT) out[e] = 0.0f;
-  for (long long t0 = static_cast<long long>(blockIdx.x * GG_WARPS + warp) * TPW; t0 < a.T; t0 += static_cast<long long>(gridDim.x) * GG_WARPS * TPW) {
-    const bool here = t0 + sub < a.T;
-    const size_t t = static_cast<size_t>(here ? t0 + sub : a.T - 1);
+  for (long long t0 = (static_cast<long long>(blockIdx.x) * GG_WARPS + warp) * TPW; t0 < a.T; t0 += static_cast<long long>(gridDim.x) * GG_WARPS * TPW) {
+    const bool here = t0 + lane / LPT < a.T;
+    const size_t t = static_cast<size_t>(here ? t0 + lane / LPT : a.T - 1);
     const float* row = a.logits + t * a.E;
-    const int32_t* ids = a.ids_in + t * a.topk;
-    const float* dw = a.dweights + t * a.topk;
-    auto inside = [&](int j) { return ids[j] >= 0 && ids[j] < a.E; };
-    auto chosen = [&](int j) { return inside(j) ? fmaxf(__ldg(row + ids[j]), -INFINITY) : -INFINITY; };
-    __syncwarp();
+    float* out = a.dlogits + t * a.E;
+    auto expert = [&](int v, int i) { return vec ? (v * LPT + l) * 4 + i : (v * 4 + i) * LPT + l; };
+    auto id = [&](int j) {
+      const int e = __ldg(a.ids_in + t * a.topk + j);
+      return e < a.E ? e : -1;
+    };
+    auto grad = [&](int j) { return a.scale * __ldg(a.dweights + t * a.topk + j); };
+    auto logit = [&](int e) { return e >= 0 ? fmaxf(__ldg(row + e), -INFINITY) : -INFINITY; };
+    float f[V][4] = {};
+    float peak = -INFINITY, total = 0.0f, dot = 0.0f;
     if (every) {
-      float top = -INFINITY, total = 0.0f;
-      each_logit<LPT>(row, a.E, l, [&](int e, float x) {
-        out[e] = x;
-        top = fmaxf(top, x);
-      });
-      top = O::maxf(top);
-      __syncwarp();
-      for (int e = l; e < a.E; e += LPT) {
-        out[e] = isinf(top) ? 0.0f : ex2((out[e] - top) * G_LOG2E);
-        total += out[e];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (vec) {
+          const int e = expert(v, 0);
+          const float4 q = e < a.E ? __ldg(reinterpret_cast<const float4*>(row + e)) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          f[v][0] = q.x, f[v][1] = q.y, f[v][2] = q.z, f[v][3] = q.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[v][i] = expert(v, i) < a.E ? __ldg(row + expert(v, i)) : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) peak = fmaxf(peak, f[v][i] = fmaxf(f[v][i], -INFINITY));
       }
+      peak = O::maxf(peak);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) total += f[v][i] = isinf(peak) ? 0.0f : ex2((f[v][i] - peak) * G_LOG2E);
       total = O::sum(total);
-      const float inv = isinf(top) ? 0.0f : 1.0f / total;
-      __syncwarp();
-      float dot = 0.0f;
-      for (int j = l; j < a.topk; j += LPT)
-        if (inside(j)) dot += out[ids[j]] * inv * (a.scale * __ldg(dw + j));
-      dot = O::sum(dot);
-      __syncwarp();
-      // the sum's terms, then the chosen ones' own
-      for (int e = l; e < a.E; e += LPT) out[e] *= -dot * inv;
-      __syncwarp();
-      for (int j = l; j < a.topk; j += LPT)
-        if (inside(j) && !isinf(top)) out[ids[j]] += ex2((chosen(j) - top) * G_LOG2E) * inv * (a.scale * __ldg(dw + j));
-    } else {
-      float peak = -INFINITY, sum = 1.0f, dot = 0.0f;
-      if (a.renorm) {
-        for (int j = l; j < a.topk; j += LPT) peak = fmaxf(peak, chosen(j));
-        peak = O::maxf(peak);
-      }
-      const bool constant = a.renorm && (a.softmax ? isinf(peak) : peak == -INFINITY);  // the weights do not depend on the scores
-      auto part = [&](float x) {
-        if (a.softmax) return expf(x - peak);
-        return expf(fminf(x, 0.0f) - (a.renorm ? fminf(peak, 0.0f) : 0.0f)) / (1.0f + expf(-fabsf(x)));
-      };
-      if (a.renorm) {
-        sum = 0.0f;
-        for (int j = l; j < a.topk; j += LPT) {
-          const float v = constant ? 0.0f : part(chosen(j));
-          sum += v;
-          dot += v * (a.scale * __ldg(dw + j));
-        }
-        sum = O::sum(sum);
-        dot = O::sum(dot) / sum;
-      }
+    } else if (a.renorm) {
+      for (int j = l; j < a.topk; j += LPT) peak = fmaxf(peak, logit(id(j)));
+      peak = O::maxf(peak);
+    }
+    const bool constant = (every || a.renorm) && (a.softmax ? isinf(peak) : peak == -INFINITY);
+    auto part = [&](float x) {  // of a chosen score, before the sum
+      if (constant || x == -INFINITY) return 0.0f;
+      if (a.softmax) return every ? ex2((x - peak) * G_LOG2E) : expf(x - peak);
+      return expf(fminf(x, 0.0f) - (a.renorm ? fminf(peak, 0.0f) : 0.0f)) / (1.0f + expf(-fabsf(x)));
+    };
+    if (every || a.renorm) {
+      float sum = 0.0f;
       for (int j = l; j < a.topk; j += LPT) {
-        if (!inside(j) || constant) continue;
-        const float x = chosen(j), g = a.scale * __ldg(dw + j);
-        float d = part(x) / sum * (a.renorm ? g - dot : g);
-        if (!a.softmax) {
-          const float e = expf(-fabsf(x));  // 1 - s
-          d *= (x > 0.0f ? e : 1.0f) / (1.0f + e);
-        }
-        if (!sparse) out[ids[j]] = d;
-        else if (here) a.dlogits[t * a.E + ids[j]] += d;
+        const float v = part(logit(id(j)));
+        sum += v;
+        dot += v * grad(j);
       }
+      if (!every) total = O::sum(sum);
+      dot = O::sum(dot);
+      dot = constant ? 0.0f : dot / total;
+    } else {
+      total = 1.0f;
     }
-    if (sparse) continue;
-    __syncwarp();
-    if (here) {
-      float* dst = a.dlogits + t * a.E;
-      if (a.E % 4 == 0) {
-        for (int e = l * 4; e < a.E; e += LPT * 4) {
-          float4 v = *reinterpret_cast<const float4*>(out + e);
-          if (a.accumulate) {
-            const float4 o = *reinterpret_cast<const float4*>(dst + e);
-            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    const float inv = constant ? 0.0f : 1.0f / total;
+    // the rows without the chosen ones' own terms
+    if (!a.accumulate || every) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float4 q = make_float4(-f[v][0] * inv * dot, -f[v][1] * inv * dot, -f[v][2] * inv * dot, -f[v][3] * inv * dot);
+        if (!every) q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int e = expert(v, 0);
+        if (vec) {
+          if (here && e < a.E) {
+            if (a.accumulate) {
+              const float4 o = *reinterpret_cast<const float4*>(out + e);
+              q.x += o.x, q.y += o.y, q.z += o.z, q.w += o.w;
+            }
+            *reinterpret_cast<float4*>(out + e) = q;
           }
-          *reinterpret_cast<float4*>(dst + e) = v;
+        } else {
+          const float s[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (here && expert(v, i) < a.E) out[expert(v, i)] = a.accumulate ? out[expert(v, i)] + s[i] : s[i];
         }
-      } else {
-        for (int e = l; e < a.E; e += LPT) dst[e] = a.accumulate ? dst[e] + out[e] : out[e];
       }
+      __syncwarp();
     }
-    __syncwarp();
-    if (!every)
-      for (int j = l; j < a.topk; j += LPT)
-        if (inside(j)) out[ids[j]] = 0.0f;
+    for (int j = l; j < a.topk; j += LPT) {
+      const int e = id(j);
+      if (e < 0 || !here) continue;
+      const float x = logit(e), g = grad(j), p = part(x) * inv;
+      float d = a.renorm || every ? p * (g - dot) : p * g;
+      if (!a.softmax) {
+        const float small = expf(-fabsf(x));
+        d *= (x > 0.0f ? small : 1.0f) / (1.0f + small);
+      }
+      // over the zero or the row's term; with accumulate onto what was there, of which
+      // the row's term is a part by now
+      out[e] = !a.accumulate ? d : out[e] + (every ? p * g : d);
+    }
   }
 }
 
@@ -957,13 +1023,33 @@ flux_status_t launch_wide(const GroupGateArgs& a, const DeviceInfo& dev, cudaStr
   return launch_wide<0, 8, GROUPED>(a, dev, s);
 }
 
-template <int LPT>
-flux_status_t launch_gate_bwd(const GroupGateArgs& a, cudaStream_t s) {
-  constexpr int TPC = GG_WARPS * (32 / LPT);
-  const size_t smem = static_cast<size_t>(TPC) * ((a.E + 3) & ~3) * sizeof(float);  // at most 32 KB
-  const int grid = std::min(ceil_div(a.T, TPC), GG_SMS * 4);
-  const cudaError_t e = launch_behind(group_gate_bwd_kernel<LPT>, dim3(grid), GG_THREADS, smem, s, a);
+template <int SLOTS>
+flux_status_t launch_bwd_chosen(const GroupGateArgs& a, cudaStream_t s) {
+  const int grid = std::min(ceil_div(a.T, GG_WARPS * (32 / SLOTS)), GG_SMS * 8);
+  const cudaError_t e = launch_behind(group_gate_bwd_chosen_kernel<SLOTS>, dim3(grid), GG_THREADS, 0, s, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
+}
+
+template <int LPT, int V>
+flux_status_t launch_bwd(const GroupGateArgs& a, cudaStream_t s) {
+  const int grid = std::min(ceil_div(a.T, GG_WARPS * (32 / LPT)), GG_SMS * 6);
+  const cudaError_t e = launch_behind(group_gate_bwd_kernel<LPT, V>, dim3(grid), GG_THREADS, 0, s, a);
+  return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
+}
+
+flux_status_t launch_gate_bwd(const GroupGateArgs& a, cudaStream_t s) {
+  if (!(a.softmax && !a.renorm) && a.topk <= 32) {
+    if (a.topk <= 2) return launch_bwd_chosen<2>(a, s);
+    if (a.topk <= 4) return launch_bwd_chosen<4>(a, s);
+    if (a.topk <= 8) return launch_bwd_chosen<8>(a, s);
+    return launch_bwd_chosen<32>(a, s);
+  }
+  if (a.E <= 32) return launch_bwd<8, 1>(a, s);
+  if (a.E <= 64) return launch_bwd<8, 2>(a, s);
+  if (a.E <= 128) return launch_bwd<32, 1>(a, s);
+  if (a.E <= 256) return launch_bwd<32, 2>(a, s);
+  if (a.E <= 512) return launch_bwd<32, 4>(a, s);
+  return launch_bwd<32, 8>(a, s);
 }
 
 }  // namespace
@@ -1054,5 +1140,5 @@ extern "C" flux_status_t flux_moe_group_gate_bwd(int T, int E, int topk, int sco
   a.accumulate = accumulate != 0;
   a.scale = scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return E <= 64 ? launch_gate_bwd<8>(a, s) : launch_gate_bwd<32>(a, s);
+  return launch_gate_bwd(a, s);
 }
