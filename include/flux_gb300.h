@@ -59,8 +59,8 @@
  *   - Workspaces must be 256-byte aligned, at least flux_*workspace_size()
  *     bytes, and zero-filled once before first use (flux_workspace_init).
  *     Every successful call leaves its workspace zero again (the MoE layers leave
- *     their routing and staged rows in it, flux_q8_gemm of more than 32 rows its
- *     widened operands).  The block-norm, layer-norm, router, 4-bit and 8-bit
+ *     their routing and staged rows in it, flux_q8_gemm of more than 8 rows its
+ *     widened tokens and partial sums).  The block-norm, layer-norm, router, 4-bit and 8-bit
  *     calls need zeros in the first 256 bytes only.  Calls that share
  *     one workspace must be ordered on the GPU (same stream or events); calls
  *     that overlap on the GPU need separate workspaces.
@@ -822,7 +822,7 @@ flux_status_t flux_moe_group_gate_bwd(int T, int E, int topk, int score, int ren
  * out[m, n] = x_scales[m] w_scales[n] sum_k x[m, k] w[n, k] (+ bias[n]): a linear
  * layer whose weights are held in 8 bits with a scale for each output channel and
  * whose inputs are quantised token by token as they come.
- * Requires K % 16 == 0, K < 131072, N % 8 == 0, N <= 2^30 (FLUX_ERR_UNSUPPORTED).
+ * Requires K % 16 == 0, K < 131072, N % 8 == 0, N and M <= 2^30 (FLUX_ERR_UNSUPPORTED).
  * These calls take whole matrices and rows; they know no ranks. */
 
 /* 8-bit codes and the scale of each of `rows` rows of 16-bit numbers:
@@ -842,7 +842,7 @@ size_t flux_q8_workspace_size(int M, int N, int K);
 /*   x  device int8[M x K]   x_scales  device float[M]
  *   w  device int8[N x K]   w_scales  device float[N]   bias  device [N] in dtype, or NULL
  *   out  device [M x N] in dtype
- * The integer sums are exact for M <= 32; for more rows as long as they stay below
+ * The integer sums are exact for M <= 8; for more rows as long as they stay below
  * 2^24, past that to 24 bits.  K = 0 writes the bias, or zeros. */
 flux_status_t flux_q8_gemm(int M, int N, int K, flux_dtype_t dtype, const int8_t* x,
                            const float* x_scales, const int8_t* w, const float* w_scales,

@@ -22,7 +22,7 @@ namespace {
 
 constexpr int Q8_SMS = 152;
 constexpr int Q8_MAX_K = 131072 - 16;  // 2^14 K stays within 32 bits
-constexpr int Q8_FEW = 32;             // rows up to which the few-row kernel is taken
+constexpr int Q8_FEW = 8;              // rows up to which the few-row kernel is taken
 
 // ---------------------------------------------------------------- quantisation
 
@@ -274,7 +274,9 @@ flux_status_t quantize(int rows, int K, const void* x, int8_t* q, float* scales,
 }
 
 bool q8_sizes_ok(int M, int N, int K) { return M >= 0 && N >= 0 && K >= 0; }
-bool q8_sizes_supported(int N, int K) { return K % 16 == 0 && K <= Q8_MAX_K && N % 8 == 0 && N <= (1 << 30); }
+bool q8_sizes_supported(int M, int N, int K) {
+  return K % 16 == 0 && K <= Q8_MAX_K && N % 8 == 0 && N <= (1 << 30) && M <= (1 << 30);
+}
 
 }  // namespace
 }  // namespace flux
@@ -296,7 +298,7 @@ extern "C" flux_status_t flux_q8_quantize(int rows, int K, flux_dtype_t dtype, c
 }
 
 extern "C" size_t flux_q8_workspace_size(int M, int N, int K) {
-  if (!q8_sizes_ok(M, N, K) || !q8_sizes_supported(N, K)) return 0;
+  if (!q8_sizes_ok(M, N, K) || !q8_sizes_supported(M, N, K)) return 0;
   if (M == 0 || N == 0 || K == 0) return WS_HEADER;
   return WS_HEADER + (M <= Q8_FEW ? few_plan(M, N, K).total : q8_gemm_bytes(M, N, K));
 }
@@ -305,7 +307,7 @@ extern "C" flux_status_t flux_q8_gemm(int M, int N, int K, flux_dtype_t dtype, c
                                       const int8_t* w, const float* w_scales, const void* bias, void* out,
                                       void* workspace, size_t workspace_bytes, void* stream) {
   if (!q8_sizes_ok(M, N, K) || (dtype != FLUX_F16 && dtype != FLUX_BF16)) return FLUX_ERR_INVALID_ARG;
-  if (!q8_sizes_supported(N, K)) return FLUX_ERR_UNSUPPORTED;
+  if (!q8_sizes_supported(M, N, K)) return FLUX_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return FLUX_OK;
   if (out == nullptr || (K > 0 && (x == nullptr || w == nullptr || x_scales == nullptr || w_scales == nullptr)))
     return FLUX_ERR_INVALID_ARG;

@@ -116,8 +116,8 @@ class Product:
     def check(self):
         got = self.run()
         want, mag, reach = oracle.q8_gemm(self.x, self.xs, self.w, self.ws, self.b)
-        # exact sums: the scales' two roundings, the bias's; else one rounding to 24 bits for 16 codes too
-        if self.M > 32 and reach >= 1 << 24:
+        # exact sums (up to 8 rows: whole numbers): the scales' two roundings, the bias's; else one rounding to 24 bits for 16 codes too
+        if self.M > 8 and reach >= 1 << 24:
             big = (np.abs(self.x.astype(np.float64)) @ np.abs(self.w.astype(np.float64)).T) * self.xs[:, None] * self.ws[None]
             check16(got, want, mag + big, self.dtype, depth=8 + 2 * self.K // 16)
         else:
