@@ -12,10 +12,12 @@
 // 350 cycles of products, which 128 bytes a cycle cannot feed; this way 38 KB).  The
 // tokens, which every channel tile reads, are widened once by a small kernel before.
 //
-// A pair of CTAs computes 256 channels x up to 192 tokens (tcgen05.mma.cta_group::2,
+// A pair of CTAs computes 256 channels x up to 160 tokens (tcgen05.mma.cta_group::2,
 // 128 channels and half of the tokens' codes in each CTA).  TMEM: two accumulators of
-// 192 columns, so that one tile is scaled and stored under the products of the next,
-// and two buffers of the widened codes of a step.  Where there are fewer tiles than pairs K is
+// 160 columns, so that one tile is scaled and stored under the products of the next,
+// and three buffers of the widened codes of a step (with 192 columns there is room for
+// two, and a buffer's round, products, commit, widening, arrival, takes longer than the
+// products of the other: 4096 x 4096 x 14336 320 us).  Where there are fewer tiles than pairs K is
 // cut into parts, whose fp32 sums q8_parts_kernel adds in order.
 #include <limits.h>
 
@@ -30,11 +32,11 @@ namespace {
 
 constexpr int G_K = 128;                 // codes of a step
 constexpr int G_CH = 256, G_ROWS = 128;  // channels of a tile, of a CTA
-constexpr int G_TOK = 192;               // most tokens of a tile
+constexpr int G_TOK = 160;               // most tokens of a tile
 constexpr int G_RAW = G_ROWS * G_K, G_RAW_STAGES = 6;
 constexpr int G_ATOM = G_TOK / 2 * 128;  // 64 widened codes of a CTA's tokens
-constexpr int G_TOK_BYTES = 2 * G_ATOM, G_TOK_STAGES = 4;
-constexpr int G_A = 2 * G_TOK, G_A_COLS = 64, G_A_BUFS = 2;  // TMEM columns of the widened weights of a step
+constexpr int G_TOK_BYTES = 2 * G_ATOM, G_TOK_STAGES = 5;
+constexpr int G_A = 2 * G_TOK, G_A_COLS = 64, G_A_BUFS = 3;  // TMEM columns of the widened weights of a step
 constexpr int G_SMEM = G_RAW_STAGES * G_RAW + G_TOK_STAGES * G_TOK_BYTES + 1024 + 512;
 // warps: 0 weights, 1 tokens, 2 products, 4..7 epilogue, 8..15 widening
 constexpr int G_THREADS = 16 * 32;
@@ -143,10 +145,10 @@ q8_gemm_kernel(const __grid_constant__ Q8GemmParams p) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < G_RAW_STAGES; ++i) {
       mbar_init(smem_u32(&rawfull[i]), 1);
-      mbar_init(smem_u32(&rawempty[i]), 8);  // the widening warps of this CTA
+      mbar_init(smem_u32(&rawempty[i]), 4);  // the widening warps of the step
     }
     for (int i = 0; i < G_TOK_STAGES; ++i) {
-      mbar_init(smem_u32(&full[i]), 17);  // a step's tokens, and the widening warps of both CTAs
+      mbar_init(smem_u32(&full[i]), 9);  // a step's tokens, and its widening warps of both CTAs
       mbar_init(smem_u32(&done[i]), 1);   // its products
     }
     for (int i = 0; i < 2; ++i) {
@@ -264,41 +266,45 @@ q8_gemm_kernel(const __grid_constant__ Q8GemmParams p) {
     }
     __syncwarp();
   } else if (warp >= 8) {
-    // Widening.  A thread takes 64 codes of one channel: warps 8..11 the first half of
-    // every step, 12..15 the second.
-    const int half = (warp - 8) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16, raw = smem_u32(base) + row * 128;
+    // Widening.  A thread takes the 128 codes of one channel; warps 8..11 the even steps,
+    // 12..15 the odd ones, so that a warp waits once for two steps.
+    const uint32_t odd = (warp - 8) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lanes = quarter * 32 << 16, raw = smem_u32(base) + row * 128;
     uint32_t n = 0;
     bool ok = true;
     for (int u = pair; ok && u < units; u += pairs) {
       const Q8Unit w(p, u);
       for (int k = w.k0; k < w.k1; ++k, ++n) {
+        if ((n & 1u) != odd) continue;
         const uint32_t s = n % G_RAW_STAGES;
         if (!warp_wait(smem_u32(&rawfull[s]), n / G_RAW_STAGES & 1u, c, W_FULL, s, false)) {
           ok = false;
           break;
         }
-        const uint32_t src = raw + s * G_RAW;
-        uint4 v[4];
+        const uint32_t src = raw + s * G_RAW, ta = tmem + G_A + n % G_A_BUFS * G_A_COLS + lanes;
+        uint4 v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src + (((half * 4 + j) ^ (row & 7)) << 4));
-        uint32_t r[32];
+        for (int j = 0; j < 8; ++j) v[j] = ld_shared_v4(src + ((j ^ (row & 7)) << 4));
+        uint32_t r[2][32];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          widen(v[j].x, r[j * 8], r[j * 8 + 1]);
-          widen(v[j].y, r[j * 8 + 2], r[j * 8 + 3]);
-          widen(v[j].z, r[j * 8 + 4], r[j * 8 + 5]);
-          widen(v[j].w, r[j * 8 + 6], r[j * 8 + 7]);
+        for (int j = 0; j < 8; ++j) {
+          uint32_t(&o)[32] = r[j >> 2];
+          const int at = (j & 3) * 8;
+          widen(v[j].x, o[at], o[at + 1]);
+          widen(v[j].y, o[at + 2], o[at + 3]);
+          widen(v[j].z, o[at + 4], o[at + 5]);
+          widen(v[j].w, o[at + 6], o[at + 7]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&rawempty[s]));
-        const uint32_t ab = n % G_A_BUFS, before = n - G_A_BUFS;  // the step that had the buffer
-        if (n >= G_A_BUFS && !warp_wait(smem_u32(&done[before % G_TOK_STAGES]), before / G_TOK_STAGES & 1u, c, W_EMPTY, 32 + ab, true)) {
+        const uint32_t before = n - G_A_BUFS;  // the step that had the buffer
+        if (n >= G_A_BUFS && !warp_wait(smem_u32(&done[before % G_TOK_STAGES]), before / G_TOK_STAGES & 1u, c, W_EMPTY, 32, true)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        tmem_st_32x32b_x32(tmem + G_A + ab * G_A_COLS + half * 32 + lanes, r);
+        tmem_st_32x32b_x32(ta, r[0]);
+        tmem_st_32x32b_x32(ta + 32, r[1]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_light(mapa_shared(smem_u32(&full[n % G_TOK_STAGES]), 0u));
