@@ -117,7 +117,7 @@ __device__ __forceinline__ void each_logit(const float* row, int E, int l, F&& f
   if (E % 4 == 0) {
 #pragma unroll 2
     for (int e = l * 4; e < E; e += LPT * 4) {
-      const float4 q = __ldg(reinterpret_cast<const float4*>(row + e));
+      const float4 q = load_global(reinterpret_cast<const float4*>(row + e));
       f(e, fmaxf(q.x, -INFINITY));
       f(e + 1, fmaxf(q.y, -INFINITY));
       f(e + 2, fmaxf(q.z, -INFINITY));
@@ -125,7 +125,7 @@ __device__ __forceinline__ void each_logit(const float* row, int E, int l, F&& f
     }
   } else {
 #pragma unroll 4
-    for (int e = l; e < E; e += LPT) f(e, fmaxf(__ldg(row + e), -INFINITY));
+    for (int e = l; e < E; e += LPT) f(e, fmaxf(load_global(row + e), -INFINITY));
   }
 }
 
@@ -176,7 +176,7 @@ __device__ __noinline__ void choose64(const GroupGateArgs& a, const float* row, 
   constexpr unsigned long long LEAST = 0x000FFFFFFFFFFFFFull;  // order_of(-inf)
   const uint32_t mask = LPT == 32 ? 0xFFFFFFFFu : some;
   auto logit = [&](int e) {
-    const float x = __ldg(row + e);
+    const float x = load_global(row + e);
     return static_cast<double>(x != x ? -INFINITY : x);
   };
   double top = -INFINITY, total = 0.0;
@@ -194,7 +194,7 @@ __device__ __noinline__ void choose64(const GroupGateArgs& a, const float* row, 
   unsigned long long c[MINE];  // experts l, l + LPT, ...
 #pragma unroll 1
   for (int e = l, i = 0; e < a.E; e += LPT, ++i) {
-    const double x = logit(e), v = a.bias != nullptr ? score(x) + static_cast<double>(__ldg(a.bias + e)) : x;
+    const double x = logit(e), v = a.bias != nullptr ? score(x) + static_cast<double>(load_global(a.bias + e)) : x;
     c[i] = v != v ? LEAST : order_of(v);
   }
   uint32_t in = 0xFFFFFFFFu;
@@ -322,7 +322,7 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
       if (biased) {
         auto third = [&](int e) {
           const int at = place(a, e);
-          r.val[at] = fmaxf(r.val[at] * inv + __ldg(a.bias + e), -INFINITY);
+          r.val[at] = fmaxf(r.val[at] * inv + load_global(a.bias + e), -INFINITY);
         };
         if (a.E % 4 == 0) {
           for (int e = l * 4; e < a.E; e += LPT * 4) third(e), third(e + 1), third(e + 2), third(e + 3);
@@ -332,7 +332,7 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
       }
     } else {
       each_logit<LPT>(row, a.E, l, [&](int e, float x) {
-        r.val[place(a, e)] = biased ? fmaxf(score(x) + __ldg(a.bias + e), -INFINITY) : x;
+        r.val[place(a, e)] = biased ? fmaxf(score(x) + load_global(a.bias + e), -INFINITY) : x;
       });
     }
     __syncwarp();
@@ -419,7 +419,7 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
     auto expert = [&](int j) { return expert_at(a, r.kept, r.pick[j]); };
     if (biased) {
       auto apart = [&](float hi, float lo) { return hi - lo > unsure + 0x1p-23f * (fabsf(hi) + fabsf(lo)); };
-      auto same = [&](int e, int f) { return __ldg(row + e) == __ldg(row + f) && __ldg(a.bias + e) == __ldg(a.bias + f); };
+      auto same = [&](int e, int f) { return load_global(row + e) == load_global(row + f) && load_global(a.bias + e) == load_global(a.bias + f); };
       const float last = r.val[place(a, expert(a.topk - 1))];
       uint32_t close = m != 0u && !apart(last, value_of(m));
       for (int j = l; j + 1 < a.topk; j += LPT) close |= !apart(r.val[place(a, expert(j))], r.val[place(a, expert(j + 1))]);
@@ -441,7 +441,7 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
     if (doubt) choose64<LPT>(a, row, r.kept, r.pick, l, LPT == 32 ? 0xFFFFFFFFu : ((1u << LPT % 32) - 1u) << (sub * LPT));
     __syncwarp();
     // the weights
-    auto chosen = [&](int j) { return fmaxf(__ldg(row + expert(j)), -INFINITY); };
+    auto chosen = [&](int j) { return fmaxf(load_global(row + expert(j)), -INFINITY); };
     float peak = -INFINITY;
     if (a.renorm) {
       for (int j = l; j < a.topk; j += LPT) peak = fmaxf(peak, chosen(j));
@@ -506,7 +506,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
   for (int q = 0; q < LISTS; ++q) list[(q * 32 + lane) * 5 + 4] = NAN;
   wait_for_previous();
   if constexpr (BIASED) {
-    for (int e = threadIdx.x; e < wide; e += GG_THREADS) bias[e] = e < a.E ? __ldg(a.bias + e) : -INFINITY;
+    for (int e = threadIdx.x; e < wide; e += GG_THREADS) bias[e] = e < a.E ? load_global(a.bias + e) : -INFINITY;
     __syncthreads();
   }
   auto fetch = [&](long long at, float* dst) {
@@ -817,10 +817,10 @@ group_gate_bwd_chosen_kernel(const __grid_constant__ GroupGateArgs a) {
     int id = -1;
     float g = 0.0f, x = -INFINITY;
     if (t < a.T && l < a.topk) {
-      id = __ldg(a.ids_in + t * a.topk + l);
+      id = load_global(a.ids_in + t * a.topk + l);
       if (id >= a.E) id = -1;
-      g = a.scale * __ldg(a.dweights + t * a.topk + l);
-      if (id >= 0) x = fmaxf(__ldg(a.logits + t * a.E + id), -INFINITY);
+      g = a.scale * load_global(a.dweights + t * a.topk + l);
+      if (id >= 0) x = fmaxf(load_global(a.logits + t * a.E + id), -INFINITY);
     }
     if (!a.accumulate) {
       float* rows = a.dlogits + t0 * a.E;
@@ -872,11 +872,11 @@ group_gate_bwd_kernel(const __grid_constant__ GroupGateArgs a) {
     float* out = a.dlogits + t * a.E;
     auto expert = [&](int v, int i) { return vec ? (v * LPT + l) * 4 + i : (v * 4 + i) * LPT + l; };
     auto id = [&](int j) {
-      const int e = __ldg(a.ids_in + t * a.topk + j);
+      const int e = load_global(a.ids_in + t * a.topk + j);
       return e < a.E ? e : -1;
     };
-    auto grad = [&](int j) { return a.scale * __ldg(a.dweights + t * a.topk + j); };
-    auto logit = [&](int e) { return e >= 0 ? fmaxf(__ldg(row + e), -INFINITY) : -INFINITY; };
+    auto grad = [&](int j) { return a.scale * load_global(a.dweights + t * a.topk + j); };
+    auto logit = [&](int e) { return e >= 0 ? fmaxf(load_global(row + e), -INFINITY) : -INFINITY; };
     float f[V][4] = {};
     float peak = -INFINITY, total = 0.0f, dot = 0.0f;
     if (every) {
@@ -884,11 +884,11 @@ group_gate_bwd_kernel(const __grid_constant__ GroupGateArgs a) {
       for (int v = 0; v < V; ++v) {
         if (vec) {
           const int e = expert(v, 0);
-          const float4 q = e < a.E ? __ldg(reinterpret_cast<const float4*>(row + e)) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          const float4 q = e < a.E ? load_global(reinterpret_cast<const float4*>(row + e)) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
           f[v][0] = q.x, f[v][1] = q.y, f[v][2] = q.z, f[v][3] = q.w;
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f[v][i] = expert(v, i) < a.E ? __ldg(row + expert(v, i)) : -INFINITY;
+          for (int i = 0; i < 4; ++i) f[v][i] = expert(v, i) < a.E ? load_global(row + expert(v, i)) : -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) peak = fmaxf(peak, f[v][i] = fmaxf(f[v][i], -INFINITY));

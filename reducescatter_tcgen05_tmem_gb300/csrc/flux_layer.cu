@@ -77,10 +77,10 @@ struct Dropout {
   f32x2 scale;
   __device__ __forceinline__ Dropout(const LayerNormArgs& a, bool wanted) : k0(0), k1(0), keep(a.keep), offset(0), scale(both(a.scale)) {
     if (wanted && a.keep < 65536u) {
-      const unsigned long long seed = __ldg(a.rng);
+      const unsigned long long seed = load_global(a.rng);
       k0 = static_cast<uint32_t>(seed);
       k1 = static_cast<uint32_t>(seed >> 32);
-      offset = __ldg(a.rng + 1);
+      offset = load_global(a.rng + 1);
     }
   }
   __device__ __forceinline__ bool on() const { return keep < 65536u; }
@@ -161,7 +161,7 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a) {
   const uint32_t one = pack2<DT>(1.0f, 1.0f);
   auto weights = [&](const void* base, uint32_t other, int v) {
     if (base == nullptr || column(v) >= a.H) return make_uint4(other, other, other, other);
-    return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + column(v)));
+    return load_global(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + column(v)));
   };
   uint4 wq[V], bq[V];
 #pragma unroll
@@ -285,8 +285,8 @@ layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a) {
       }
       Row r;
       r.rank = rank_a;
-      r.mean = HAS_U ? __ldg(a.mean + t_a) : 0.0f;
-      r.r = HAS_U ? __ldg(a.rstd + t_a) : 0.0f;
+      r.mean = HAS_U ? load_global(a.mean + t_a) : 0.0f;
+      r.r = HAS_U ? load_global(a.rstd + t_a) : 0.0f;
       queue[DEPTH - 1] = r;
       const size_t at = static_cast<size_t>(t_a - rank_a * a.rows_per_rank) * a.H + lane * 8;
       const uint16_t* px = HAS_U ? static_cast<const uint16_t*>(a.x[rank_a]) + at : nullptr;
@@ -324,7 +324,7 @@ layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
       wq[v] = a.weight != nullptr && column(v) < a.H
-                  ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + column(v)))
+                  ? load_global(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + column(v)))
                   : make_uint4(one, one, one, one);
   }
   const Dropout drop(a, a.has_dy != 0);

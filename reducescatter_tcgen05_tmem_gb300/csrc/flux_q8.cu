@@ -22,7 +22,6 @@ namespace {
 
 constexpr int Q8_SMS = 152;
 constexpr int Q8_MAX_K = 131072 - 16;  // 2^14 K stays within 32 bits
-constexpr int Q8_FEW = 8;              // rows up to which the few-row kernel is taken
 
 // ---------------------------------------------------------------- quantisation
 
@@ -35,7 +34,7 @@ constexpr int QZ_VECS = 4;  // vectors of 8 that a thread holds of a row
 // A row that holds a NaN or an infinity gets such a scale and codes of zero.
 template <int DT, int THREADS>
 __global__ void __launch_bounds__(THREADS)
-q8_quantize_kernel(const void* __restrict__ x, int8_t* __restrict__ q, float* __restrict__ scales, int K) {
+q8_quantize_kernel(const void* x, int8_t* q, float* scales, int K) {
   __shared__ uint32_t red[THREADS / 32];
   wait_for_previous();
   const size_t at = static_cast<size_t>(blockIdx.x) * K;
@@ -49,11 +48,11 @@ q8_quantize_kernel(const void* __restrict__ x, int8_t* __restrict__ q, float* __
 #pragma unroll
   for (int i = 0; i < QZ_VECS; ++i) {
     const int v = i * THREADS + threadIdx.x;
-    held[i] = v < nvec ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
+    held[i] = v < nvec ? load_global(src + v) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < QZ_VECS; ++i) see(held[i]);
-  for (int v = QZ_VECS * THREADS + threadIdx.x; v < nvec; v += THREADS) see(__ldg(src + v));
+  for (int v = QZ_VECS * THREADS + threadIdx.x; v < nvec; v += THREADS) see(load_global(src + v));
   top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = top;
   __syncthreads();
@@ -83,7 +82,7 @@ q8_quantize_kernel(const void* __restrict__ x, int8_t* __restrict__ q, float* __
     const int v = i * THREADS + threadIdx.x;
     if (v < nvec) put(v, held[i]);
   }
-  for (int v = QZ_VECS * THREADS + threadIdx.x; v < nvec; v += THREADS) put(v, __ldg(src + v));
+  for (int v = QZ_VECS * THREADS + threadIdx.x; v < nvec; v += THREADS) put(v, load_global(src + v));
   if (threadIdx.x == 0) scales[blockIdx.x] = scale;
 }
 
@@ -95,27 +94,31 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr int FEW_WARPS = 8, FEW_THREADS = FEW_WARPS * 32;
+constexpr int FEW_ROWS = 8;             // of x: the columns of one instruction
+constexpr int FEW_WARPS = 8, FEW_THREADS = FEW_WARPS * 32, FEW_CTAS = 3;
 constexpr int FEW_CH = 16;              // channels of a block: the rows of one instruction
 constexpr int FEW_K = FEW_WARPS * 64;   // of a step: 64 codes a warp
+constexpr int FEW_DEPTH = 4;            // steps on their way
+constexpr int FEW_SLOT = FEW_ROWS * FEW_CH;
 
 struct FewPlan {
-  int blocks, steps;    // of channels; of K in a block
-  int ctas;
-  size_t slot, total;   // ints of one partial block; bytes past the header
+  int blocks, steps;  // of channels; of K in a block
+  int ctas;           // as many as blocks: each has one; else equal stretches of steps
+  size_t total;       // bytes past the header
 };
 
-template <int NT>
-__host__ __device__ constexpr int few_depth() { return NT <= 2 ? 4 : 2; }
-
-FewPlan few_plan(int M, int N, int K) {
+// Whole blocks leave some SMs idle at the end, equal stretches need the parts of cut
+// blocks joined by a second kernel, which costs about as much as 11 steps (4096 x 4096:
+// 27 steps an SM on average, 32 with whole blocks, which are faster by 1.5 us; 28672 x
+// 8192: 189 against 224, and stretches are faster by 5 us).
+FewPlan few_plan(int N, int K) {
   FewPlan p{};
-  const int rows = M <= 8 ? 8 : M <= 16 ? 16 : 32;
   p.blocks = ceil_div(N, FEW_CH);
   p.steps = ceil_div(K, FEW_K);
-  p.ctas = static_cast<int>(std::min<long long>(static_cast<long long>(p.blocks) * p.steps, 2 * Q8_SMS));
-  p.slot = static_cast<size_t>(rows) * FEW_CH;
-  p.total = sizeof(int) * p.slot * 2 * p.ctas;
+  const long long units = static_cast<long long>(p.blocks) * p.steps;
+  const long long whole = static_cast<long long>(ceil_div(p.blocks, Q8_SMS)) * p.steps, even = units / Q8_SMS + 11;
+  p.ctas = static_cast<int>(whole <= even ? p.blocks : std::min<long long>(units, FEW_CTAS * Q8_SMS));
+  p.total = p.ctas == p.blocks ? 0 : sizeof(int) * FEW_SLOT * 2 * static_cast<size_t>(p.ctas);
   return p;
 }
 
@@ -125,81 +128,86 @@ __host__ __device__ __forceinline__ long long first_unit(long long units, int ct
 template <int DT>
 __device__ __forceinline__ void few_store(const Q8Args& a, int ch, int row, int sum) {
   if (ch >= a.N || row >= a.M) return;
-  float v = static_cast<float>(sum) * __ldg(a.x_scales + row) * __ldg(a.w_scales + ch);
+  float v = static_cast<float>(sum) * load_global(a.x_scales + row) * load_global(a.w_scales + ch);
   if (a.bias != nullptr) v += load16<DT>(a.bias, ch);
   static_cast<uint16_t*>(a.out)[static_cast<size_t>(row) * a.N + ch] = static_cast<uint16_t>(pack2<DT>(v, 0.0f));
 }
 
-// One CTA takes an equal stretch of the steps of all blocks of 16 channels, its
-// warps 64 codes of a step each.  A lane's 16 bytes of a weight row and of a token
-// are the operands of two instructions (the order of K within them is the lanes'
-// own, the same for both sides).  Weights and tokens are loaded D steps ahead into
+// Up to 8 rows.  A CTA takes a stretch of the steps of all blocks of 16 channels, its
+// warps 64 codes of a step each.  A lane's 16 bytes of a weight row and of a token are
+// the operands of two instructions (the order of K within them is the lanes' own, the
+// same for both sides).  Weights and tokens are loaded FEW_DEPTH steps ahead into
 // registers.  The warps' sums meet in shared memory at the end of a block; a block
 // that a CTA has only a part of goes to the workspace, two places for each CTA, and
 // q8_few_join_kernel adds the parts.
-template <int DT, int NT>
-__global__ void __launch_bounds__(FEW_THREADS, 2)
+//
+// The 8-bit instruction is no faster than 16 cycles an SM, so that 16 rows would be
+// bound by it (13 rows of 28672 x 8192: 70 us, tensor pipe 75 % busy); 8 need half the
+// time of their weights.
+template <int DT>
+__global__ void __launch_bounds__(FEW_THREADS, FEW_CTAS)
 q8_few_kernel(const __grid_constant__ Q8Args a, int* parts, int steps, long long units) {
-  constexpr int D = few_depth<NT>(), ROWS = NT * 8, SLOT = ROWS * FEW_CH;
-  __shared__ int red[FEW_WARPS][SLOT];
+  __shared__ int red[FEW_WARPS][FEW_SLOT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const long long u0 = first_unit(units, gridDim.x, blockIdx.x), u1 = first_unit(units, gridDim.x, blockIdx.x + 1);
+  const int first_block = static_cast<int>(u0 / steps), first_step = static_cast<int>(u0 - static_cast<long long>(first_block) * steps);
+  int left_a = static_cast<int>(u1 - u0), left = left_a;  // steps to fetch, to work on
+  // what is fetched next: 16 bytes of channels g and g + 8 of a block, and of token g
+  const size_t pitch = static_cast<size_t>(a.K);
+  int step_a = first_step, k_a = first_step * FEW_K + warp * 64 + t * 16, n_a = first_block * FEW_CH + g;
+  const int8_t* w_a = a.w + static_cast<size_t>(n_a) * pitch + k_a;
+  const int8_t* x_a = a.x + static_cast<size_t>(g) * pitch + k_a;
   wait_for_previous();
-  uint4 w0[D], w1[D], xs[D][NT];
-  int block_a = static_cast<int>(u0 / steps), step_a = static_cast<int>(u0 % steps);
-  long long u_a = u0;
+  uint4 lo[FEW_DEPTH], hi[FEW_DEPTH], xs[FEW_DEPTH];
   const uint4 none = make_uint4(0, 0, 0, 0);
-  auto fetch = [&](uint4& lo, uint4& hi, uint4 (&x)[NT]) {
-    const int k = step_a * FEW_K + warp * 64 + t * 16;
-    const bool in = u_a < u1 && k < a.K;
-    const int n = block_a * FEW_CH + g;
-    const int8_t* p = a.w + static_cast<size_t>(n) * a.K + k;
-    lo = in && n < a.N ? __ldg(reinterpret_cast<const uint4*>(p)) : none;
-    hi = in && n + 8 < a.N ? __ldg(reinterpret_cast<const uint4*>(p + 8 * static_cast<size_t>(a.K))) : none;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int row = j * 8 + g;
-      x[j] = in && row < a.M ? __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(row) * a.K + k)) : none;
-    }
-    ++u_a;
-    if (++step_a == steps) {
+  auto fetch = [&](uint4& l, uint4& h, uint4& x) {
+    const bool in = left_a > 0 && k_a < a.K;
+    l = in && n_a < a.N ? load_global(reinterpret_cast<const uint4*>(w_a)) : none;
+    h = in && n_a + 8 < a.N ? load_global(reinterpret_cast<const uint4*>(w_a + 8 * pitch)) : none;
+    x = in && g < a.M ? load_global(reinterpret_cast<const uint4*>(x_a)) : none;
+    --left_a;
+    if (++step_a < steps) {
+      k_a += FEW_K;
+      w_a += FEW_K;
+      x_a += FEW_K;
+    } else {  // the next block's first step
+      const int back = (steps - 1) * FEW_K;
       step_a = 0;
-      ++block_a;
+      k_a -= back;
+      x_a -= back;
+      n_a += FEW_CH;
+      w_a += FEW_CH * pitch - back;
     }
   };
 #pragma unroll
-  for (int i = 0; i < D; ++i) fetch(w0[i], w1[i], xs[i]);
-  int acc[NT][4] = {};
-  int block = static_cast<int>(u0 / steps), step = static_cast<int>(u0 % steps);
+  for (int i = 0; i < FEW_DEPTH; ++i) fetch(lo[i], hi[i], xs[i]);
+  int acc[4] = {};
+  int block = first_block, step = first_step;
   bool from_start = step == 0, first = true;
-  for (long long u = u0; u < u1;) {
+  while (left > 0) {
 #pragma unroll
-    for (int i = 0; i < D; ++i) {
-      if (u >= u1) break;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        mma_s8(acc[j], w0[i].x, w1[i].x, w0[i].y, w1[i].y, xs[i][j].x, xs[i][j].y);
-        mma_s8(acc[j], w0[i].z, w1[i].z, w0[i].w, w1[i].w, xs[i][j].z, xs[i][j].w);
-      }
-      fetch(w0[i], w1[i], xs[i]);
-      ++u;
+    for (int i = 0; i < FEW_DEPTH; ++i) {
+      if (left == 0) break;
+      mma_s8(acc, lo[i].x, hi[i].x, lo[i].y, hi[i].y, xs[i].x, xs[i].y);
+      mma_s8(acc, lo[i].z, hi[i].z, lo[i].w, hi[i].w, xs[i].z, xs[i].w);
+      fetch(lo[i], hi[i], xs[i]);
+      --left;
       const bool ends = ++step == steps;
-      if (ends || u == u1) {
-        // a lane's sums: channels g and g + 8, rows 2 t and 2 t + 1 of each eight
+      if (ends || left == 0) {
+        // a lane's sums: channels g and g + 8 of rows 2 t and 2 t + 1
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            red[warp][(j * 8 + 2 * t + (c & 1)) * FEW_CH + g + (c & 2) * 4] = acc[j][c];
-            acc[j][c] = 0;
-          }
+        for (int c = 0; c < 4; ++c) {
+          red[warp][(2 * t + (c & 1)) * FEW_CH + g + (c & 2) * 4] = acc[c];
+          acc[c] = 0;
+        }
         __syncthreads();
-        for (int o = threadIdx.x; o < SLOT; o += FEW_THREADS) {
+        if (threadIdx.x < FEW_SLOT) {
+          const int o = threadIdx.x;
           int s = 0;
 #pragma unroll
           for (int v = 0; v < FEW_WARPS; ++v) s += red[v][o];
           if (ends && from_start) few_store<DT>(a, block * FEW_CH + o % FEW_CH, o / FEW_CH, s);
-          else parts[(2 * static_cast<size_t>(blockIdx.x) + (first ? 0 : 1)) * SLOT + o] = s;
+          else parts[(2 * static_cast<size_t>(blockIdx.x) + (first ? 0 : 1)) * FEW_SLOT + o] = s;
         }
         __syncthreads();
         first = false;
@@ -213,46 +221,36 @@ q8_few_kernel(const __grid_constant__ Q8Args a, int* parts, int steps, long long
 
 // Adds the parts of the block that CTA b - 1 and CTA b share, if b is the first to
 // continue it, and leaves them zero.
-template <int DT, int NT>
-__global__ void __launch_bounds__(128)
+template <int DT>
+__global__ void __launch_bounds__(FEW_SLOT)
 q8_few_join_kernel(const __grid_constant__ Q8Args a, int* parts, int steps, long long units, int ctas) {
-  constexpr int SLOT = NT * 8 * FEW_CH;
   wait_for_previous();
-  const int b = blockIdx.x + 1;
+  const int b = blockIdx.x + 1, o = threadIdx.x;
   const long long at = first_unit(units, ctas, b);
   const int block = static_cast<int>(at / steps);
   const long long begin = static_cast<long long>(block) * steps, end = begin + steps;
   if (at == begin || first_unit(units, ctas, b - 1) > begin) return;
-  for (int o = threadIdx.x; o < SLOT; o += 128) {
-    int s = 0;
-    for (int c = b - 1; c < ctas; ++c) {
-      const long long u0 = first_unit(units, ctas, c);
-      if (u0 >= end) break;
-      // a CTA's first block is in its first place, the one it ends in the second
-      int* p = parts + (2 * static_cast<size_t>(c) + (u0 >= begin ? 0 : 1)) * SLOT + o;
-      s += *p;
-      *p = 0;
-    }
-    few_store<DT>(a, block * FEW_CH + o % FEW_CH, o / FEW_CH, s);
+  int s = 0;
+  for (int c = b - 1; c < ctas; ++c) {
+    const long long u0 = first_unit(units, ctas, c);
+    if (u0 >= end) break;
+    // a CTA's first block is in its first place, the one it ends in the second
+    int* p = parts + (2 * static_cast<size_t>(c) + (u0 >= begin ? 0 : 1)) * FEW_SLOT + o;
+    s += *p;
+    *p = 0;
   }
-}
-
-template <int DT, int NT>
-flux_status_t launch_few(const Q8Args& a, const FewPlan& p, void* workspace, cudaStream_t s) {
-  int* parts = reinterpret_cast<int*>(static_cast<char*>(workspace) + WS_HEADER);
-  const long long units = static_cast<long long>(p.blocks) * p.steps;
-  cudaError_t e = launch_behind(q8_few_kernel<DT, NT>, dim3(p.ctas), FEW_THREADS, 0, s, a, parts, p.steps, units);
-  if (e == cudaSuccess && p.ctas > 1)
-    e = launch_behind(q8_few_join_kernel<DT, NT>, dim3(p.ctas - 1), 128, 0, s, a, parts, p.steps, units, p.ctas);
-  return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
+  few_store<DT>(a, block * FEW_CH + o % FEW_CH, o / FEW_CH, s);
 }
 
 template <int DT>
 flux_status_t few_rows(const Q8Args& a, void* workspace, cudaStream_t s) {
-  const FewPlan p = few_plan(a.M, a.N, a.K);
-  if (a.M <= 8) return launch_few<DT, 1>(a, p, workspace, s);
-  if (a.M <= 16) return launch_few<DT, 2>(a, p, workspace, s);
-  return launch_few<DT, 4>(a, p, workspace, s);
+  const FewPlan p = few_plan(a.N, a.K);
+  int* parts = reinterpret_cast<int*>(static_cast<char*>(workspace) + WS_HEADER);
+  const long long units = static_cast<long long>(p.blocks) * p.steps;
+  cudaError_t e = launch_behind(q8_few_kernel<DT>, dim3(p.ctas), FEW_THREADS, 0, s, a, parts, p.steps, units);
+  if (e == cudaSuccess && p.ctas != p.blocks)
+    e = launch_behind(q8_few_join_kernel<DT>, dim3(p.ctas - 1), FEW_SLOT, 0, s, a, parts, p.steps, units, p.ctas);
+  return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 
 // K = 0: the bias, or zeros.
@@ -300,7 +298,7 @@ extern "C" flux_status_t flux_q8_quantize(int rows, int K, flux_dtype_t dtype, c
 extern "C" size_t flux_q8_workspace_size(int M, int N, int K) {
   if (!q8_sizes_ok(M, N, K) || !q8_sizes_supported(M, N, K)) return 0;
   if (M == 0 || N == 0 || K == 0) return WS_HEADER;
-  return WS_HEADER + (M <= Q8_FEW ? few_plan(M, N, K).total : q8_gemm_bytes(M, N, K));
+  return WS_HEADER + (M <= FEW_ROWS ? few_plan(N, K).total : q8_gemm_bytes(M, N, K));
 }
 
 extern "C" flux_status_t flux_q8_gemm(int M, int N, int K, flux_dtype_t dtype, const int8_t* x, const float* x_scales,
@@ -325,6 +323,6 @@ extern "C" flux_status_t flux_q8_gemm(int M, int N, int K, flux_dtype_t dtype, c
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
   }
-  if (M <= Q8_FEW) return dtype == FLUX_BF16 ? few_rows<1>(a, workspace, s) : few_rows<0>(a, workspace, s);
+  if (M <= FEW_ROWS) return dtype == FLUX_BF16 ? few_rows<1>(a, workspace, s) : few_rows<0>(a, workspace, s);
   return q8_gemm_launch(a, dtype, workspace, dev, s);
 }

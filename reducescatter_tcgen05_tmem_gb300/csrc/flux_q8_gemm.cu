@@ -54,6 +54,11 @@ struct Q8GemmParams {
   int n, ch_tiles, tok_tiles, steps, splits;
 };
 
+// (as in flux_rows.cuh, whose pack2 the GEMM headers define too)
+template <typename T>
+__device__ __forceinline__ T load_global(const T* p) {
+  return *p;
+}
 __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -89,11 +94,11 @@ __device__ __forceinline__ void widen(uint32_t v, uint32_t& lo, uint32_t& hi) {
   hi = *reinterpret_cast<const uint32_t*>(&hb);
 }
 
-__global__ void __launch_bounds__(256) q8_widen_kernel(const uint4* __restrict__ x, uint4* __restrict__ xf, size_t n) {
+__global__ void __launch_bounds__(256) q8_widen_kernel(const uint4* x, uint4* xf, size_t n) {
   after_previous();
   const size_t step = static_cast<size_t>(gridDim.x) * 256;
   for (size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) {
-    const uint4 v = __ldg(x + i);
+    const uint4 v = load_global(x + i);
     uint4 o[2];
     widen(v.x, o[0].x, o[0].y);
     widen(v.y, o[0].z, o[0].w);
@@ -139,7 +144,8 @@ q8_gemm_kernel(const __grid_constant__ Q8GemmParams p) {
   uint64_t *rawfull = bars, *rawempty = rawfull + G_RAW_STAGES, *full = rawempty + G_RAW_STAGES, *done = full + G_TOK_STAGES;
   uint64_t *tfull = done + G_TOK_STAGES, *tempty = tfull + 2, *drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (shuffled, so that the compiler knows them to be the same for a warp)
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t cta = cluster_ctarank();
   const Ctl c{p.hdr, p.seq, p.timeout_ns, 2 * p.timeout_ns + 10000000ull};
   if (threadIdx.x == 0) {
@@ -166,7 +172,7 @@ q8_gemm_kernel(const __grid_constant__ Q8GemmParams p) {
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const int pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
   const int units = p.ch_tiles * p.tok_tiles * p.splits;
   after_previous();
@@ -320,10 +326,10 @@ q8_gemm_kernel(const __grid_constant__ Q8GemmParams p) {
       tc_fence_after();
       const int ch = w.ct * G_CH + static_cast<int>(cta) * G_ROWS + quarter * 32 + lane;
       const bool in = ch < p.a.N;
-      const float ws = in ? __ldg(p.a.w_scales + ch) : 0.0f;
+      const float ws = in ? load_global(p.a.w_scales + ch) : 0.0f;
       float bias = 0.0f;
       if (in && p.a.bias != nullptr) {
-        const uint16_t h = __ldg(static_cast<const uint16_t*>(p.a.bias) + ch);
+        const uint16_t h = load_global(static_cast<const uint16_t*>(p.a.bias) + ch);
         bias = DT == 1 ? __uint_as_float(static_cast<uint32_t>(h) << 16) : __half2float(__ushort_as_half(h));
       }
       const int t0 = w.tt * p.n;
@@ -337,7 +343,7 @@ q8_gemm_kernel(const __grid_constant__ Q8GemmParams p) {
           for (int j = 0; j < 16; ++j)
             if (in && j < left) dst[static_cast<size_t>(j) * p.a.N] = __uint_as_float(r[j]);
         } else {
-          const float xs = (lane & 15) < left ? __ldg(p.a.x_scales + t0 + c0 + (lane & 15)) : 0.0f;
+          const float xs = (lane & 15) < left ? load_global(p.a.x_scales + t0 + c0 + (lane & 15)) : 0.0f;
           uint16_t* dst = static_cast<uint16_t*>(p.a.out) + static_cast<size_t>(t0 + c0) * p.a.N + ch;
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -362,7 +368,7 @@ q8_gemm_kernel(const __grid_constant__ Q8GemmParams p) {
 
 // Adds the parts of K, four channels a thread.
 template <int DT>
-__global__ void __launch_bounds__(256) q8_parts_kernel(const __grid_constant__ Q8Args a, const float* __restrict__ parts, int splits) {
+__global__ void __launch_bounds__(256) q8_parts_kernel(const __grid_constant__ Q8Args a, const float* parts, int splits) {
   after_previous();
   const size_t n4 = static_cast<size_t>(a.M) * a.N / 4, i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= n4) return;
@@ -373,11 +379,11 @@ __global__ void __launch_bounds__(256) q8_parts_kernel(const __grid_constant__ Q
     s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
   }
   const int row = static_cast<int>(4 * i / a.N), ch = static_cast<int>(4 * i - static_cast<size_t>(row) * a.N);
-  const float xs = __ldg(a.x_scales + row);
-  const float4 ws = __ldg(reinterpret_cast<const float4*>(a.w_scales + ch));
+  const float xs = load_global(a.x_scales + row);
+  const float4 ws = load_global(reinterpret_cast<const float4*>(a.w_scales + ch));
   float b[4] = {};
   if (a.bias != nullptr) {
-    const uint2 h = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.bias) + ch));
+    const uint2 h = load_global(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.bias) + ch));
     const uint16_t e[4] = {static_cast<uint16_t>(h.x), static_cast<uint16_t>(h.x >> 16), static_cast<uint16_t>(h.y), static_cast<uint16_t>(h.y >> 16)};
 #pragma unroll
     for (int j = 0; j < 4; ++j) b[j] = DT == 1 ? __uint_as_float(static_cast<uint32_t>(e[j]) << 16) : __half2float(__ushort_as_half(e[j]));
@@ -415,7 +421,7 @@ Q8Plan q8_plan(int M, int N, int K) {
         best.tok_tiles = tt;
         best.splits = splits;
       }
-      if (units > 2 * G_PAIRS) break;
+      if (units > 4 * G_PAIRS) break;
     }
   }
   // whole tiles: what lies past the last token is read, and never stored

@@ -9,6 +9,14 @@
 
 namespace flux {
 
+// A load of what a kernel before this one may have written.  __ldg would promise the
+// compiler that nothing writes there while the kernel runs, and let it move the load in
+// front of wait_for_previous, where that kernel still does.
+template <typename T>
+__device__ __forceinline__ T load_global(const T* p) {
+  return *p;
+}
+
 // DT as in the GEMM kernels: 0 fp16, 1 bf16.
 template <int DT>
 __device__ __forceinline__ float2 unpack2(uint32_t v) {
@@ -32,7 +40,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 template <int DT>
 __device__ __forceinline__ float load16(const void* p, size_t i) {
-  const uint16_t v = __ldg(static_cast<const uint16_t*>(p) + i);
+  const uint16_t v = load_global(static_cast<const uint16_t*>(p) + i);
   if constexpr (DT == 1) return __uint_as_float(static_cast<uint32_t>(v) << 16);
   return __half2float(__ushort_as_half(v));
 }
