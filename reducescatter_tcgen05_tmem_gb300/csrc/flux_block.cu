@@ -82,7 +82,7 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
   const int team = threadIdx.x / TT, lane = threadIdx.x % TT, wit = lane / 32;
   int turn = 0;
   wait_for_previous();
-  const float rho = a.res_scale != nullptr ? __ldg(a.res_scale) : 1.0f;
+  const float rho = a.res_scale != nullptr ? load_global(a.res_scale) : 1.0f;
   const float inv_h = 1.0f / static_cast<float>(a.H);
   const int step = gridDim.x * TEAMS;
   auto column = [&](int v) { return (v * TT + lane) * 8; };
@@ -125,7 +125,7 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
   const uint32_t one = pack2<DT>(1.0f, 1.0f);
   auto weights = [&](const void* base, size_t at, int v) {
     if (base == nullptr || column(v) >= a.H) return make_uint4(one, one, one, one);
-    return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at + column(v)));
+    return load_global(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at + column(v)));
   };
   const bool col_gate = HAS_Y && a.gate != nullptr && a.gate_cols != 1, row_gate = HAS_Y && a.gate != nullptr && a.gate_cols == 1;
   const bool one_gate = col_gate && a.gate_per == a.T;
@@ -267,7 +267,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
   const int team = threadIdx.x / TT, lane = threadIdx.x % TT, wit = lane / 32;
   int turn1 = 0, turn2 = 0;
   wait_for_previous();
-  const float rho = a.res_scale != nullptr ? __ldg(a.res_scale) : 1.0f;
+  const float rho = a.res_scale != nullptr ? load_global(a.res_scale) : 1.0f;
   const float inv_h = 1.0f / static_cast<float>(a.H);
   const bool row_gate = a.gate != nullptr && a.gate_cols == 1;
   const bool col_gate = a.gate != nullptr && a.gate_cols != 1;
@@ -299,8 +299,8 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
       }
       Row r;
       r.rank = rank_a;
-      r.ry = a.post_norm ? __ldg(a.rstd_y + t_a) : 1.0f;
-      r.rx = HAS_U ? __ldg(a.rstd_x + t_a) : 0.0f;
+      r.ry = a.post_norm ? load_global(a.rstd_y + t_a) : 1.0f;
+      r.rx = HAS_U ? load_global(a.rstd_x + t_a) : 0.0f;
       r.gt = row_gate ? load16<DT>(a.gate, a.gate_per == 1 ? t_a : t_a / a.gate_per) : 1.0f;
       queue[DEPTH - 1] = r;
       const size_t at = static_cast<size_t>(t_a - rank_a * a.rows_per_rank) * a.H + lane * 8;
@@ -333,7 +333,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[i] = 0;
     } else if (base != nullptr) {
-      unpack8<DT>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at)), f);
+      unpack8<DT>(load_global(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at)), f);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[i] = both(1.0f);
@@ -387,7 +387,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
       uint4 q = make_uint4(0, 0, 0, 0);
       if (column(v) < a.H)
         q = a.w_pre != nullptr
-                ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.w_pre) + column(v)))
+                ? load_global(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.w_pre) + column(v)))
                 : make_uint4(one16, one16, one16, one16);
       if constexpr (ROOMY) unpack8<DT>(q, wp_r[v]);
       else wp_s[v * CTA + threadIdx.x] = q;
@@ -435,7 +435,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a) {
   };
   auto times = [&](const void* w, size_t at, float4 s) {
     if (w != nullptr) {
-      const uint2 p = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + at));
+      const uint2 p = load_global(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + at));
       const float2 lo = unpack2<DT>(p.x), hi = unpack2<DT>(p.y);
       s.x *= lo.x;
       s.y *= lo.y;

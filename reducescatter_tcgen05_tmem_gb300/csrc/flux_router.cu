@@ -59,11 +59,11 @@ struct Lanes {
     for (int v = 0; v < V; ++v) {
       if constexpr (VEC) {
         const int e = expert(l, v, 0);
-        const float4 q = e < E ? __ldg(reinterpret_cast<const float4*>(row + e)) : make_float4(other, other, other, other);
+        const float4 q = e < E ? load_global(reinterpret_cast<const float4*>(row + e)) : make_float4(other, other, other, other);
         f[v][0] = q.x, f[v][1] = q.y, f[v][2] = q.z, f[v][3] = q.w;
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[v][i] = expert(l, v, i) < E ? __ldg(row + expert(l, v, i)) : other;
+        for (int i = 0; i < 4; ++i) f[v][i] = expert(l, v, i) < E ? load_global(row + expert(l, v, i)) : other;
       }
     }
   }
@@ -233,8 +233,8 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
     L::load(a.logits + at * E, l, E, -INFINITY, next);
 #pragma unroll
     for (int k = 0; k < L::IDS; ++k)
-      if (l + k * LPT < a.topk) next_id[k] = __ldg(a.ids + at * a.topk + l + k * LPT);
-    if (a.mask != nullptr) next_mask = __ldg(a.mask + at);
+      if (l + k * LPT < a.topk) next_id[k] = load_global(a.ids + at * a.topk + l + k * LPT);
+    if (a.mask != nullptr) next_mask = load_global(a.mask + at);
   };
   if (t0 + warp * L::TPW < t1) fetch(t0 + warp * L::TPW + tg);
   for (int tw = t0 + warp * L::TPW; tw < t1; tw += L::TPC) {
@@ -292,7 +292,7 @@ balance_kernel(const __grid_constant__ BalanceArgs a) {
 #pragma unroll
       for (int k = 0; k < L::IDS; ++k)
         if (l + k * LPT < a.topk) count(id[k]);
-      for (int j = l + L::IDS * LPT; j < a.topk; j += LPT) count(__ldg(a.ids + static_cast<size_t>(t) * a.topk + j));
+      for (int j = l + L::IDS * LPT; j < a.topk; j += LPT) count(load_global(a.ids + static_cast<size_t>(t) * a.topk + j));
     }
   }
   // tokens side by side in a warp, then the warps
@@ -539,8 +539,8 @@ router_bwd_kernel(const __grid_constant__ RouterBwdArgs a) {
   const bool gates = a.dweights != nullptr;
   if (gates)
     for (int e = l; e < WIDE; e += LPT) g[e] = 0.0f;
-  const float db = a.dloss != nullptr ? __ldg(a.dloss) : 1.0f, dz = a.dloss != nullptr ? __ldg(a.dloss + 1) : 1.0f;
-  const float n = static_cast<float>(max(__ldg(a.tokens + seq), 1)), all = static_cast<float>(max(__ldg(a.tokens + a.S), 1));
+  const float db = a.dloss != nullptr ? load_global(a.dloss) : 1.0f, dz = a.dloss != nullptr ? load_global(a.dloss + 1) : 1.0f;
+  const float n = static_cast<float>(max(load_global(a.tokens + seq), 1)), all = static_cast<float>(max(load_global(a.tokens + a.S), 1));
   const float scale = db * (a.balance_coef * E / (static_cast<float>(a.topk) * a.S)) / (n * n);
   const float z_scale = dz * (2.0f * a.z_coef) / all;
   float A[V][4];
@@ -549,22 +549,22 @@ router_bwd_kernel(const __grid_constant__ RouterBwdArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = L::expert(l, v, i);
-      A[v][i] = e < E ? scale * static_cast<float>(__ldg(a.counts + static_cast<size_t>(seq) * E + e)) : 0.0f;
+      A[v][i] = e < E ? scale * static_cast<float>(load_global(a.counts + static_cast<size_t>(seq) * E + e)) : 0.0f;
     }
   __syncwarp();
   for (int tw = t0 + warp * L::TPW; tw < t1; tw += L::TPC) {
     const int t = tw + tg;
     const bool here = t < t1;
     const size_t row = static_cast<size_t>(here ? t : t0);
-    const bool keep = here && (a.mask == nullptr || __ldg(a.mask + t) != 0);
-    const float lse = __ldg(a.lse + row);
+    const bool keep = here && (a.mask == nullptr || load_global(a.mask + t) != 0);
+    const float lse = load_global(a.lse + row);
     const bool flat = isinf(lse) || lse != lse;
     float w = 0.0f, dw = 0.0f;
     int id = -1;
     if (gates && l < a.topk) {
-      w = __ldg(a.weights + row * a.topk + l);
-      dw = __ldg(a.dweights + row * a.topk + l);
-      id = __ldg(a.ids + row * a.topk + l);
+      w = load_global(a.weights + row * a.topk + l);
+      dw = load_global(a.dweights + row * a.topk + l);
+      id = load_global(a.ids + row * a.topk + l);
     }
     float f[V][4];
     if (keep) {
@@ -587,14 +587,14 @@ router_bwd_kernel(const __grid_constant__ RouterBwdArgs a) {
     const float shift = (flat ? 0.0f : z_scale * lse) - mean;
     if (gates) {
       float dot = w * dw;
-      for (int j = l + LPT; j < a.topk; j += LPT) dot += __ldg(a.weights + row * a.topk + j) * __ldg(a.dweights + row * a.topk + j);
+      for (int j = l + LPT; j < a.topk; j += LPT) dot += load_global(a.weights + row * a.topk + j) * load_global(a.dweights + row * a.topk + j);
       dot = L::sum(dot);
       if (here && !flat) {
         for (int j = l; j < a.topk; j += LPT) {
           if (j != l) {
-            w = __ldg(a.weights + row * a.topk + j);
-            dw = __ldg(a.dweights + row * a.topk + j);
-            id = __ldg(a.ids + row * a.topk + j);
+            w = load_global(a.weights + row * a.topk + j);
+            dw = load_global(a.dweights + row * a.topk + j);
+            id = load_global(a.ids + row * a.topk + j);
           }
           if (id >= 0 && id < E) g[id] = w * (dw - dot);
         }

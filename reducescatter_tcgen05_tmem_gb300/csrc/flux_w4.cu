@@ -622,8 +622,8 @@ constexpr int W4_QUANT_COLS = 4;
 
 template <int DT>
 __global__ void __launch_bounds__(128)
-w4_quantize_kernel(int K, int N, int runs, int group, int groups, const uint16_t* __restrict__ w, uint8_t* __restrict__ q,
-                   uint16_t* __restrict__ scales) {
+w4_quantize_kernel(int K, int N, int runs, int group, int groups, const uint16_t* w, uint8_t* q,
+                   uint16_t* scales) {
   constexpr int C = W4_QUANT_COLS;
   const int n = (blockIdx.x * 128 + threadIdx.x) * C;
   const size_t e = blockIdx.z;
@@ -633,7 +633,7 @@ w4_quantize_kernel(int K, int N, int runs, int group, int groups, const uint16_t
     const uint16_t* from = w + (e * K + k) * N + n;
     uint2 raw[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) raw[i] = __ldg(reinterpret_cast<const uint2*>(from + static_cast<size_t>(i) * N));
+    for (int i = 0; i < 8; ++i) raw[i] = load_global(reinterpret_cast<const uint2*>(from + static_cast<size_t>(i) * N));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float2 lo = unpack2<DT>(raw[i].x), hi = unpack2<DT>(raw[i].y);
