@@ -51,31 +51,19 @@ struct LayerNormArgs {
 
 namespace {
 
-// The 128 bits of a counter, as four words.
-__device__ __forceinline__ void philox(uint32_t k0, uint32_t k1, unsigned long long block, unsigned long long offset,
-                                       uint32_t (&w)[4]) {
-  uint32_t a = static_cast<uint32_t>(block), b = static_cast<uint32_t>(block >> 32);
-  uint32_t c = static_cast<uint32_t>(offset), d = static_cast<uint32_t>(offset >> 32);
-#pragma unroll
-  for (int i = 0; i < 10; ++i) {
-    const unsigned long long m0 = static_cast<unsigned long long>(a) * 0xD2511F53u;
-    const unsigned long long m1 = static_cast<unsigned long long>(c) * 0xCD9E8D57u;
-    a = static_cast<uint32_t>(m1 >> 32) ^ b ^ k0;
-    b = static_cast<uint32_t>(m1);
-    c = static_cast<uint32_t>(m0 >> 32) ^ d ^ k1;
-    d = static_cast<uint32_t>(m0);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
-  }
-  w[0] = a, w[1] = b, w[2] = c, w[3] = d;
-}
+// Which elements of V vectors of eight neighbours stay: the four words of each
+// vector's counter, made together, so that the rounds' keys are made once.
+template <int V>
+struct Bits {
+  uint32_t w[V][4];
+};
 
-// Eight neighbours times scale, or zero where dropped (a NaN there too).
 struct Dropout {
-  uint32_t k0, k1, keep;
+  uint32_t k0, k1, keep, keep_high;
   unsigned long long offset;
   f32x2 scale;
-  __device__ __forceinline__ Dropout(const LayerNormArgs& a, bool wanted) : k0(0), k1(0), keep(a.keep), offset(0), scale(both(a.scale)) {
+  __device__ __forceinline__ Dropout(const LayerNormArgs& a, bool wanted)
+      : k0(0), k1(0), keep(a.keep), keep_high(a.keep << 16), offset(0), scale(both(a.scale)) {
     if (wanted && a.keep < 65536u) {
       const unsigned long long seed = load_global(a.rng);
       k0 = static_cast<uint32_t>(seed);
@@ -84,13 +72,42 @@ struct Dropout {
     }
   }
   __device__ __forceinline__ bool on() const { return keep < 65536u; }
-  __device__ __forceinline__ void operator()(unsigned long long block, f32x2 (&v)[4]) const {
-    uint32_t w[4];
-    philox(k0, k1, block, offset, w);
+  // vectors block, block + step, ...
+  template <int V>
+  __device__ __forceinline__ Bits<V> draw(unsigned long long block, int step) const {
+    Bits<V> b;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const unsigned long long n = block + static_cast<unsigned long long>(v) * step;
+      b.w[v][0] = static_cast<uint32_t>(n);
+      b.w[v][1] = static_cast<uint32_t>(n >> 32);
+      b.w[v][2] = static_cast<uint32_t>(offset);
+      b.w[v][3] = static_cast<uint32_t>(offset >> 32);
+    }
+    uint32_t k = k0, l = k1;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const unsigned long long m0 = static_cast<unsigned long long>(b.w[v][0]) * 0xD2511F53u;
+        const unsigned long long m1 = static_cast<unsigned long long>(b.w[v][2]) * 0xCD9E8D57u;
+        b.w[v][0] = static_cast<uint32_t>(m1 >> 32) ^ b.w[v][1] ^ k;
+        b.w[v][1] = static_cast<uint32_t>(m1);
+        b.w[v][2] = static_cast<uint32_t>(m0 >> 32) ^ b.w[v][3] ^ l;
+        b.w[v][3] = static_cast<uint32_t>(m0);
+      }
+      k += 0x9E3779B9u;
+      l += 0xBB67AE85u;
+    }
+    return b;
+  }
+  // eight neighbours times scale, or zero where dropped (a NaN there too)
+  __device__ __forceinline__ void apply(const uint32_t (&w)[4], f32x2 (&x)[4]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 h = halves(mul2(v[i], scale));
-      v[i] = pair((w[i] & 0xFFFFu) < keep ? h.x : 0.0f, (w[i] >> 16) < keep ? h.y : 0.0f);
+      const float2 h = halves(mul2(x[i], scale));
+      // the high half is below keep where the word is below keep 2^16
+      x[i] = pair((w[i] & 0xFFFFu) < keep ? h.x : 0.0f, w[i] < keep_high ? h.y : 0.0f);
     }
   }
 };
@@ -178,13 +195,17 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a) {
     const size_t row = static_cast<size_t>(t - rank * a.rows_per_rank) * a.H + lane * 8;
     copy_wait<DEPTH - 1>();
     f32x2 x1[V][4], s = 0;
+    Bits<HAS_Y ? V : 1> bits = {};
+    if constexpr (HAS_Y) {
+      if (drop.on()) bits = drop.draw<V>(static_cast<unsigned long long>(t) * (a.H / 8) + lane, TT);
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       unpack8<DT>(slot(stage, 0, v), x1[v]);
       if constexpr (HAS_Y) {
         f32x2 y[4];
         unpack8<DT>(slot(stage, 1, v), y);
-        if (drop.on()) drop(static_cast<unsigned long long>(t) * (a.H / 8) + (v * TT + lane), y);
+        if (drop.on()) drop.apply(bits.w[v], y);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x1[v][i] = add2(x1[v][i], y[i]);
         if (column(v) < a.H)
@@ -358,6 +379,8 @@ layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a) {
       k2 = both(-s2[1] * inv_h);
     }
     const size_t at = static_cast<size_t>(t - row.rank * a.rows_per_rank) * a.H + lane * 8;
+    Bits<V> bits = {};
+    if (a.has_dy && drop.on()) bits = drop.draw<V>(static_cast<unsigned long long>(t) * (a.H / 8) + lane, TT);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       f32x2 d[4];
@@ -376,7 +399,7 @@ layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a) {
       if (column(v) < a.H) {
         if (a.has_dx) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_a[row.rank]) + at + v * TT * 8) = pack8<DT>(d);
         if (a.has_dy) {
-          if (drop.on()) drop(static_cast<unsigned long long>(t) * (a.H / 8) + (v * TT + lane), d);
+          if (drop.on()) drop.apply(bits.w[v], d);
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_b[row.rank]) + at + v * TT * 8) = pack8<DT>(d);
         }
       }
