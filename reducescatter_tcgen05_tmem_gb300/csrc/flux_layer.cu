@@ -258,7 +258,10 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a) {
 
 // Backward.  A CTA takes a stretch of consecutive rows, its teams one row each in
 // turn, with the same slots of shared memory; both sums over a row are taken at
-// once.  The sums of a thread's own columns over the rows (dw, db) stay in its
+// once.  (Rows of more than 6144 columns leave room for one CTA an SM, whose warps all
+// wait for one another; more warps with fewer vectors make that worse: 16384 x 8192 with
+// 32 warps of one vector 308 us, with 16 of two 249, 4061 x 12288 with 24 of two 80, with
+// 16 of three 76.)  The sums of a thread's own columns over the rows (dw, db) stay in its
 // registers; the teams' are joined in shared memory and the CTAs' by
 // layer_norm_sums_kernel, both in a fixed order, so repeat calls give the same
 // bits.
@@ -445,14 +448,15 @@ layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a) {
 }
 
 // Joins the CTAs' sums of dw (the first blocks) and db, and leaves them zero.
-__global__ void __launch_bounds__(SUM_THREADS)
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS * 32)
 layer_norm_sums_kernel(const __grid_constant__ LayerNormArgs a, int w_blocks) {
-  __shared__ float part[SUM_WARPS][SUM_COLS];
+  __shared__ float part[WARPS][SUM_COLS];
   wait_for_previous();
   const int lane = threadIdx.x % SUM_COLS, warp = threadIdx.x / SUM_COLS;
   const bool is_w = static_cast<int>(blockIdx.x) < w_blocks;
   const int col = (is_w ? blockIdx.x : blockIdx.x - w_blocks) * SUM_COLS + lane;
-  const float s = column_sum(is_w ? a.part_w : a.part_b, a.ctas, a.H, col, warp, lane, part);
+  const float s = column_sum<WARPS>(is_w ? a.part_w : a.part_b, a.ctas, a.H, col, warp, lane, part);
   if (warp == 0 && col < a.H) (is_w ? a.dweight : a.dbias)[col] = s;
 }
 
@@ -520,7 +524,10 @@ flux_status_t launch_bwd(const LayerNormArgs& a, const DeviceInfo& dev, cudaStre
   });
   const int w_blocks = a.dweight != nullptr ? sum_blocks(a.H) : 0, b_blocks = a.dbias != nullptr ? sum_blocks(a.H) : 0;
   if (st != FLUX_OK || w_blocks + b_blocks == 0) return st;
-  const cudaError_t e = launch_behind(layer_norm_sums_kernel, dim3(w_blocks + b_blocks), SUM_THREADS, 0, s, a, w_blocks);
+  // up to 912 CTAs to join: more warps for many of them (32768 x 2048: 30 us with eight
+  // warps, 9 with 32), fewer for few, where most of 32 would have nothing to add
+  const cudaError_t e = a.ctas > 2 * BN_SMS ? launch_behind(layer_norm_sums_kernel<32>, dim3(w_blocks + b_blocks), 1024, 0, s, a, w_blocks)
+                                            : launch_behind(layer_norm_sums_kernel<8>, dim3(w_blocks + b_blocks), 256, 0, s, a, w_blocks);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
 

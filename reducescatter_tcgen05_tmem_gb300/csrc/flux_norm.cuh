@@ -73,7 +73,7 @@ inline bool shards_ok(int R, P const* shards, flux_status_t* st) {
 }
 
 // Sums over the CTAs' partial sums [ctas x H] of one column, by blocks of
-// SUM_COLS columns x SUM_WARPS warps, in a fixed order; leaves the partial sums
+// SUM_COLS columns x WARPS warps, in a fixed order; leaves the partial sums
 // zero.  The sum is in the lanes of warp 0; every thread of the block calls this.
 // SUM_BATCH loads of a thread are on their way together: a few MB from L2 are
 // bound by latency (one load after the other, each behind the store of the last,
@@ -81,20 +81,21 @@ inline bool shards_ok(int R, P const* shards, flux_status_t* st) {
 constexpr int SUM_COLS = 32, SUM_WARPS = 8, SUM_BATCH = 20, SUM_THREADS = SUM_COLS * SUM_WARPS;
 inline int sum_blocks(int H) { return (H + SUM_COLS - 1) / SUM_COLS; }
 
+template <int WARPS>
 __device__ __forceinline__ float column_sum(float* src, int ctas, int H, int col, int warp, int lane,
-                                            float (&part)[SUM_WARPS][SUM_COLS]) {
+                                            float (&part)[WARPS][SUM_COLS]) {
   float s = 0.0f;
   if (col < H) {
-    for (int i0 = warp; i0 < ctas; i0 += SUM_WARPS * SUM_BATCH) {
+    for (int i0 = warp; i0 < ctas; i0 += WARPS * SUM_BATCH) {
       float v[SUM_BATCH];
 #pragma unroll
       for (int j = 0; j < SUM_BATCH; ++j) {
-        const int i = i0 + j * SUM_WARPS;
+        const int i = i0 + j * WARPS;
         v[j] = i < ctas ? src[static_cast<size_t>(i) * H + col] : 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < SUM_BATCH; ++j) {
-        const int i = i0 + j * SUM_WARPS;
+        const int i = i0 + j * WARPS;
         if (i < ctas) src[static_cast<size_t>(i) * H + col] = 0.0f;
         s += v[j];
       }
@@ -104,7 +105,7 @@ __device__ __forceinline__ float column_sum(float* src, int ctas, int H, int col
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < SUM_WARPS; ++w) s += part[w][lane];
+    for (int w = 1; w < WARPS; ++w) s += part[w][lane];
   }
   return s;
 }
