@@ -13,6 +13,7 @@ from __future__ import annotations
 import array
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # FLUX_CHECKED=1 in the environment loads the checked build (bounds checks in
@@ -99,6 +100,7 @@ _i = ctypes.c_int
 _sz = ctypes.c_size_t
 _vpp = ctypes.POINTER(ctypes.c_void_p)
 _f = ctypes.c_float
+_rows = ctypes.c_char_p  # an array of pointers as the bytes of _row_ptrs
 _opt = ctypes.POINTER(flux_opts_t)
 
 _SIGS = {
@@ -153,9 +155,9 @@ _SIGS = {
     "flux_w4_gemv": ([_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
     "flux_moe_w4_layer0": ([_i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
     "flux_moe_w4_layer1": ([_i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i),
-    "flux_layer_norm": ([_i, _i, _i, _i, _f, _f, _vpp, _vpp, _vp, _vp, _vp, _vpp, _vpp, _vp, _vp, _vp], _i),
+    "flux_layer_norm": ([_i, _i, _i, _i, _f, _f, _rows, _rows, _vp, _vp, _vp, _rows, _rows, _vp, _vp, _vp], _i),
     "flux_layer_norm_workspace_size": ([_i, _i], _sz),
-    "flux_layer_norm_bwd": ([_i, _i, _i, _i, _f, _vpp, _vp, _vp, _vp, _vp, _vpp, _vpp, _vpp, _vpp, _vp, _vp, _vp,
+    "flux_layer_norm_bwd": ([_i, _i, _i, _i, _f, _rows, _vp, _vp, _vp, _vp, _rows, _rows, _rows, _rows, _vp, _vp, _vp,
                              _sz, _vp], _i),
     "flux_moe_group_gate": ([_i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp], _i),
     "flux_moe_group_gate_bwd": ([_i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _i, _vp, _vp], _i),
@@ -195,6 +197,22 @@ def _ptrs(xs):
 
 def _optional_ptrs(xs):
     return None if xs is None else _ptrs(xs)
+
+
+_PACK = {}  # struct packers by length
+
+
+def _row_ptrs(R, xs):
+    """The pointers of R row shards (or None) as bytes: half the time of a ctypes array."""
+    if xs is None:
+        return None
+    n = len(xs)
+    if n < R <= FLUX_MAX_RANKS:
+        raise ValueError(f"{n} row shards for {R} ranks")
+    pack = _PACK.get(n) or _PACK.setdefault(n, struct.Struct(f"{n}P").pack)
+    if n == 1:
+        return pack(_ptr(xs[0]) or 0)
+    return pack(*[_ptr(x) or 0 for x in xs])
 
 
 def _nbytes(t):
@@ -484,8 +502,8 @@ def flux_layer_norm_workspace_size(T: int, H: int) -> int:
 def flux_layer_norm(R, T, H, dtype, p, eps, x_shards, y_shards, rng, weight, bias, x_out, u_out, mean=None, rstd=None,
                     stream=None) -> None:
     """Dropout, residual and the next block's layer norm in one pass."""
-    _check(_lib.flux_layer_norm(R, T, H, dtype, p, eps, _optional_ptrs(x_shards), _optional_ptrs(y_shards), _ptr(rng),
-                                _ptr(weight), _ptr(bias), _optional_ptrs(x_out), _optional_ptrs(u_out), _ptr(mean),
+    _check(_lib.flux_layer_norm(R, T, H, dtype, p, eps, _row_ptrs(R, x_shards), _row_ptrs(R, y_shards), _ptr(rng),
+                                _ptr(weight), _ptr(bias), _row_ptrs(R, x_out), _row_ptrs(R, u_out), _ptr(mean),
                                 _ptr(rstd), _stream(stream)), "flux_layer_norm")
 
 
@@ -493,8 +511,8 @@ def flux_layer_norm_bwd(R, T, H, dtype, p, x_out, rng, weight, mean, rstd, dx_ou
                         workspace, stream=None) -> None:
     """Gradients of flux_layer_norm."""
     _check(_lib.flux_layer_norm_bwd(
-        R, T, H, dtype, p, _optional_ptrs(x_out), _ptr(rng), _ptr(weight), _ptr(mean), _ptr(rstd), _optional_ptrs(dx_out),
-        _optional_ptrs(du), _optional_ptrs(dx), _optional_ptrs(dy), _ptr(dweight), _ptr(dbias), _ptr(workspace),
+        R, T, H, dtype, p, _row_ptrs(R, x_out), _ptr(rng), _ptr(weight), _ptr(mean), _ptr(rstd), _row_ptrs(R, dx_out),
+        _row_ptrs(R, du), _row_ptrs(R, dx), _row_ptrs(R, dy), _ptr(dweight), _ptr(dbias), _ptr(workspace),
         _nbytes(workspace), _stream(stream)), "flux_layer_norm_bwd")
 
 

@@ -138,7 +138,7 @@ def test_q8_quantize_refusals(fx, kw, err):
     (dict(x=None), "INVALID_ARG"), (dict(w=None), "INVALID_ARG"), (dict(out=None), "INVALID_ARG"),
     (dict(x_scales=None), "INVALID_ARG"), (dict(w_scales=None), "INVALID_ARG"), (dict(x=FAKE + 8), "UNSUPPORTED"),
     (dict(w=FAKE + 8), "UNSUPPORTED"), (dict(out=FAKE + 8), "UNSUPPORTED"), (dict(bias=FAKE + 2), "UNSUPPORTED"),
-    (dict(x_scales=FAKE + 4), "UNSUPPORTED"), (dict(w_scales=FAKE + 4), "UNSUPPORTED"), (dict(workspace=WS(256)), "WORKSPACE"),
+    (dict(x_scales=FAKE + 4), "UNSUPPORTED"), (dict(w_scales=FAKE + 4), "UNSUPPORTED"), (dict(workspace=WS(255)), "WORKSPACE"),
     (dict(workspace=WS(1 << 30, FAKE + 16)), "WORKSPACE"),
 ], ids=str)
 def test_q8_gemm_refusals(fx, kw, err, M):
@@ -150,7 +150,8 @@ def test_q8_workspace(fx):
     size = fx.flux_q8_workspace_size
     assert size(-1, 64, 64) == size(4, 12, 64) == size(4, 64, 24) == size(4, 64, 131072) == 0
     assert size(0, 64, 64) == size(4, 0, 64) == size(4, 64, 0) == 256
-    assert size(4, 64, 64) > 256
+    assert size(4, 64, 64) == 256  # whole blocks of channels: no partial sums
+    assert size(4, 8192, 28672) > 256
     assert size(400, 64, 64) > 256
 
 
@@ -160,3 +161,13 @@ def test_empty_calls_return_without_a_gpu(fx):
     fx.flux_moe_group_gate_bwd(0, 8, 2, 0, 0, 1.0, None, None, None, 0, None, stream=0)
     fx.flux_q8_quantize(0, 64, 0, None, None, None, stream=0)
     fx.flux_q8_gemm(0, 64, 64, 0, None, None, None, None, None, None, WS(256), stream=0)
+
+
+def test_row_shards_in_python(fx):
+    for bad in (1.5, "1048576", b"1048576", [FAKE], object()):
+        for shards in ([bad], [FAKE, bad]):
+            with pytest.raises((AttributeError, TypeError)):
+                fx.flux_layer_norm(len(shards), 0, 64, 0, 0.0, 1e-5, shards, None, None, None, None, None, P, stream=0)
+    with pytest.raises(ValueError):  # fewer than ranks: the library would read past them
+        fx.flux_layer_norm(4, 8, 64, 0, 0.0, 1e-5, [FAKE] * 3, None, None, None, None, None, P, stream=0)
+    assert fx.binding._row_ptrs(2, [FAKE, None]) == (FAKE).to_bytes(8, "little") + bytes(8)
