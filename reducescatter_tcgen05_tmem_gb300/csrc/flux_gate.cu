@@ -47,6 +47,8 @@ struct GroupGateArgs {
   int T, E, topk, G, kept, top;
   int n, pad;          // experts of a group; words between groups in shared memory
   int lpg, log_lpg;    // lanes that rank one group
+  int per;             // octet form: scores of a lane
+  uint32_t div_per;    // ceil(2^20 / per)
   int vecs, trips, rivals;  // wide form: vectors of a lane; of a lane in its group; groups that a lane compares
   uint32_t div_n;      // ceil(2^20 / n): e / n = e div_n >> 20 for e < 1024
   int row;             // values of a token's row in shared memory
@@ -165,6 +167,10 @@ __device__ __forceinline__ unsigned long long largest_of(uint32_t mask, unsigned
   return static_cast<unsigned long long>(hi) << 32 | lo;
 }
 
+__device__ __noinline__ double biased_sigmoid64(float x, float bias) {
+  return 1.0 / (1.0 + exp(-static_cast<double>(x != x ? -INFINITY : x))) + static_cast<double>(bias);
+}
+
 // The choice in doubles, by the LPT lanes of one token (mask).  Writes the kept groups
 // and, as pick, the places of the chosen ones among the kept groups'
 // experts.  One token in a thousand comes here, and the last one holds up the launch:
@@ -192,7 +198,7 @@ __device__ __noinline__ void choose64(const GroupGateArgs& a, const float* row, 
     return (isinf(top) ? (x == top ? 1.0 : 0.0) : exp(x - top)) / total;
   };
   unsigned long long c[MINE];  // experts l, l + LPT, ...
-#pragma unroll 1
+#pragma unroll 4
   for (int e = l, i = 0; e < a.E; e += LPT, ++i) {
     const double x = logit(e), v = a.bias != nullptr ? score(x) + static_cast<double>(load_global(a.bias + e)) : x;
     c[i] = v != v ? LEAST : order_of(v);
@@ -791,6 +797,317 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
   copy_wait<0>();
 }
 
+// Words of a lane in shared memory, octet form: its logits, then its sorted lists of
+// four (values, a NaN, their order; 8-byte stores).  No two of the eight lanes that read
+// 16 bytes at a time meet in a bank.
+template <int P>
+__host__ __device__ constexpr int octet_pitch() {
+  return P == 32 ? 52 : P == 16 ? 28 : 12;
+}
+__host__ __device__ inline int octet_words(int pitch) { return 32 * pitch + 4 * 8 + 8 + 32; }
+
+// Four tokens to a warp: a token's scores lie in neighbouring order in eight lanes, P
+// at most in each, so that a group is one lane (or 2, 4 or 8) and most of the work is
+// in the lanes' own registers.  Lists and rounds as in group_gate_wide_kernel.
+template <int P, bool SOFT, bool BIASED>
+__global__ void __launch_bounds__(GG_THREADS, P == 32 ? 3 : 4)
+group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
+  constexpr int LISTS = P / 4, S = octet_pitch<P>();
+  extern __shared__ uint4 smem[];
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), l = lane & 7, sub = lane >> 3;
+  float* bias = reinterpret_cast<float*>(smem);  // [8][P + 4], as the lanes hold the scores
+  float* mem = bias + (BIASED ? 8 * (P + 4) : 0) + warp * octet_words(S);
+  float* own = mem + lane * S;
+  int32_t* pick = reinterpret_cast<int32_t*>(mem + 32 * S) + sub * 8;
+  int32_t* pick64 = reinterpret_cast<int32_t*>(mem + 32 * S) + 4 * 8;
+  int32_t* kept64 = pick64 + 8;
+  using O = Over<8>;
+  const bool grouped = a.kept < a.G, two = a.top == 2 && a.n > 1;
+  const bool soft_row = SOFT && (BIASED || !a.renorm || (grouped && two));
+  const int mine = min(a.per, max(a.E - l * a.per, 0));  // scores of this lane
+  const bool full = a.per == P && a.E == 8 * P;
+  const int group = l >> a.log_lpg, lpg = 1 << a.log_lpg;
+  wait_for_previous();
+  if constexpr (BIASED) {
+    for (int i = threadIdx.x; i < 8 * (P + 4); i += GG_THREADS) {
+      const int b = i / (P + 4), k = i - b * (P + 4), e = b * a.per + k;
+      bias[i] = k < a.per && e < a.E ? load_global(a.bias + e) : -INFINITY;
+    }
+    __syncthreads();
+  }
+  const long long step = static_cast<long long>(gridDim.x) * GG_WARPS * 4;
+  for (long long first = static_cast<long long>(blockIdx.x) * GG_WARPS * 4; first < a.T; first += step) {
+    const bool token = first + warp * 4 + sub < a.T;
+    const long long t = token ? first + warp * 4 + sub : a.T - 1;
+    const float* row = a.logits + static_cast<size_t>(t) * a.E;
+    __syncwarp();
+    // the row, vectors or scores in turn to the lanes of the token
+    float* slots = mem + sub * 8 * S;
+    if (a.vecs) {
+#pragma unroll
+      for (int k = 0; k < LISTS; ++k) {
+        const int e = (k * 8 + l) * 4;
+        if (e < a.E) {
+          const int to = full ? e / P : static_cast<int>((e * a.div_per) >> 20);
+          copy16_async(slots + to * S + e - to * a.per, row + e);
+        }
+      }
+    } else {
+      for (int e = l; e < a.E; e += 8) {
+        const int to = static_cast<int>((e * a.div_per) >> 20);
+        slots[to * S + e - to * a.per] = load_global(row + e);
+      }
+    }
+    copy_commit();
+    copy_wait<0>();
+    __syncwarp();
+    float c[P];
+#pragma unroll
+    for (int k = 0; k < LISTS; ++k) {
+      const float4 q = *reinterpret_cast<const float4*>(own + 4 * k);
+      c[4 * k] = fmaxf(q.x, -INFINITY), c[4 * k + 1] = fmaxf(q.y, -INFINITY);
+      c[4 * k + 2] = fmaxf(q.z, -INFINITY), c[4 * k + 3] = fmaxf(q.w, -INFINITY);
+    }
+    if (!full) {
+#pragma unroll
+      for (int k = 0; k < P; ++k) c[k] = k < mine ? c[k] : -INFINITY;
+    }
+    float top = -INFINITY, inv = 1.0f, total = 1.0f;
+    auto soft = [&](float x) { return isinf(top) ? (x == top ? 1.0f : 0.0f) : ex2((x - top) * G_LOG2E); };
+    auto score = [&](float x) {
+      if constexpr (SOFT) return soft(x) * inv;
+      else return rcp(1.0f + ex2(-x * G_LOG2E));
+    };
+    if (soft_row) {
+#pragma unroll
+      for (int k = 0; k < P; ++k) top = fmaxf(top, c[k]);
+      top = O::maxf(top);
+      total = 0.0f;
+#pragma unroll
+      for (int k = 0; k < P; ++k) total += soft(c[k]);
+      total = O::sum(total);
+      if (top == -INFINITY) total = static_cast<float>(a.E);  // (not the lanes' empty places)
+      inv = rcp(total);
+    }
+    if constexpr (BIASED) {
+#pragma unroll
+      for (int k = 0; k < LISTS; ++k) {
+        const float4 b = *reinterpret_cast<const float4*>(bias + l * (P + 4) + 4 * k);
+        c[4 * k] = score(c[4 * k]) + b.x, c[4 * k + 1] = score(c[4 * k + 1]) + b.y;
+        c[4 * k + 2] = score(c[4 * k + 2]) + b.z, c[4 * k + 3] = score(c[4 * k + 3]) + b.w;
+      }
+    }
+    // (how far apart: as in group_gate_kernel)
+    const float unsure = SOFT ? 0x1p-16f * inv : 0x1p-20f;
+    bool doubt = false, in = true;
+    if (grouped) {
+      float m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        m2 = fmaxf(m2, fminf(m1, c[k]));
+        m1 = fmaxf(m1, c[k]);
+      }
+      for (int o = lpg >> 1; o > 0; o >>= 1) {
+        const float o1 = __shfl_xor_sync(0xFFFFFFFFu, m1, o), o2 = __shfl_xor_sync(0xFFFFFFFFu, m2, o);
+        m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+        m1 = fmaxf(m1, o1);
+      }
+      if (!two) m2 = 0.0f;
+      else if (!BIASED) m1 = score(m1), m2 = score(m2);
+      // lanes of groups before this one in the order
+      const float rank = fmaxf(m1 + m2, -INFINITY);
+      int before = 0;
+#pragma unroll
+      for (int d = 1; d < 8; ++d) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, rank, d);
+        const int g = (l ^ d) >> a.log_lpg;
+        before += g != group && (other > rank || (other == rank && g < group));
+      }
+      in = before < a.kept * lpg;
+      if (BIASED || two) {
+        const float big = (isinf(m1) ? 0.0f : fabsf(m1)) + (isinf(m2) ? 0.0f : fabsf(m2));
+        const float last = -O::maxf(in ? -rank : -INFINITY), next = O::maxf(in ? -INFINITY : rank);
+        doubt = !(last - next > 2.0f * unsure + 0x1p-21f * O::maxf(big));
+      }
+    }
+    // lists of four, largest first, equal ones in order
+    float h[LISTS];
+    int at[LISTS];
+#pragma unroll
+    for (int q = 0; q < LISTS; ++q) {
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = full || q * 4 + k < mine ? c[q * 4 + k] : NAN;
+      uint32_t id[4] = {0, 1, 2, 3};
+      auto sort2 = [&](int k) {  // neighbours, if out of order
+        const bool swap = v[k] < v[k + 1];
+        const float hi = swap ? v[k + 1] : v[k], lo = swap ? v[k] : v[k + 1];
+        const uint32_t one = swap ? id[k + 1] : id[k], other = swap ? id[k] : id[k + 1];
+        v[k] = hi, v[k + 1] = lo, id[k] = one, id[k + 1] = other;
+      };
+      sort2(0), sort2(1), sort2(2), sort2(0), sort2(1), sort2(0);
+      float2* list = reinterpret_cast<float2*>(own + q * 6);
+      list[0] = make_float2(v[0], v[1]);
+      list[1] = make_float2(v[2], v[3]);
+      list[2] = make_float2(NAN, __uint_as_float(id[0] | id[1] << 8 | id[2] << 16 | id[3] << 24));
+      h[q] = in ? v[0] : NAN;
+      at[q] = lane * S + q * 6;
+    }
+    auto head = [&] {
+      float m = h[0];
+#pragma unroll
+      for (int q = 1; q < LISTS; ++q) m = fmaxf(m, h[q]);
+      return O::maxf(m);
+    };
+    // the expert at a place of the lists
+    auto expert = [&](int where) {
+      const int rest = where - sub * 8 * S, of = rest / S, in_lane = rest - of * S, q = in_lane / 6;
+      const uint32_t order = __float_as_uint(mem[(sub * 8 + of) * S + q * 6 + 5]);
+      return of * a.per + q * 4 + static_cast<int>(order >> (in_lane - q * 6) * 8 & 3u);
+    };
+    float value = NAN;  // of the choice that this lane stands for
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= a.topk) break;
+      const float best = head();
+      value = l == j ? best : value;
+#pragma unroll
+      for (int q = 0; q < LISTS; ++q) {
+        if (h[q] == best) {
+          pick[j] = at[q];
+          h[q] = mem[++at[q]];
+        }
+      }
+    }
+    int taken = 0;
+#pragma unroll
+    for (int q = 0; q < LISTS; ++q) taken += at[q] - (lane * S + q * 6);
+    taken += __shfl_xor_sync(0xFFFFFFFFu, taken, 1);
+    taken += __shfl_xor_sync(0xFFFFFFFFu, taken, 2);
+    taken += __shfl_xor_sync(0xFFFFFFFFu, taken, 4);
+    if (__any_sync(0xFFFFFFFFu, taken != a.topk)) {
+      // several lists had the largest: the rounds again, the first expert takes it
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < LISTS; ++q) {
+        at[q] = lane * S + q * 6;
+        h[q] = in ? own[q * 6] : NAN;
+      }
+      for (int j = 0; j < a.topk; ++j) {
+        const float best = head();
+        value = l == j ? best : value;
+        uint32_t of = 0xFFFFFFFFu;
+#pragma unroll
+        for (int q = LISTS - 1; q >= 0; --q)
+          if (h[q] == best) of = expert(at[q]);
+        const uint32_t e = O::min(of);
+        bool here = of == e && of != 0xFFFFFFFFu;
+#pragma unroll
+        for (int q = 0; q < LISTS; ++q) {
+          if (here && h[q] == best) {
+            pick[j] = at[q];
+            h[q] = mem[++at[q]];
+            here = false;
+          }
+        }
+      }
+    }
+    __syncwarp();
+    const bool here = l < a.topk;
+    int e = here ? expert(pick[l]) : 0;
+    if constexpr (BIASED) {
+      float next = h[0];
+#pragma unroll
+      for (int q = 1; q < LISTS; ++q) next = fmaxf(next, h[q]);
+      next = O::maxf(next);  // the best one left, NaN if none is
+      auto apart = [&](float hi, float lo) { return hi - lo > unsure + 0x1p-23f * (fabsf(hi) + fabsf(lo)); };
+      auto same = [&](int f, int g) {
+        return load_global(row + f) == load_global(row + g) && load_global(a.bias + f) == load_global(a.bias + g);
+      };
+      const float after = __shfl_down_sync(0xFFFFFFFFu, value, 1, 8), lo = l + 1 < a.topk ? after : next;
+      const bool close = here && lo == lo && !apart(value, lo);
+      const int follower = __shfl_down_sync(0xFFFFFFFFu, e, 1, 8);
+      const float end = __shfl_sync(0xFFFFFFFFu, value, a.topk - 1, 8);
+      const int last = __shfl_sync(0xFFFFFFFFu, e, a.topk - 1, 8);
+      if (__any_sync(0xFFFFFFFFu, close)) {
+        // equal inputs have equal values: their order is that of the indexes
+        bool unsorted = close && l + 1 < a.topk && !same(e, follower);
+        // and what was left out next to the last one in
+        uint32_t out = 0xFFFFFFFFu, others = 0, equal = 0;
+#pragma unroll
+        for (int q = 0; q < LISTS; ++q) {
+          for (int i = in ? at[q] : lane * S + q * 6 + 4; i < lane * S + q * 6 + 4; ++i) {
+            if (mem[i] != mem[i] || apart(end, mem[i])) continue;
+            const int f = expert(i);
+            if (same(last, f)) {
+              ++equal;
+            } else {
+              ++others;
+              out = f;
+            }
+          }
+        }
+        others = static_cast<uint32_t>(O::sum(static_cast<float>(others)));
+        out = O::min(out);
+        equal = O::any(equal);
+        unsorted = O::any(unsorted || others > 0u) != 0u;
+        if (SOFT || others > 1u || equal != 0u) doubt |= unsorted;
+        // Mostly it is two neighbours, or the last one in and the first one out: their order
+        // is told by the doubles of these nine alone (the choice in full takes 12 us).
+        const bool nine = unsorted && !SOFT && others <= 1u && equal == 0u;
+        if (__any_sync(0xFFFFFFFFu, nine)) {
+          const double d = here ? biased_sigmoid64(load_global(row + e), load_global(a.bias + e)) : -INFINITY;
+          const int f = others == 1u ? static_cast<int>(out) : 0;
+          const double of = biased_sigmoid64(load_global(row + f), load_global(a.bias + f));
+          auto first = [](double u, int i, double v, int k) { return u > v || (u == v && i < k); };
+          int place = others == 1u && first(of, f, d, e);
+          int place_out = here && first(d, e, of, f);
+#pragma unroll
+          for (int m = 1; m < 8; ++m) {
+            const double v = __shfl_xor_sync(0xFFFFFFFFu, d, m);
+            const int k = __shfl_xor_sync(0xFFFFFFFFu, e, m);
+            place += (l ^ m) < a.topk && first(v, k, d, e);
+          }
+          place_out += __shfl_xor_sync(0xFFFFFFFFu, place_out, 1);
+          place_out += __shfl_xor_sync(0xFFFFFFFFu, place_out, 2);
+          place_out += __shfl_xor_sync(0xFFFFFFFFu, place_out, 4);
+          __syncwarp();
+          if (nine && here && place < a.topk) pick[place] = e;
+          if (nine && l == 0 && others == 1u && place_out < a.topk) pick[place_out] = f;
+          __syncwarp();
+          if (nine && here) e = pick[l];
+        }
+      }
+    }
+    uint32_t doubts = __ballot_sync(0xFFFFFFFFu, doubt);
+    while (doubts != 0u) {  // token by token, by the whole warp
+      const int of = (__ffs(doubts) - 1) >> 3;
+      doubts &= ~(0xFFu << of * 8);
+      const long long u = __shfl_sync(0xFFFFFFFFu, t, of * 8);
+      __syncwarp();
+      choose64<32>(a, a.logits + static_cast<size_t>(u) * a.E, kept64, pick64, lane, 0xFFFFFFFFu);
+      if (sub == of && here) e = expert_at(a, kept64, pick64[l]);
+      __syncwarp();
+    }
+    // the weights, with the rules of group_gate_kernel
+    const float x = here ? fmaxf(load_global(row + e), -INFINITY) : -INFINITY;
+    const float peak = a.renorm ? O::maxf(x) : 0.0f;
+    float w;
+    if constexpr (SOFT) {
+      const float from = a.renorm ? peak : top;
+      w = isinf(from) ? (x == from ? 1.0f : 0.0f) : expf(x - from);
+    } else {
+      w = !a.renorm || peak > -64.0f ? rcp(1.0f + expf(-x)) : peak == -INFINITY ? 1.0f : expf(x - peak);
+    }
+    w = here ? w : 0.0f;
+    const float sum = a.renorm ? O::sum(w) : total;
+    if (here && token) {
+      a.ids[static_cast<size_t>(t) * a.topk + l] = e;
+      a.weights[static_cast<size_t>(t) * a.topk + l] = a.scale * w * rcp(sum);
+    }
+  }
+}
+
 // Gradient of the scores where only the chosen ones have one (sigmoid, or weights
 // that are renormalised).  A token's slots lie in SLOTS neighbouring lanes, so that a
 // warp works on 32 / SLOTS tokens at once; it writes their rows, which lie behind one
@@ -1023,6 +1340,25 @@ flux_status_t launch_wide(const GroupGateArgs& a, const DeviceInfo& dev, cudaStr
   return launch_wide<0, 8, GROUPED>(a, dev, s);
 }
 
+template <int P, bool SOFT, bool BIASED>
+flux_status_t launch_octet(const GroupGateArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  constexpr auto kernel = group_gate_octet_kernel<P, SOFT, BIASED>;
+  constexpr int PER_SM = P == 32 ? 3 : 4;
+  const int smem = static_cast<int>(sizeof(float)) * (GG_WARPS * octet_words(octet_pitch<P>()) + (BIASED ? 8 * (P + 4) : 0));
+  static OncePerDevice once;
+  const cudaError_t attr = once(dev.device, [smem] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  if (attr != cudaSuccess) return cuda_fail(attr);
+  const int grid = std::min(ceil_div(a.T, GG_WARPS * 4), GG_SMS * PER_SM);
+  const cudaError_t e = launch_behind(kernel, dim3(grid), GG_THREADS, smem, s, a);
+  return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
+}
+
+template <int P>
+flux_status_t launch_octet(const GroupGateArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  if (a.softmax) return a.bias ? launch_octet<P, true, true>(a, dev, s) : launch_octet<P, true, false>(a, dev, s);
+  return a.bias ? launch_octet<P, false, true>(a, dev, s) : launch_octet<P, false, false>(a, dev, s);
+}
+
 template <int SLOTS>
 flux_status_t launch_bwd_chosen(const GroupGateArgs& a, cudaStream_t s) {
   const int grid = std::min(ceil_div(a.T, GG_WARPS * (32 / SLOTS)), GG_SMS * 8);
@@ -1088,11 +1424,25 @@ extern "C" flux_status_t flux_moe_group_gate(int T, int E, int topk, int score, 
   a.softmax = score == FLUX_SCORE_SOFTMAX;
   a.renorm = renorm != 0;
   a.scale = scale;
+  // Eight lanes a token where its groups fit them
+  const bool grouped = topk_groups < groups;
+  const int lanes = !grouped ? 8 : groups <= 8 && 8 % groups == 0 ? 8 / groups : 0;  // of a group
+  if (topk <= 8 && E <= 256 && lanes > 0 && (!grouped || a.n % lanes == 0)) {
+    a.per = grouped ? a.n / lanes : ceil_div(E, 8);
+    a.div_per = ((1u << 20) + a.per - 1) / a.per;
+    while (grouped && 1 << a.log_lpg < lanes) ++a.log_lpg;
+    a.vecs = a.per % 4 == 0 && E % 4 == 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a.per <= 4) return launch_octet<4>(a, dev, s);
+    if (a.per <= 8) return launch_octet<8>(a, dev, s);
+    if (a.per <= 16) return launch_octet<16>(a, dev, s);
+    return launch_octet<32>(a, dev, s);
+  }
   const int lpt = E <= 64 ? 8 : 32;
   a.lpg = lpt;  // lanes of a group: as many as let all groups be ranked at once, at least one
   while (a.lpg > 1 && a.lpg * groups > lpt) a.lpg /= 2;
   while (1 << a.log_lpg < a.lpg) ++a.log_lpg;
-  const bool grouped = topk_groups < groups, wide = lpt == 32 && a.n % 4 == 0;
+  const bool wide = lpt == 32 && a.n % 4 == 0;
   // words between the groups' rows: lanes of neighbouring groups read other banks
   a.pad = !grouped ? 0 : !wide ? a.lpg : a.lpg >= 8 ? 0 : (4 * a.lpg - a.n % 32 + 32) % 32;
   a.vecs = ceil_div(E, 128);

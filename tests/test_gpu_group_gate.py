@@ -70,6 +70,22 @@ CASES = [
     (4099, 8, 2, "softmax", 1, 1, 1, True, 1.0, False),
     (129, 128, 8, "sigmoid", 4, 2, 2, True, 1.0, False),    # ranks of scores, choice of logits
     (129, 66, 8, "sigmoid", 2, 1, 1, True, 1.0, False),
+    # eight lanes a token: every number of scores a lane, groups of 1, 2, 4 and 8 lanes
+    (70, 24, 5, "sigmoid", 2, 1, 2, True, 1.0, True),
+    (70, 40, 8, "softmax", 4, 3, 2, False, 1.0, True),
+    (70, 104, 7, "sigmoid", 1, 1, 1, False, 1.0, True),
+    (70, 121, 8, "softmax", 1, 1, 1, True, 1.0, True),
+    (70, 256, 1, "sigmoid", 2, 1, 1, True, 1.0, False),
+    (70, 200, 8, "softmax", 8, 5, 2, False, 2.0, False),
+    # one warp a token
+    (70, 256, 9, "sigmoid", 8, 4, 2, True, 1.0, True),
+    (70, 256, 12, "softmax", 1, 1, 1, False, 1.0, True),
+    (70, 260, 8, "sigmoid", 1, 1, 1, True, 1.0, True),
+    (70, 128, 10, "softmax", 2, 1, 1, True, 1.0, False),
+    (70, 512, 8, "softmax", 16, 5, 2, True, 1.0, True),
+    # rows that begin off 16 bytes, more than 64 experts
+    (33, 95, 9, "sigmoid", 5, 3, 2, True, 1.0, True),
+    (33, 250, 20, "softmax", 1, 1, 1, True, 1.0, True),
 ]
 
 
@@ -101,6 +117,34 @@ def test_values_closer_than_fp32(score, groups, kept, top, E):
     c = s + bias
     assert np.unique(np.sort(c)).size > E // 2 and np.ptp(c) < 2.0 ** -23
     Gate(37, E, 6, score, groups, kept, top, True, 1.0, bias=bias, logits=logits).check()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,kept", [(8, 1, 1), (40, 1, 1), (64, 8, 3), (100, 4, 2), (255, 1, 1), (256, 8, 4), (256, 2, 1),
+                                           (512, 1, 1)])
+def test_two_neighbours_closer_than_fp32(score, E, groups, kept):
+    # two experts whose s + bias are equal to 2^-24 or so in every token, anywhere in the order:
+    # both in, both out, or one in and one out
+    r = np.random.default_rng(E + groups)
+    T, k = 600, min(4, E // groups * kept)
+    logits = r.standard_normal((T, E)).astype(np.float32)
+    bias = (r.standard_normal(E) * 0.05).astype(np.float32)
+    pairs = [(0, E - 1), (1, 2), (E // 2, 3), (E // 2 + 1, E // 2 + 2)]
+    if score == "softmax":  # the same sum in every token: permuted rows of one
+        base = logits[0].copy()
+        for t in range(T):
+            logits[t] = base
+            rest = np.setdiff1d(np.arange(E), np.array(pairs).ravel())
+            logits[t, rest] = base[r.permutation(rest)]
+    else:
+        logits[:, np.array(pairs).ravel()] = r.standard_normal(8).astype(np.float32) + 1.0
+    s = oracle.gate_scores(logits[:1], score)[0]
+    for a, b in pairs:
+        bias[b] = np.float32(s[a] + np.float64(bias[a]) - s[b])
+    c = s + bias.astype(np.float64)
+    assert all(0 < abs(c[a] - c[b]) < 2.0 ** -23 for a, b in pairs)
+    for top in (1, 2):
+        Gate(T, E, k, score, groups, kept, top, True, 1.0, bias=bias, logits=logits).check()
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
