@@ -927,7 +927,38 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
       if (BIASED || two) {
         const float big = (isinf(m1) ? 0.0f : fabsf(m1)) + (isinf(m2) ? 0.0f : fabsf(m2));
         const float last = -O::maxf(in ? -rank : -INFINITY), next = O::maxf(in ? -INFINITY : rank);
-        doubt = !(last - next > 2.0f * unsure + 0x1p-21f * O::maxf(big));
+        const float room = 2.0f * unsure + 0x1p-21f * O::maxf(big);
+        doubt = !(last - next > room);
+        if constexpr (BIASED && !SOFT) {
+          // Groups next to the border, where a group is one lane: their ranks in doubles, from
+          // their two largest values (unless a third is next to the second) or their largest.
+          if (lpg == 1 && __any_sync(0xFFFFFFFFu, doubt)) {
+            const bool near = doubt && (in ? rank - next <= room : last - rank <= room);
+            const float least = (two ? m2 : m1) - room;
+            int count = 0, places = 0;
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+              const bool one = (full || k < mine) && c[k] >= least;
+              count += one;
+              places = one ? places << 8 | k : places;
+            }
+            const bool told = near && count == (two ? 2 : 1);
+            const int e = told ? l * a.per + (places & 255) : 0, f = told && two ? l * a.per + (places >> 8 & 255) : 0;
+            const double u = biased_sigmoid64(load_global(row + e), load_global(a.bias + e));
+            const double v = biased_sigmoid64(load_global(row + f), load_global(a.bias + f));
+            const double exact = !told ? rank : two ? u + v : u;
+            int ahead = 0;
+#pragma unroll
+            for (int d = 1; d < 8; ++d) {
+              const double other = __shfl_xor_sync(0xFFFFFFFFu, exact, d);
+              ahead += other > exact || (other == exact && (l ^ d) < l);
+            }
+            if (O::any(near && !told) == 0u && doubt) {
+              in = ahead < a.kept;
+              doubt = false;
+            }
+          }
+        }
       }
     }
     // lists of four, largest first, equal ones in order

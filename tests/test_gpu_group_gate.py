@@ -147,6 +147,32 @@ def test_two_neighbours_closer_than_fp32(score, E, groups, kept):
         Gate(T, E, k, score, groups, kept, top, True, 1.0, bias=bias, logits=logits).check()
 
 
+@pytest.mark.parametrize("E,groups", [(64, 8), (256, 8), (256, 4), (96, 3), (512, 16)])
+@pytest.mark.parametrize("top", [1, 2])
+def test_two_groups_closer_than_fp32(E, groups, top):
+    # two groups whose ranks are equal to 2^-23 or so in every token, inside, outside and on the border
+    r = np.random.default_rng(E + groups + top)
+    n, T = E // groups, 200
+    logits = (r.standard_normal((T, E)) * 0.5 - 1.0).astype(np.float32)
+    bias = (r.standard_normal(E) * 0.02).astype(np.float32)
+    a, b = 1, groups - 1  # the groups; their two largest are the same in every token
+    lead = [a * n + 1, a * n + 2, b * n, b * n + 3]
+    logits[:, lead] = np.array([2.0, 1.5, 1.75, 1.25], np.float32)
+    logits[::5, b * n + 5] = 1.25  # a third beside the second
+    s = oracle.gate_scores(logits[:1], "sigmoid")[0]
+    c = s + bias.astype(np.float64)
+    if top == 1:
+        bias[lead[2]] = np.float32(c[lead[0]] - s[lead[2]])
+    else:
+        bias[lead[3]] = np.float32(c[lead[0]] + c[lead[1]] - c[lead[2]] - s[lead[3]])
+    for t in range(T):  # other groups above and below them
+        for g in range(groups):
+            if g not in (a, b) and r.random() < 0.5:
+                logits[t, g * n:g * n + 2] = 3.0 + r.random(2)
+    for kept in sorted({1, 2, groups // 2, groups - 1}):
+        Gate(T, E, min(5, n * kept), "sigmoid", groups, kept, top, True, 1.0, bias=bias, logits=logits).check()
+
+
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("bias", ["zero", "own", None])
 @pytest.mark.parametrize("groups,kept,top", [(1, 1, 1), (8, 2, 1), (8, 2, 2)])
