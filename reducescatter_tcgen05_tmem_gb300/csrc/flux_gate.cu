@@ -167,8 +167,32 @@ __device__ __forceinline__ unsigned long long largest_of(uint32_t mask, unsigned
   return static_cast<unsigned long long>(hi) << 32 | lo;
 }
 
-__device__ __noinline__ double biased_sigmoid64(float x, float bias) {
-  return 1.0 / (1.0 + exp(-static_cast<double>(x != x ? -INFINITY : x))) + static_cast<double>(bias);
+// Two values in doubles, side by side: a dependent double operation takes some 100
+// cycles on this GPU.
+__device__ __noinline__ double2 biased_sigmoids64(float x, float x_bias, float y, float y_bias) {
+  const double u = -static_cast<double>(x != x ? -INFINITY : x), v = -static_cast<double>(y != y ? -INFINITY : y);
+  const double a = exp(u), b = exp(v);
+  return make_double2(1.0 / (1.0 + a) + static_cast<double>(x_bias), 1.0 / (1.0 + b) + static_cast<double>(y_bias));
+}
+
+// The order of a token's chosen experts, one to each of LANES lanes (those from topk on
+// have none), and of the one expert left out next to them (-1: none), by their doubles:
+// the place of the lane's own in x, of the one left out in y.  Takes 3 us, the choice in
+// full 12 to 20.
+template <int LANES>
+__device__ __noinline__ int2 order64(const float* row, const float* bias, int e, int out, int l, int topk) {
+  const bool here = l < topk;
+  const int mine = here ? e : 0, f = out >= 0 ? out : 0;
+  const double2 d = biased_sigmoids64(load_global(row + mine), load_global(bias + mine), load_global(row + f), load_global(bias + f));
+  auto first = [](double u, int i, double v, int k) { return u > v || (u == v && i < k); };
+  int2 place = make_int2(out >= 0 && first(d.y, out, d.x, e), 0);
+  for (int j = 0; j < topk; ++j) {
+    const double v = __shfl_sync(0xFFFFFFFFu, d.x, j, LANES);
+    const int k = __shfl_sync(0xFFFFFFFFu, e, j, LANES);
+    place.x += j != l && first(v, k, d.x, e);
+    place.y += first(v, k, d.y, out);
+  }
+  return place;
 }
 
 // The choice in doubles, by the LPT lanes of one token (mask).  Writes the kept groups
@@ -736,14 +760,42 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
         auto same = [&](int e, int f) { return raw[e] == raw[f] && bias[e] == bias[f]; };
         auto picked = [&](int j) { return expert(few ? candidate(pick[j]) : pick[j]); };
         const int end = picked(a.topk - 1);
+        bool unsorted = false;
         for (int j = lane; j + 1 < a.topk; j += 32) {
           const int e = picked(j), f = picked(j + 1);
-          if (!apart(value(e), value(f))) doubt |= !same(e, f);
+          if (!apart(value(e), value(f))) unsorted |= !same(e, f);
         }
+        // and what was left out next to the last one in
+        uint32_t out = 0xFFFFFFFFu, others = 0, equal = 0;
 #pragma unroll
-        for (int q = 0; q < LISTS; ++q)
-          for (int i = at[q]; i < (q * 32 + lane) * 5 + 4; ++i)  // what is left
-            if (list[i] == list[i] && !apart(value(end), list[i])) doubt |= !same(end, expert(candidate(i)));
+        for (int q = 0; q < LISTS; ++q) {
+          for (int i = at[q]; i < (q * 32 + lane) * 5 + 4; ++i) {
+            if (list[i] != list[i] || apart(value(end), list[i])) continue;
+            const int f = expert(candidate(i));
+            if (same(end, f)) {
+              ++equal;
+            } else {
+              ++others;
+              out = f;
+            }
+          }
+        }
+        others = __reduce_add_sync(0xFFFFFFFFu, others);
+        out = __reduce_min_sync(0xFFFFFFFFu, out);
+        equal = __reduce_add_sync(0xFFFFFFFFu, equal);
+        unsorted = __any_sync(0xFFFFFFFFu, unsorted) || others > 0u;
+        if (unsorted && !SOFT && few && others <= 1u && equal == 0u) {
+          // two neighbours, or the last one in and the first one out: by their doubles alone
+          const int f = others == 1u ? static_cast<int>(out) : -1;
+          const int2 place = order64<32>(a.logits + static_cast<size_t>(t) * a.E, a.bias, own, f, lane, a.topk);
+          __syncwarp();
+          if (lane < a.topk && place.x < a.topk) pick[place.x] = own;
+          if (lane == 0 && f >= 0 && place.y < a.topk) pick[place.y] = f;
+          __syncwarp();
+          if (lane < a.topk) own = pick[lane];
+        } else {
+          doubt |= unsorted;
+        }
       }
     }
     if ((BIASED || GROUPED) && __any_sync(0xFFFFFFFFu, doubt)) {
@@ -944,14 +996,13 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
             }
             const bool told = near && count == (two ? 2 : 1);
             const int e = told ? l * a.per + (places & 255) : 0, f = told && two ? l * a.per + (places >> 8 & 255) : 0;
-            const double u = biased_sigmoid64(load_global(row + e), load_global(a.bias + e));
-            const double v = biased_sigmoid64(load_global(row + f), load_global(a.bias + f));
-            const double exact = !told ? rank : two ? u + v : u;
+            const double2 d = biased_sigmoids64(load_global(row + e), load_global(a.bias + e), load_global(row + f), load_global(a.bias + f));
+            const double exact = !told ? rank : two ? d.x + d.y : d.x;
             int ahead = 0;
 #pragma unroll
-            for (int d = 1; d < 8; ++d) {
-              const double other = __shfl_xor_sync(0xFFFFFFFFu, exact, d);
-              ahead += other > exact || (other == exact && (l ^ d) < l);
+            for (int k = 1; k < 8; ++k) {
+              const double other = __shfl_xor_sync(0xFFFFFFFFu, exact, k);
+              ahead += other > exact || (other == exact && (l ^ k) < l);
             }
             if (O::any(near && !told) == 0u && doubt) {
               in = ahead < a.kept;
@@ -1084,27 +1135,14 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
         unsorted = O::any(unsorted || others > 0u) != 0u;
         if (SOFT || others > 1u || equal != 0u) doubt |= unsorted;
         // Mostly it is two neighbours, or the last one in and the first one out: their order
-        // is told by the doubles of these nine alone (the choice in full takes 12 us).
+        // is told by the doubles of these nine alone.
         const bool nine = unsorted && !SOFT && others <= 1u && equal == 0u;
         if (__any_sync(0xFFFFFFFFu, nine)) {
-          const double d = here ? biased_sigmoid64(load_global(row + e), load_global(a.bias + e)) : -INFINITY;
-          const int f = others == 1u ? static_cast<int>(out) : 0;
-          const double of = biased_sigmoid64(load_global(row + f), load_global(a.bias + f));
-          auto first = [](double u, int i, double v, int k) { return u > v || (u == v && i < k); };
-          int place = others == 1u && first(of, f, d, e);
-          int place_out = here && first(d, e, of, f);
-#pragma unroll
-          for (int m = 1; m < 8; ++m) {
-            const double v = __shfl_xor_sync(0xFFFFFFFFu, d, m);
-            const int k = __shfl_xor_sync(0xFFFFFFFFu, e, m);
-            place += (l ^ m) < a.topk && first(v, k, d, e);
-          }
-          place_out += __shfl_xor_sync(0xFFFFFFFFu, place_out, 1);
-          place_out += __shfl_xor_sync(0xFFFFFFFFu, place_out, 2);
-          place_out += __shfl_xor_sync(0xFFFFFFFFu, place_out, 4);
+          const int f = others == 1u ? static_cast<int>(out) : -1;
+          const int2 place = order64<8>(row, a.bias, e, f, l, a.topk);
           __syncwarp();
-          if (nine && here && place < a.topk) pick[place] = e;
-          if (nine && l == 0 && others == 1u && place_out < a.topk) pick[place_out] = f;
+          if (nine && here && place.x < a.topk) pick[place.x] = e;
+          if (nine && l == 0 && f >= 0 && place.y < a.topk) pick[place.y] = f;
           __syncwarp();
           if (nine && here) e = pick[l];
         }
@@ -1458,7 +1496,11 @@ extern "C" flux_status_t flux_moe_group_gate(int T, int E, int topk, int score, 
   // Eight lanes a token where its groups fit them
   const bool grouped = topk_groups < groups;
   const int lanes = !grouped ? 8 : groups <= 8 && 8 % groups == 0 ? 8 / groups : 0;  // of a group
-  if (topk <= 8 && E <= 256 && lanes > 0 && (!grouped || a.n % lanes == 0)) {
+  // A warp a token is faster while every token has one of its own (256 experts, 8 groups,
+  // us a warp a token and eight lanes: 13 tokens 2.8 and 5.3, 4864 9.0 and 12.3, 9728 25
+  // and 15).
+  const bool lone = T <= 32 * GG_SMS && E > 64;
+  if (topk <= 8 && E <= 256 && !lone && lanes > 0 && (!grouped || a.n % lanes == 0)) {
     a.per = grouped ? a.n / lanes : ceil_div(E, 8);
     a.div_per = ((1u << 20) + a.per - 1) / a.per;
     while (grouped && 1 << a.log_lpg < lanes) ++a.log_lpg;

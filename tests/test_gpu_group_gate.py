@@ -45,7 +45,20 @@ class Gate:
         assert np.array_equal(ids, want_ids)
         # exponentials, their sum and quotients, the arguments' rounding (up to 20 ulps of scores at most 20)
         check32(w, want_w, np.abs(want_w), depth=128, what="weights")
+        self.check_many(want_ids, want_w, 128)
         return ids
+
+    def check_many(self, want_ids, want_w, depth):
+        """The same tokens over and over: past 4864 of them more than one shares a warp."""
+        if self.E <= 64 or self.T > 4864:
+            return
+        times = 4900 // self.T + 1
+        ids = torch.full((times * self.T * self.k,), -7, dtype=torch.int32, device="cuda")
+        w = torch.empty(times * self.T * self.k, device="cuda")
+        fx.flux_moe_group_gate(times * self.T, *self.args[1:], self.cu.repeat(times, 1), self.cb, ids, w)
+        ids, w = ids.view(times, self.T, self.k).cpu().numpy(), w.view(times, self.T, self.k).double().cpu().numpy()
+        assert (ids == want_ids).all()
+        check32(w, np.broadcast_to(want_w, w.shape), np.broadcast_to(np.abs(want_w), w.shape), depth=depth, what="weights")
 
 
 CASES = [
@@ -192,7 +205,8 @@ def test_equal_scores(score, bias, groups, kept, top):
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("bias", [True, False])
 @pytest.mark.parametrize("groups,kept", [(1, 1), (4, 2)])
-def test_odd_rows(score, renorm, bias, groups, kept):
+@pytest.mark.parametrize("pad", [0, 64])
+def test_odd_rows(score, renorm, bias, groups, kept, pad):
     r = np.random.default_rng(10)
     z = r.standard_normal((14, 32)).astype(np.float32)
     z[0] = np.nan
@@ -208,11 +222,15 @@ def test_odd_rows(score, renorm, bias, groups, kept):
     z[10, 0] = 3e38
     z[11] = 45.0                      # equal 64-bit sigmoids from equal and from unequal scores
     z[12] = 40.0 + np.arange(32) % 3
-    g = Gate(14, 32, 4, score, groups, kept, 2, renorm, 1.5, bias=bias, logits=z)
+    if pad:  # wide rows: what was every score of a row is every score still
+        z = np.concatenate([z, z, z], axis=1)
+    g = Gate(14, z.shape[1], 4, score, groups, kept, 2, renorm, 1.5, bias=bias, logits=z)
     ids, w = g.run()
     want_ids, want_w = oracle.group_gate(z, None if g.bias is None else g.bias.astype(np.float64), *g.ref)
     assert np.array_equal(ids, want_ids)
     check32(w, want_w, np.abs(want_w), depth=1024, what="weights")  # arguments up to 200 round by 200 ulps of 1
+    if pad:
+        g.check_many(want_ids, want_w, 1024)
 
 
 def test_infinite_bias():
