@@ -836,7 +836,8 @@ flux_status_t flux_moe_group_gate_bwd(int T, int E, int topk, int score, int ren
 flux_status_t flux_q8_quantize(int rows, int K, flux_dtype_t dtype, const void* x, int8_t* q,
                                float* scales, void* stream);
 
-/* Bytes of workspace flux_q8_gemm needs; 0 for invalid sizes. */
+/* Bytes of workspace that are enough for flux_q8_gemm of up to M rows; 0 for invalid
+ * sizes. */
 size_t flux_q8_workspace_size(int M, int N, int K);
 
 /*   x  device int8[M x K]   x_scales  device float[M]

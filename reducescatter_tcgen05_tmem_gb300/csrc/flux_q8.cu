@@ -317,7 +317,8 @@ extern "C" flux_status_t flux_q8_quantize(int rows, int K, flux_dtype_t dtype, c
 extern "C" size_t flux_q8_workspace_size(int M, int N, int K) {
   if (!q8_sizes_ok(M, N, K) || !q8_sizes_supported(M, N, K)) return 0;
   if (M == 0 || N == 0 || K == 0) return WS_HEADER;
-  return WS_HEADER + (M <= FEW_ROWS ? few_plan(N, K).total : q8_gemm_bytes(M, N, K));
+  const size_t few = few_plan(N, K).total;
+  return WS_HEADER + (M <= FEW_ROWS ? few : std::max(few, q8_gemm_most_bytes(M, N, K)));
 }
 
 extern "C" flux_status_t flux_q8_gemm(int M, int N, int K, flux_dtype_t dtype, const int8_t* x, const float* x_scales,
@@ -330,7 +331,8 @@ extern "C" flux_status_t flux_q8_gemm(int M, int N, int K, flux_dtype_t dtype, c
     return FLUX_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w) || !aligned16(x_scales) || !aligned16(w_scales) || !aligned16(bias) || !aligned16(out))
     return FLUX_ERR_UNSUPPORTED;
-  flux_status_t st = check_workspace(workspace, workspace_bytes, flux_q8_workspace_size(M, N, K));
+  const size_t need = K == 0 ? 0 : M <= FEW_ROWS ? few_plan(N, K).total : q8_gemm_bytes(M, N, K);
+  flux_status_t st = check_workspace(workspace, workspace_bytes, WS_HEADER + need);
   if (st != FLUX_OK) return st;
   DeviceInfo dev;
   if ((st = current_device(&dev)) != FLUX_OK) return st;

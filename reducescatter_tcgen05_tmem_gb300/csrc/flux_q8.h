@@ -16,8 +16,10 @@ struct Q8Args {
   int M, N, K;
 };
 
-// The GEMM of many rows: its workspace (past the header) and its launch.
+// The GEMM of many rows: its workspace (past the header) for this size, and for every
+// M up to this; its launch.
 size_t q8_gemm_bytes(int M, int N, int K);
+size_t q8_gemm_most_bytes(int M, int N, int K);
 flux_status_t q8_gemm_launch(const Q8Args& a, flux_dtype_t dtype, void* workspace, const DeviceInfo& dev,
                              cudaStream_t s);
 

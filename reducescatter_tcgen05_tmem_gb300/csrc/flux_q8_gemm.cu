@@ -392,6 +392,8 @@ __global__ void __launch_bounds__(256) q8_parts_kernel(const __grid_constant__ Q
       make_uint2(pack2<DT>(s.x * xs * ws.x + b[0], s.y * xs * ws.y + b[1]), pack2<DT>(s.z * xs * ws.z + b[2], s.w * xs * ws.w + b[3]));
 }
 
+constexpr int G_MOST_SPLITS = 16, G_MOST_UNITS = 4 * G_PAIRS;  // parts of K; units where K is cut
+
 // Tokens of a tile and parts of K: those of the least estimated time, in cycles.  A step
 // of n tokens takes 4 n cycles of products, and at least as long as the weights' bytes
 // need; a unit begins and ends with about 1500 cycles that nothing covers, and the
@@ -410,8 +412,9 @@ Q8Plan q8_plan(int M, int N, int K) {
   for (int tiles = fewest; tiles <= fewest + fewest / 2 + 1; ++tiles) {
     const int n = ceil_div(ceil_div(M, tiles), 16) * 16, tt = ceil_div(M, n);
     const double step = std::max(4.0 * n, 600.0);
-    for (int splits = 1; splits <= 16 && splits <= best.steps; ++splits) {
+    for (int splits = 1; splits <= G_MOST_SPLITS && splits <= best.steps; ++splits) {
       const long long units = static_cast<long long>(tt) * best.ch_tiles * splits;
+      if (splits > 1 && units > G_MOST_UNITS) break;
       const double waves = static_cast<double>((units + G_PAIRS - 1) / G_PAIRS);
       double time = waves * (ceil_div(best.steps, splits) * step + 1500.0);
       if (splits > 1) time += 3000.0 + 8.0 * splits * M * N / 5000.0;
@@ -421,7 +424,6 @@ Q8Plan q8_plan(int M, int N, int K) {
         best.tok_tiles = tt;
         best.splits = splits;
       }
-      if (units > 4 * G_PAIRS) break;
     }
   }
   // whole tiles: what lies past the last token is read, and never stored
@@ -451,6 +453,15 @@ flux_status_t launch(const Q8GemmParams& p, const DeviceInfo& dev, cudaStream_t 
 size_t q8_gemm_bytes(int M, int N, int K) {
   const Q8Plan p = q8_plan(M, N, K);
   return p.x_bytes + p.part_bytes;
+}
+
+// Enough for every call of up to M rows: up to 15 rows of padding a tile, and the parts
+// of as many units as are cut at most.
+size_t q8_gemm_most_bytes(int M, int N, int K) {
+  const int fewest = ceil_div(M, G_TOK);
+  const size_t rows = static_cast<size_t>(M) + 16 * (static_cast<size_t>(fewest) + fewest / 2 + 1);
+  const size_t parts = std::min(sizeof(float) * G_MOST_SPLITS * M * N, sizeof(float) * G_MOST_UNITS * G_CH * G_TOK);
+  return round_up(rows * K * 2, WS_ALIGN) + parts;
 }
 
 flux_status_t q8_gemm_launch(const Q8Args& a, flux_dtype_t dtype, void* workspace, const DeviceInfo& dev, cudaStream_t s) {

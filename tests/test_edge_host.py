@@ -155,6 +155,22 @@ def test_q8_workspace(fx):
     assert size(400, 64, 64) > 256
 
 
+@pytest.mark.parametrize("N,K", [(8, 16), (256, 512), (4096, 4096), (4096, 14336), (8192, 28672), (14336, 4096), (264, 131056)])
+def test_a_q8_workspace_is_enough_for_every_smaller_batch(fx, N, K):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the calls would run")
+    last = 0
+    for M in (1, 8, 9, 16, 100, 333, 1000, 4096):
+        size = fx.flux_q8_workspace_size(M, N, K)
+        assert size >= last
+        last = size
+    for M in list(range(1, 200)) + list(range(200, 4097, 61)):
+        # everything is in order but the machine
+        assert _status(fx, fx.flux_q8_gemm, dict(M=M, N=N, K=K, dtype=0, x=FAKE, x_scales=FAKE, w=FAKE, w_scales=FAKE, bias=None,
+                                                 out=FAKE, workspace=WS(last), stream=0)) in (fx.FLUX_ERR_CUDA, fx.FLUX_ERR_NO_DEVICE)
+
+
 def test_empty_calls_return_without_a_gpu(fx):
     fx.flux_layer_norm(1, 0, 64, 0, 0.0, 1e-5, None, None, None, None, None, None, P, stream=0)
     fx.flux_moe_group_gate(0, 8, 2, 0, 1, 1, 1, 0, 1.0, None, None, None, None, stream=0)
