@@ -113,6 +113,13 @@ struct Over {
   }
 };
 
+// Whether the last kept group and the first one left out are told apart by their fp32
+// ranks: by more than their errors, or equal and infinite where nothing finite is so
+// large that its sum may have become so (then `room` is infinite too).
+__device__ __forceinline__ bool ranks_apart(float last, float next, float room) {
+  return last - next > room || (last == next && isinf(last) && room < INFINITY);
+}
+
 // f(e, logit) for the lane's experts of a row, a NaN as -inf.
 template <int LPT, typename F>
 __device__ __forceinline__ void each_logit(const float* row, int E, int l, F&& f) {
@@ -417,7 +424,7 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
       __syncwarp();
       // (ranks that are logits are exact)
       if (biased || (a.top == 2 && a.n > 1))
-        doubt = !(r.sorted[a.kept - 1] - r.sorted[a.kept] > 2.0f * unsure + 0x1p-21f * big);
+        doubt = !ranks_apart(r.sorted[a.kept - 1], r.sorted[a.kept], 2.0f * unsure + 0x1p-21f * big);
     }
     const int count = a.kept * a.n;
     uint32_t key[NC];
@@ -640,7 +647,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
       if (BIASED || two) {
         const float big = g < a.G ? (isinf(m1) ? 0.0f : fabsf(m1)) + (isinf(m2) ? 0.0f : fabsf(m2)) : 0.0f;
         const float last = -warp_largest(in ? -rank : NAN), next = warp_largest(in || g >= a.G ? NAN : rank);
-        doubt = !(last - next > 2.0f * unsure + 0x1p-21f * warp_largest(big));
+        doubt = !ranks_apart(last, next, 2.0f * unsure + 0x1p-21f * warp_largest(big));
       }
       __syncwarp();
     }
@@ -980,12 +987,12 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
         const float big = (isinf(m1) ? 0.0f : fabsf(m1)) + (isinf(m2) ? 0.0f : fabsf(m2));
         const float last = -O::maxf(in ? -rank : -INFINITY), next = O::maxf(in ? -INFINITY : rank);
         const float room = 2.0f * unsure + 0x1p-21f * O::maxf(big);
-        doubt = !(last - next > room);
+        doubt = !ranks_apart(last, next, room);
         if constexpr (BIASED && !SOFT) {
           // Groups next to the border, where a group is one lane: their ranks in doubles, from
           // their two largest values (unless a third is next to the second) or their largest.
           if (lpg == 1 && __any_sync(0xFFFFFFFFu, doubt)) {
-            const bool near = doubt && (in ? rank - next <= room : last - rank <= room);
+            const bool near = doubt && (room == INFINITY || (in ? rank - next <= room : last - rank <= room));
             const float least = (two ? m2 : m1) - room;
             int count = 0, places = 0;
 #pragma unroll
@@ -997,7 +1004,7 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
             const bool told = near && count == (two ? 2 : 1);
             const int e = told ? l * a.per + (places & 255) : 0, f = told && two ? l * a.per + (places >> 8 & 255) : 0;
             const double2 d = biased_sigmoids64(load_global(row + e), load_global(a.bias + e), load_global(row + f), load_global(a.bias + f));
-            const double exact = !told ? rank : two ? d.x + d.y : d.x;
+            const double exact = !told ? rank : two ? fmax(d.x + d.y, static_cast<double>(-INFINITY)) : d.x;
             int ahead = 0;
 #pragma unroll
             for (int k = 1; k < 8; ++k) {

@@ -409,8 +409,9 @@ Q8Plan q8_plan(int M, int N, int K) {
   best.steps = ceil_div(K, G_K);
   double least = 0.0;
   const int fewest = ceil_div(M, G_TOK);
-  for (int tiles = fewest; tiles <= fewest + fewest / 2 + 1; ++tiles) {
-    const int n = ceil_div(ceil_div(M, tiles), 16) * 16, tt = ceil_div(M, n);
+  for (int most = G_TOK; most > 0; most -= 16) {
+    const int tt = ceil_div(M, most), n = ceil_div(ceil_div(M, tt), 16) * 16;
+    if (tt > fewest + fewest / 2 + 1) break;
     const double step = std::max(4.0 * n, 600.0);
     for (int splits = 1; splits <= G_MOST_SPLITS && splits <= best.steps; ++splits) {
       const long long units = static_cast<long long>(tt) * best.ch_tiles * splits;

@@ -233,6 +233,32 @@ def test_odd_rows(score, renorm, bias, groups, kept, pad):
         g.check_many(want_ids, want_w, 1024)
 
 
+@pytest.mark.parametrize("E,groups,kept", [(64, 8, 4), (16, 8, 3), (32, 4, 2), (60, 5, 2), (95, 5, 2), (96, 3, 1), (256, 8, 4), (256, 2, 1), (512, 16, 4)])
+@pytest.mark.parametrize("top", [1, 2])
+def test_biases_whose_sums_pass_fp32(E, groups, kept, top):
+    """A rank that is a sum of two may be infinite in fp32; in doubles it is not."""
+    r = np.random.default_rng(E + top)
+    bias = r.uniform(1.8e38, 3.3e38, E).astype(np.float32)
+    Gate(40, E, 2, "sigmoid", groups, kept, top, bias=bias, seed=E).check()
+    Gate(40, E, 2, "sigmoid", groups, kept, top, bias=-bias, seed=E).check()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,kept,open_groups", [(64, 8, 4, 2), (16, 8, 3, 1), (60, 5, 2, 1), (95, 5, 2, 1), (256, 8, 4, 3), (512, 16, 4, 2)])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("low", [-np.inf, float(np.finfo(np.float32).min)])
+def test_masked_groups(score, E, groups, kept, open_groups, top, low):
+    """Fewer groups than are kept have experts that are not masked; a masked one is never chosen."""
+    r = np.random.default_rng(E + kept + top)
+    n = E // groups
+    bias = (r.standard_normal(E) * 0.01).astype(np.float32)
+    closed = r.permutation(groups)[open_groups:]
+    for g in closed:
+        bias[g * n:(g + 1) * n] = low
+    ids = Gate(40, E, 2, score, groups, kept, top, bias=bias, seed=E).check()
+    assert not np.isin(ids // n, closed).any()
+
+
 def test_infinite_bias():
     b = np.zeros(64, np.float32)
     b[::3] = -np.inf  # experts that are switched off
