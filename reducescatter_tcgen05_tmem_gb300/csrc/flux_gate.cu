@@ -641,14 +641,51 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
         before += o < a.G && (other > rank || (other == rank && o < g));
       }
       for (int o = a.lpg >> 1; o > 0; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
-      const bool in = g < a.G && before < a.kept;
-      const uint32_t set = __ballot_sync(0xFFFFFFFFu, in && sub == 0);
-      if (in && sub == 0) kept[__popc(set & ((1u << lane) - 1u))] = g;
+      bool in = g < a.G && before < a.kept;
       if (BIASED || two) {
         const float big = g < a.G ? (isinf(m1) ? 0.0f : fabsf(m1)) + (isinf(m2) ? 0.0f : fabsf(m2)) : 0.0f;
         const float last = -warp_largest(in ? -rank : NAN), next = warp_largest(in || g >= a.G ? NAN : rank);
-        doubt = !ranks_apart(last, next, 2.0f * unsure + 0x1p-21f * warp_largest(big));
+        const float room = 2.0f * unsure + 0x1p-21f * warp_largest(big);
+        doubt = !ranks_apart(last, next, room);
+        if constexpr (BIASED && !SOFT) {
+          // Groups next to the border: their ranks in doubles, from their two largest values
+          // (unless a third is next to the second) or their largest, wherever they lie.
+          if (doubt) {
+            const bool near = g < a.G && (room == INFINITY || (in ? rank - next <= room : last - rank <= room));
+            const float least = (two ? m2 : m1) - room;
+            int count = 0, e = 0, f = 0;
+            if (near) {
+              for (int k = 0; k < a.trips; ++k) {
+                const int i = (k * a.lpg + sub) * 4;
+                for (int j = i; j < min(i + 4, a.n); ++j) {
+                  if (mine[j] < least) continue;
+                  ++count;
+                  f = e;
+                  e = g * a.n + j;
+                }
+              }
+            }
+            int all = count;
+            for (int o = a.lpg >> 1; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+            const bool told = near && all == (two ? 2 : 1);
+            const double2 d = biased_sigmoids64(raw[e], bias[e], raw[f], bias[f]);
+            double exact = (count > 0 ? d.x : 0.0) + (count > 1 ? d.y : 0.0);
+            for (int o = a.lpg >> 1; o > 0; o >>= 1) exact += __shfl_xor_sync(0xFFFFFFFFu, exact, o);
+            exact = told ? fmax(exact, static_cast<double>(-INFINITY)) : rank;
+            int ahead = 0;
+            for (int o = 0; o < a.G; ++o) {
+              const double other = __shfl_sync(0xFFFFFFFFu, exact, o << a.log_lpg);
+              ahead += other > exact || (other == exact && o < g);
+            }
+            if (!__any_sync(0xFFFFFFFFu, near && !told)) {
+              in = g < a.G && ahead < a.kept;
+              doubt = false;
+            }
+          }
+        }
       }
+      const uint32_t set = __ballot_sync(0xFFFFFFFFu, in && sub == 0);
+      if (in && sub == 0) kept[__popc(set & ((1u << lane) - 1u))] = g;
       __syncwarp();
     }
     // lists of four, largest first, equal ones in order; their numbers in the bytes of a
@@ -1246,12 +1283,14 @@ group_gate_bwd_chosen_kernel(const __grid_constant__ GroupGateArgs a) {
   }
 }
 
+constexpr int bwd_ctas(int v) { return v <= 2 ? 6 : v == 4 ? 4 : 3; }  // per SM
+
 // The same for tokens of more than 32 slots, and the softmax that is not renormalised:
 // every score has a gradient, -p sum_i p_i g_i, and the chosen ones p g more.  LPT lanes
 // hold a token's scores in V vectors of four (or, for rows that do not begin on 16
 // bytes, scores one by one).
 template <int LPT, int V>
-__global__ void __launch_bounds__(GG_THREADS)
+__global__ void __launch_bounds__(GG_THREADS, bwd_ctas(V))
 group_gate_bwd_kernel(const __grid_constant__ GroupGateArgs a) {
   constexpr int TPW = 32 / LPT;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT;
@@ -1264,12 +1303,18 @@ group_gate_bwd_kernel(const __grid_constant__ GroupGateArgs a) {
     const float* row = a.logits + t * a.E;
     float* out = a.dlogits + t * a.E;
     auto expert = [&](int v, int i) { return vec ? (v * LPT + l) * 4 + i : (v * 4 + i) * LPT + l; };
-    auto id = [&](int j) {
-      const int e = load_global(a.ids_in + t * a.topk + j);
-      return e < a.E ? e : -1;
+    struct Slot {
+      int e;
+      float g, x;
     };
-    auto grad = [&](int j) { return a.scale * load_global(a.dweights + t * a.topk + j); };
-    auto logit = [&](int e) { return e >= 0 ? fmaxf(load_global(row + e), -INFINITY) : -INFINITY; };
+    auto load = [&](int j) {
+      const int e = load_global(a.ids_in + t * a.topk + j);
+      const float g = a.scale * load_global(a.dweights + t * a.topk + j);
+      return Slot{e < a.E ? e : -1, g, e >= 0 && e < a.E ? fmaxf(load_global(row + e), -INFINITY) : -INFINITY};
+    };
+    // a lane's first slot is on its way before the row is worked on
+    const Slot first = l < a.topk ? load(l) : Slot{-1, 0.0f, -INFINITY};
+    auto slot = [&](int j) { return j == l ? first : load(j); };
     float f[V][4] = {};
     float peak = -INFINITY, total = 0.0f, dot = 0.0f;
     if (every) {
@@ -1293,7 +1338,7 @@ group_gate_bwd_kernel(const __grid_constant__ GroupGateArgs a) {
         for (int i = 0; i < 4; ++i) total += f[v][i] = isinf(peak) ? 0.0f : ex2((f[v][i] - peak) * G_LOG2E);
       total = O::sum(total);
     } else if (a.renorm) {
-      for (int j = l; j < a.topk; j += LPT) peak = fmaxf(peak, logit(id(j)));
+      for (int j = l; j < a.topk; j += LPT) peak = fmaxf(peak, slot(j).x);
       peak = O::maxf(peak);
     }
     const bool constant = (every || a.renorm) && (a.softmax ? isinf(peak) : peak == -INFINITY);
@@ -1305,9 +1350,10 @@ group_gate_bwd_kernel(const __grid_constant__ GroupGateArgs a) {
     if (every || a.renorm) {
       float sum = 0.0f;
       for (int j = l; j < a.topk; j += LPT) {
-        const float v = part(logit(id(j)));
+        const Slot c = slot(j);
+        const float v = part(c.x);
         sum += v;
-        dot += v * grad(j);
+        dot += v * c.g;
       }
       if (!every) total = O::sum(sum);
       dot = O::sum(dot);
@@ -1341,9 +1387,10 @@ group_gate_bwd_kernel(const __grid_constant__ GroupGateArgs a) {
       __syncwarp();
     }
     for (int j = l; j < a.topk; j += LPT) {
-      const int e = id(j);
+      const Slot c = slot(j);
+      const int e = c.e;
       if (e < 0 || !here) continue;
-      const float x = logit(e), g = grad(j), p = part(x) * inv;
+      const float x = c.x, g = c.g, p = part(x) * inv;
       float d = a.renorm || every ? p * (g - dot) : p * g;
       if (!a.softmax) {
         const float small = expf(-fabsf(x));
@@ -1444,7 +1491,7 @@ flux_status_t launch_bwd_chosen(const GroupGateArgs& a, cudaStream_t s) {
 
 template <int LPT, int V>
 flux_status_t launch_bwd(const GroupGateArgs& a, cudaStream_t s) {
-  const int grid = std::min(ceil_div(a.T, GG_WARPS * (32 / LPT)), GG_SMS * 6);
+  const int grid = std::min(ceil_div(a.T, GG_WARPS * (32 / LPT)), GG_SMS * bwd_ctas(V));
   const cudaError_t e = launch_behind(group_gate_bwd_kernel<LPT, V>, dim3(grid), GG_THREADS, 0, s, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
 }
@@ -1503,10 +1550,10 @@ extern "C" flux_status_t flux_moe_group_gate(int T, int E, int topk, int score, 
   // Eight lanes a token where its groups fit them
   const bool grouped = topk_groups < groups;
   const int lanes = !grouped ? 8 : groups <= 8 && 8 % groups == 0 ? 8 / groups : 0;  // of a group
-  // A warp a token is faster while every token has one of its own (256 experts, 8 groups,
-  // us a warp a token and eight lanes: 13 tokens 2.8 and 5.3, 4864 9.0 and 12.3, 9728 25
-  // and 15).
-  const bool lone = T <= 32 * GG_SMS && E > 64;
+  // A warp a token is faster while a warp has at most two or three of them (256 experts, 8
+  // groups, us with cold caches, a warp a token and eight lanes: 13 tokens 4.1 and 6.2,
+  // 4864 10 and 14, 9728 13 and 16, 19456 20 and 20, 131072 120 and 80).
+  const bool lone = T <= 64 * GG_SMS && E > 64;
   if (topk <= 8 && E <= 256 && !lone && lanes > 0 && (!grouped || a.n % lanes == 0)) {
     a.per = grouped ? a.n / lanes : ceil_div(E, 8);
     a.div_per = ((1u << 20) + a.per - 1) / a.per;

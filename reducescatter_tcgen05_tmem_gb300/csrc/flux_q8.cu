@@ -116,8 +116,8 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
 constexpr int FEW_ROWS = 8;             // of x: the columns of one instruction
 constexpr int FEW_WARPS = 8, FEW_THREADS = FEW_WARPS * 32, FEW_CTAS = 3;
 constexpr int FEW_CH = 16;              // channels of a block: the rows of one instruction
-constexpr int FEW_K = FEW_WARPS * 64;   // of a step: 64 codes a warp
-constexpr int FEW_DEPTH = 4;            // steps on their way
+constexpr int FEW_K = FEW_WARPS * 128;  // of a step: 128 codes a warp
+constexpr int FEW_DEPTH = 2;            // steps on their way
 constexpr int FEW_SLOT = FEW_ROWS * FEW_CH;
 
 struct FewPlan {
@@ -127,15 +127,15 @@ struct FewPlan {
 };
 
 // Whole blocks leave some SMs idle at the end, equal stretches need the parts of cut
-// blocks joined by a second kernel, which costs about as much as 11 steps (4096 x 4096:
-// 27 steps an SM on average, 32 with whole blocks, which are faster by 1.5 us; 28672 x
-// 8192: 189 against 224, and stretches are faster by 5 us).
+// blocks joined by a second kernel, which costs about as much as 6 steps (4096 x 4096: 7
+// steps an SM on average, 8 with whole blocks, which are faster by 1.5 us; 28672 x
+// 8192: 94 against 112, and stretches are faster by 5 us).
 FewPlan few_plan(int N, int K) {
   FewPlan p{};
   p.blocks = ceil_div(N, FEW_CH);
   p.steps = ceil_div(K, FEW_K);
   const long long units = static_cast<long long>(p.blocks) * p.steps;
-  const long long whole = static_cast<long long>(ceil_div(p.blocks, Q8_SMS)) * p.steps, even = units / Q8_SMS + 11;
+  const long long whole = static_cast<long long>(ceil_div(p.blocks, Q8_SMS)) * p.steps, even = units / Q8_SMS + 6;
   p.ctas = static_cast<int>(whole <= even ? p.blocks : std::min<long long>(units, FEW_CTAS * Q8_SMS));
   p.total = p.ctas == p.blocks ? 0 : sizeof(int) * FEW_SLOT * 2 * static_cast<size_t>(p.ctas);
   return p;
@@ -153,7 +153,7 @@ __device__ __forceinline__ void few_store(const Q8Args& a, int ch, int row, int 
 }
 
 // Up to 8 rows.  A CTA takes a stretch of the steps of all blocks of 16 channels, its
-// warps 64 codes of a step each.  A lane's 16 bytes of a weight row and of a token are
+// warps 128 codes of a step each.  A lane's 16 bytes of a weight row and of a token are
 // the operands of two instructions (the order of K within them is the lanes' own, the
 // same for both sides).  Weights and tokens are loaded FEW_DEPTH steps ahead into
 // registers.  The warps' sums meet in shared memory at the end of a block; a block
@@ -173,17 +173,20 @@ q8_few_kernel(const __grid_constant__ Q8Args a, int* parts, int steps, long long
   int left_a = static_cast<int>(u1 - u0), left = left_a;  // steps to fetch, to work on
   // what is fetched next: 16 bytes of channels g and g + 8 of a block, and of token g
   const size_t pitch = static_cast<size_t>(a.K);
-  int step_a = first_step, k_a = first_step * FEW_K + warp * 64 + t * 16, n_a = first_block * FEW_CH + g;
+  int step_a = first_step, k_a = first_step * FEW_K + warp * 128 + t * 16, n_a = first_block * FEW_CH + g;
   const int8_t* w_a = a.w + static_cast<size_t>(n_a) * pitch + k_a;
   const int8_t* x_a = a.x + static_cast<size_t>(g) * pitch + k_a;
   wait_for_previous();
-  uint4 lo[FEW_DEPTH], hi[FEW_DEPTH], xs[FEW_DEPTH];
+  uint4 lo[FEW_DEPTH][2], hi[FEW_DEPTH][2], xs[FEW_DEPTH][2];
   const uint4 none = make_uint4(0, 0, 0, 0);
-  auto fetch = [&](uint4& l, uint4& h, uint4& x) {
-    const bool in = left_a > 0 && k_a < a.K;
-    l = in && n_a < a.N ? load_global(reinterpret_cast<const uint4*>(w_a)) : none;
-    h = in && n_a + 8 < a.N ? load_global(reinterpret_cast<const uint4*>(w_a + 8 * pitch)) : none;
-    x = in && g < a.M ? load_global(reinterpret_cast<const uint4*>(x_a)) : none;
+  auto fetch = [&](uint4 (&l)[2], uint4 (&h)[2], uint4 (&x)[2]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const bool in = left_a > 0 && k_a + 64 * j < a.K;
+      l[j] = in && n_a < a.N ? load_global(reinterpret_cast<const uint4*>(w_a + 64 * j)) : none;
+      h[j] = in && n_a + 8 < a.N ? load_global(reinterpret_cast<const uint4*>(w_a + 8 * pitch + 64 * j)) : none;
+      x[j] = in && g < a.M ? load_global(reinterpret_cast<const uint4*>(x_a + 64 * j)) : none;
+    }
     --left_a;
     if (++step_a < steps) {
       k_a += FEW_K;
@@ -207,8 +210,11 @@ q8_few_kernel(const __grid_constant__ Q8Args a, int* parts, int steps, long long
 #pragma unroll
     for (int i = 0; i < FEW_DEPTH; ++i) {
       if (left == 0) break;
-      mma_s8(acc, lo[i].x, hi[i].x, lo[i].y, hi[i].y, xs[i].x, xs[i].y);
-      mma_s8(acc, lo[i].z, hi[i].z, lo[i].w, hi[i].w, xs[i].z, xs[i].w);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        mma_s8(acc, lo[i][j].x, hi[i][j].x, lo[i][j].y, hi[i][j].y, xs[i][j].x, xs[i][j].y);
+        mma_s8(acc, lo[i][j].z, hi[i][j].z, lo[i][j].w, hi[i][j].w, xs[i][j].z, xs[i][j].w);
+      }
       fetch(lo[i], hi[i], xs[i]);
       --left;
       const bool ends = ++step == steps;

@@ -49,10 +49,10 @@ class Gate:
         return ids
 
     def check_many(self, want_ids, want_w, depth):
-        """The same tokens over and over: past 4864 of them more than one shares a warp."""
-        if self.E <= 64 or self.T > 4864:
+        """The same tokens over and over: past 9728 of them a warp takes four at once."""
+        if self.E <= 64 or self.T > 9728:
             return
-        times = 4900 // self.T + 1
+        times = 9800 // self.T + 1
         ids = torch.full((times * self.T * self.k,), -7, dtype=torch.int32, device="cuda")
         w = torch.empty(times * self.T * self.k, device="cuda")
         fx.flux_moe_group_gate(times * self.T, *self.args[1:], self.cu.repeat(times, 1), self.cb, ids, w)
