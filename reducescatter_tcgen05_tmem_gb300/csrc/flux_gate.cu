@@ -1505,8 +1505,8 @@ flux_status_t launch_gate_bwd(const GroupGateArgs& a, cudaStream_t s) {
   }
   if (a.E <= 32) return launch_bwd<8, 1>(a, s);
   if (a.E <= 64) return launch_bwd<8, 2>(a, s);
-  if (a.E <= 128) return launch_bwd<32, 1>(a, s);
-  if (a.E <= 256) return launch_bwd<32, 2>(a, s);
+  if (a.E <= 128) return launch_bwd<16, 2>(a, s);
+  if (a.E <= 256) return launch_bwd<16, 4>(a, s);
   if (a.E <= 512) return launch_bwd<32, 4>(a, s);
   return launch_bwd<32, 8>(a, s);
 }
