@@ -60,8 +60,10 @@
  *     bytes, and zero-filled once before first use (flux_workspace_init).
  *     Every successful call leaves its workspace zero again (the MoE layers leave
  *     their routing and staged rows in it, flux_q8_gemm of more than 8 rows its
- *     widened tokens and partial sums).  The block-norm, layer-norm, router, 4-bit and 8-bit
- *     calls need zeros in the first 256 bytes only.  Calls that share
+ *     widened tokens and partial sums: before a dense or MoE layer the workspace
+ *     has to be zero-filled again, or that layer has one of its own).  The
+ *     block-norm, layer-norm, router, 4-bit and 8-bit calls need zeros in the
+ *     first 256 bytes only.  Calls that share
  *     one workspace must be ordered on the GPU (same stream or events); calls
  *     that overlap on the GPU need separate workspaces.
  */

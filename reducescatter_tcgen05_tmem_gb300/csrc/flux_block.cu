@@ -804,8 +804,7 @@ template <int DT, int W, int V, bool HAS_Y>
 flux_status_t launch_fwd_form(const BlockNormArgs& a, const DeviceInfo& dev, cudaStream_t s) {
   using S = FwdShape<W, V>;
   constexpr auto kernel = block_norm_kernel<DT, W, V, HAS_Y>;
-  static OncePerDevice once;
-  const cudaError_t attr = once(dev.device, [] { return allow_smem(kernel, S::SMEM); });
+  const cudaError_t attr = allow_smem<kernel, S::SMEM>(dev.device);
   if (attr != cudaSuccess) return cuda_fail(attr);
   const int grid = std::min(ceil_div(a.T, Team<W>::COUNT), dev.sm_count * S::CTAS);
   const cudaError_t e = launch_behind(kernel, dim3(grid), Team<W>::CTA, S::SMEM, s, a);
@@ -824,8 +823,7 @@ template <int DT, int W, int V, bool HAS_Y, bool HAS_U>
 flux_status_t launch_bwd_form(const BlockNormArgs& a, const BwdPlan& p, const DeviceInfo& dev, cudaStream_t s) {
   constexpr int smem = BwdShape<W, V>::SMEM;
   constexpr auto kernel = block_norm_bwd_kernel<DT, W, V, HAS_Y, HAS_U>;
-  static OncePerDevice once;
-  const cudaError_t attr = once(dev.device, [] { return allow_smem(kernel, smem); });
+  const cudaError_t attr = allow_smem<kernel, smem>(dev.device);
   if (attr != cudaSuccess) return cuda_fail(attr);
   const cudaError_t e = launch_behind(kernel, dim3(p.ctas), Team<W>::CTA, smem, s, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);

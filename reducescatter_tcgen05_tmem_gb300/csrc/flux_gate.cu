@@ -375,8 +375,10 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
     __syncwarp();
     // How far apart two values have to be for their order to be sure: errors of the
     // sigmoid 4.4 2^-24 (argument, ex2, sum, reciprocal), of the softmax 70 2^-24 of its
-    // largest, and half an ulp for the bias; twice that for two values, and a margin.
-    const float unsure = a.softmax ? 0x1p-16f * inv : 0x1p-20f;
+    // largest, and half an ulp for the bias; twice that for two values, and a margin.  Of
+    // softmax ranks without a bias 5 2^-24 for each of four values: the error of their
+    // sum, most of the 70, is a factor that they share.
+    const float unsure = a.softmax ? (biased ? 0x1p-16f : 0x1p-20f) * inv : 0x1p-20f;
     uint32_t doubt = 0;  // the groups' choice is not sure
     if (grouped) {
       const int per = LPT / a.lpg;
@@ -524,6 +526,10 @@ __host__ __device__ inline int wide_words(int vecs, int row, int topk, int lists
 // groups') lie in LISTS sorted lists of four a lane, so that a round of the choice
 // is a maximum over the lists' heads and over the warp, and a shift of the winner's
 // list.
+//
+// Bound by the length of that chain: 13 tokens of 256 experts 2.9 us in a captured
+// graph, 4096 tokens 10 us with cold caches where a token of them needs doubles, 6 where
+// none does; 131072 tokens 116 us, which is why long batches take the octet form.
 template <int VECS, int LISTS, bool GROUPED, bool SOFT, bool BIASED>
 __global__ void __launch_bounds__(GG_THREADS, LISTS <= 2 ? 4 : 3)
 group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
@@ -603,7 +609,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
       return x;
     };
     // (how far apart: as in group_gate_kernel)
-    const float unsure = SOFT ? 0x1p-16f * inv : 0x1p-20f;
+    const float unsure = SOFT ? (BIASED ? 0x1p-16f : 0x1p-20f) * inv : 0x1p-20f;
     bool doubt = false;
     if constexpr (GROUPED) {
 #pragma unroll 2
@@ -905,6 +911,9 @@ __host__ __device__ inline int octet_words(int pitch) { return 32 * pitch + 4 * 
 // Four tokens to a warp: a token's scores lie in neighbouring order in eight lanes, P
 // at most in each, so that a group is one lane (or 2, 4 or 8) and most of the work is
 // in the lanes' own registers.  Lists and rounds as in group_gate_wide_kernel.
+// 131072 x 256 (8 of 256 in 4 of 8 groups) 80 us, of which the logits' bytes need 20:
+// bound by issue slots (62 % busy with the 24 warps an SM that 80 registers leave) and
+// by tokens that need doubles.
 template <int P, bool SOFT, bool BIASED>
 __global__ void __launch_bounds__(GG_THREADS, P == 32 ? 3 : 4)
 group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
@@ -994,7 +1003,7 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
       }
     }
     // (how far apart: as in group_gate_kernel)
-    const float unsure = SOFT ? 0x1p-16f * inv : 0x1p-20f;
+    const float unsure = SOFT ? (BIASED ? 0x1p-16f : 0x1p-20f) * inv : 0x1p-20f;
     bool doubt = false, in = true;
     if (grouped) {
       float m1 = -INFINITY, m2 = -INFINITY;
@@ -1224,7 +1233,9 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
 // Gradient of the scores where only the chosen ones have one (sigmoid, or weights
 // that are renormalised).  A token's slots lie in SLOTS neighbouring lanes, so that a
 // warp works on 32 / SLOTS tokens at once; it writes their rows, which lie behind one
-// another, with zeros, and then the slots' gradients over them.  Bound by the writes.
+// another, with zeros, and then the slots' gradients over them.  Bound by memory: 131072
+// x 256 34 us for 134 MB written and 75 MB read (a chosen score brings its sector of 32
+// bytes).
 template <int SLOTS>
 __global__ void __launch_bounds__(GG_THREADS)
 group_gate_bwd_chosen_kernel(const __grid_constant__ GroupGateArgs a) {
@@ -1288,7 +1299,9 @@ constexpr int bwd_ctas(int v) { return v <= 2 ? 6 : v == 4 ? 4 : 3; }  // per SM
 // The same for tokens of more than 32 slots, and the softmax that is not renormalised:
 // every score has a gradient, -p sum_i p_i g_i, and the chosen ones p g more.  LPT lanes
 // hold a token's scores in V vectors of four (or, for rows that do not begin on 16
-// bytes, scores one by one).
+// bytes, scores one by one).  A grid of as many CTAs as are on the GPU at once: 131072 x
+// 256 57 us, with a sixth CTA where five fit an SM 98; 16 lanes a token, with 32 63 us
+// (128 experts 35 and 53).
 template <int LPT, int V>
 __global__ void __launch_bounds__(GG_THREADS, bwd_ctas(V))
 group_gate_bwd_kernel(const __grid_constant__ GroupGateArgs a) {
@@ -1552,8 +1565,10 @@ extern "C" flux_status_t flux_moe_group_gate(int T, int E, int topk, int score, 
   const int lanes = !grouped ? 8 : groups <= 8 && 8 % groups == 0 ? 8 / groups : 0;  // of a group
   // A warp a token is faster while a warp has at most two or three of them (256 experts, 8
   // groups, us with cold caches, a warp a token and eight lanes: 13 tokens 4.1 and 6.2,
-  // 4864 10 and 14, 9728 13 and 16, 19456 20 and 20, 131072 120 and 80).
-  const bool lone = T <= 64 * GG_SMS && E > 64;
+  // 4864 10 and 14, 9728 13 and 16, 19456 20 and 20, 131072 120 and 80).  Groups that are
+  // not of whole vectors would have the general form instead, which is slower (255
+  // experts, 4864 tokens 30, eight lanes 16).
+  const bool lone = T <= 64 * GG_SMS && E > 64 && a.n % 4 == 0;
   if (topk <= 8 && E <= 256 && !lone && lanes > 0 && (!grouped || a.n % lanes == 0)) {
     a.per = grouped ? a.n / lanes : ceil_div(E, 8);
     a.div_per = ((1u << 20) + a.per - 1) / a.per;

@@ -110,10 +110,11 @@ __device__ __forceinline__ float column_sum(float* src, int ctas, int H, int col
   return s;
 }
 
-// Lets a kernel use `smem` bytes of shared memory on the current device.
-template <typename K>
-cudaError_t allow_smem(K kernel, int smem) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Lets a kernel use SMEM bytes of shared memory, once on each device.
+template <auto KERNEL, int SMEM>
+cudaError_t allow_smem(int device) {
+  static OncePerDevice once;
+  return once(device, [] { return cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); });
 }
 
 }  // namespace flux

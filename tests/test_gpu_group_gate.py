@@ -187,6 +187,27 @@ def test_two_groups_closer_than_fp32(E, groups, top):
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups", [(64, 8), (60, 5), (95, 5), (256, 8), (256, 4), (512, 16)])
+@pytest.mark.parametrize("scale", [1.0, 16.0])
+def test_two_sums_of_scores_closer_than_fp32(score, E, groups, scale):
+    # no bias: two groups' sums of two scores within some 2^-24 of each other, the last in and the first out
+    r = np.random.default_rng(E + groups)
+    n, T = E // groups, 400
+    logits = (r.standard_normal((T, E)) - 4.0).astype(np.float32)
+    a, b = r.permutation(groups)[:2]
+    f = (lambda x: np.exp(x)) if score == "softmax" else (lambda x: 1.0 / (1.0 + np.exp(-x)))
+    back = np.log if score == "softmax" else (lambda y: -np.log(1.0 / y - 1.0))
+    logits[:, a * n], logits[:, a * n + 1], logits[:, b * n + 1] = 0.5, 0.0, 0.25
+    x = np.float32(back(f(0.5) + f(0.0) - f(0.25)))
+    logits[:, b * n] = x + np.spacing(x) * r.integers(-6, 7, T).astype(np.float32)
+    if scale > 1.0:  # one group far above the others: their scores are small beside the sum
+        top = [g for g in range(groups) if g not in (a, b)][0]
+        logits[:, top * n] = scale
+    ids = Gate(T, E, 2, score, groups, 1 if scale == 1.0 else 2, 2, bias=None, logits=logits).check()
+    assert {a, b} <= set(np.unique(ids // n)) or scale > 1.0
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("bias", ["zero", "own", None])
 @pytest.mark.parametrize("groups,kept,top", [(1, 1, 1), (8, 2, 1), (8, 2, 2)])
 def test_equal_scores(score, bias, groups, kept, top):
