@@ -50,6 +50,8 @@ struct GroupGateArgs {
   int per;             // octet form: scores of a lane
   uint32_t div_per;    // ceil(2^20 / per)
   int vecs, trips, rivals;  // wide form: vectors of a lane; of a lane in its group; groups that a lane compares
+  int np;              // wide form: places of a group, n up to a multiple of four
+  uint32_t div_np;     // ceil(2^20 / np)
   uint32_t div_n;      // ceil(2^20 / n): e / n = e div_n >> 20 for e < 1024
   int row;             // values of a token's row in shared memory
   int softmax, renorm, accumulate;
@@ -174,23 +176,40 @@ __device__ __forceinline__ unsigned long long largest_of(uint32_t mask, unsigned
   return static_cast<unsigned long long>(hi) << 32 | lo;
 }
 
+// A softmax's sum in doubles, over the LANES lanes of a token; top, its largest logit, is
+// finite.  (All lanes of the warp take part.)
+template <int LANES>
+__device__ __noinline__ double softmax_total64(const float* row, int E, int l, float top) {
+  double total = 0.0;
+#pragma unroll 4
+  for (int e = l; e < E; e += LANES) {
+    const float x = load_global(row + e);
+    total += exp(static_cast<double>(x != x ? -INFINITY : x) - static_cast<double>(top));
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  return total;
+}
+
 // Two values in doubles, side by side: a dependent double operation takes some 100
-// cycles on this GPU.
-__device__ __noinline__ double2 biased_sigmoids64(float x, float x_bias, float y, float y_bias) {
-  const double u = -static_cast<double>(x != x ? -INFINITY : x), v = -static_cast<double>(y != y ? -INFINITY : y);
-  const double a = exp(u), b = exp(v);
-  return make_double2(1.0 / (1.0 + a) + static_cast<double>(x_bias), 1.0 / (1.0 + b) + static_cast<double>(y_bias));
+// cycles on this GPU.  (top and total: of a softmax)
+template <bool SOFT>
+__device__ __noinline__ double2 biased_scores64(float x, float x_bias, float y, float y_bias, float top, double total) {
+  const double p = static_cast<double>(x != x ? -INFINITY : x), q = static_cast<double>(y != y ? -INFINITY : y);
+  const double a = exp(SOFT ? p - static_cast<double>(top) : -p), b = exp(SOFT ? q - static_cast<double>(top) : -q);
+  const double s = SOFT ? a / total : 1.0 / (1.0 + a), t = SOFT ? b / total : 1.0 / (1.0 + b);
+  return make_double2(s + static_cast<double>(x_bias), t + static_cast<double>(y_bias));
 }
 
 // The order of a token's chosen experts, one to each of LANES lanes (those from topk on
 // have none), and of the one expert left out next to them (-1: none), by their doubles:
 // the place of the lane's own in x, of the one left out in y.  Takes 3 us, the choice in
 // full 12 to 20.
-template <int LANES>
-__device__ __noinline__ int2 order64(const float* row, const float* bias, int e, int out, int l, int topk) {
+template <int LANES, bool SOFT>
+__device__ __noinline__ int2 order64(const float* row, const float* bias, int e, int out, int l, int topk, float top, double total) {
   const bool here = l < topk;
   const int mine = here ? e : 0, f = out >= 0 ? out : 0;
-  const double2 d = biased_sigmoids64(load_global(row + mine), load_global(bias + mine), load_global(row + f), load_global(bias + f));
+  const double2 d = biased_scores64<SOFT>(load_global(row + mine), load_global(bias + mine), load_global(row + f), load_global(bias + f), top, total);
   auto first = [](double u, int i, double v, int k) { return u > v || (u == v && i < k); };
   int2 place = make_int2(out >= 0 && first(d.y, out, d.x, e), 0);
   for (int j = 0; j < topk; ++j) {
@@ -313,13 +332,15 @@ __device__ __noinline__ void choose64(const GroupGateArgs& a, const float* row, 
   }
 }
 
-// One token to LPT lanes, NC candidates each.  The lanes put the values into a row
-// of shared memory, rank the groups from there, and take their candidates (those
-// of the kept groups, in order) into registers for topk rounds of a maximum.
-template <int LPT, int NC>
-__global__ void __launch_bounds__(GG_THREADS, NC <= 8 ? 5 : 2)
+// One token of up to 64 experts to eight lanes, NC candidates each.  The lanes put the
+// values into a row of shared memory, rank the groups from there, and take their
+// candidates (those of the kept groups, in order) into registers for topk rounds of a
+// maximum.  For long batches of what the octet form does not take: 131072 tokens, 4 of 48
+// experts in 6 of 16 groups 82 us, a warp a token 108; 10 of 16 experts 31 and 55.
+template <int NC>
+__global__ void __launch_bounds__(GG_THREADS, 5)
 group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
-  constexpr int TPW = 32 / LPT;
+  constexpr int LPT = 8, TPW = 32 / LPT;
   extern __shared__ uint4 smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT, sub = lane / LPT;
   using O = Over<LPT>;
@@ -525,7 +546,8 @@ __host__ __device__ inline int wide_words(int vecs, int row, int topk, int lists
 // their way while this one's are at work.  The candidates (all experts, or the kept
 // groups') lie in LISTS sorted lists of four a lane, so that a round of the choice
 // is a maximum over the lists' heads and over the warp, and a shift of the winner's
-// list.
+// list.  Groups begin at multiples of four places; the places behind an odd group's last
+// expert hold -inf and are no candidates.
 //
 // Bound by the length of that chain: 13 tokens of 256 experts 2.9 us in a captured
 // graph, 4096 tokens 10 us with cold caches where a token of them needs doubles, 6 where
@@ -544,36 +566,52 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
   uint32_t* order = reinterpret_cast<uint32_t*>(list + LISTS * 32 * 5);
   const bool two = a.top == 2 && a.n > 1;
   const bool soft_row = SOFT && (BIASED || !a.renorm || (GROUPED && two));
-  // what lies past the last expert is -inf everywhere
-  for (int e = a.E + lane; e < wide; e += 32) raw2[e] = raw2[wide + e] = -INFINITY;
+  // experts and their places; a place that holds none is -inf everywhere
+  const int shift = a.np - a.n, places = a.G * a.np;
+  auto group_of = [&](int p) { return static_cast<int>((p * a.div_np) >> 20); };
+  auto place_of = [&](int e) { return e + static_cast<int>((e * a.div_n) >> 20) * shift; };
+  auto id_of = [&](int p) { return p - group_of(p) * shift; };
+  auto spot = [&](int p) { return a.pad == 0 ? p : p + group_of(p) * a.pad; };  // in val
+  auto kept_place = [&](int p) {  // of the kept groups' places in order
+    if (a.kept == a.G) return p;
+    const int q = group_of(p);
+    return kept[q] * a.np + (p - q * a.np);
+  };
+  const bool whole = a.E % 4 == 0 && shift == 0;  // rows are vectors, and groups too
+  for (int p = lane; p < wide; p += 32) {
+    if (p >= places || p - group_of(p) * a.np >= a.n) raw2[p] = raw2[wide + p] = -INFINITY;
+  }
   for (int q = 0; q < LISTS; ++q) list[(q * 32 + lane) * 5 + 4] = NAN;
   wait_for_previous();
   if constexpr (BIASED) {
-    for (int e = threadIdx.x; e < wide; e += GG_THREADS) bias[e] = e < a.E ? load_global(a.bias + e) : -INFINITY;
+    for (int p = threadIdx.x; p < wide; p += GG_THREADS)
+      bias[p] = p < places && p - group_of(p) * a.np < a.n ? load_global(a.bias + id_of(p)) : -INFINITY;
     __syncthreads();
   }
   auto fetch = [&](long long at, float* dst) {
     if (at < a.T) {
       const float* src = a.logits + static_cast<size_t>(at) * a.E;
+      if (whole) {
 #pragma unroll
-      for (int v = 0; v < vecs; ++v) {
-        const int e = v * 128 + lane * 4;
-        if (e < a.E) copy16_async(dst + e, src + e);
+        for (int v = 0; v < vecs; ++v) {
+          const int e = v * 128 + lane * 4;
+          if (e < a.E) copy16_async(dst + e, src + e);
+        }
+      } else {
+        for (int e = lane; e < a.E; e += 32) copy4_async(dst + place_of(e), src + e);
       }
     }
     copy_commit();
   };
-  // the CTA's warps go round together, the last time perhaps without a token
   const long long step = static_cast<long long>(gridDim.x) * GG_WARPS;
-  long long first = static_cast<long long>(blockIdx.x) * GG_WARPS;
-  fetch(first + warp, raw2);
-  for (int turn = 0; first < a.T; first += step, turn ^= 1) {
-    const bool token = first + warp < a.T;
-    const long long t = token ? first + warp : a.T - 1;
+  long long t = static_cast<long long>(blockIdx.x) * GG_WARPS + warp;
+  fetch(t, raw2);
+  for (int turn = 0; t < a.T; t += step, turn ^= 1) {
     float* raw = raw2 + turn * wide;
     __syncwarp();  // the other row's readers are done
-    fetch(first + warp + step, raw2 + (turn ^ 1) * wide);
+    fetch(t + step, raw2 + (turn ^ 1) * wide);
     copy_wait<1>();
+    if (!whole) __syncwarp();  // (vectors are read by the lanes that copied them)
     auto four = [&](int e) {
       float4 x = *reinterpret_cast<const float4*>(raw + e);
       x.x = fmaxf(x.x, -INFINITY), x.y = fmaxf(x.y, -INFINITY), x.z = fmaxf(x.z, -INFINITY), x.w = fmaxf(x.w, -INFINITY);
@@ -615,18 +653,18 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
 #pragma unroll 2
       for (int v = 0; v < vecs; ++v) {
         const int e = v * 128 + lane * 4;
-        *reinterpret_cast<float4*>(val + e + group_of(a, e) * a.pad) = values(e);
+        *reinterpret_cast<float4*>(val + spot(e)) = values(e);
       }
       __syncwarp();
       // lpg lanes a group
       const int g = lane >> a.log_lpg, sub = lane & (a.lpg - 1);
       float m1 = -INFINITY, m2 = -INFINITY;
-      const float* mine = val + g * (a.n + a.pad);
+      const float* mine = val + g * (a.np + a.pad);
 #pragma unroll 2
       for (int k = 0; k < a.trips; ++k) {
         const int i = (k * a.lpg + sub) * 4;
         float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (g < a.G && i < a.n) q = *reinterpret_cast<const float4*>(mine + i);
+        if (g < a.G && i < a.np) q = *reinterpret_cast<const float4*>(mine + i);
         const float p = fmaxf(q.x, q.y), s = fminf(q.x, q.y), u = fmaxf(q.z, q.w), w = fminf(q.z, q.w);
         m2 = fmaxf(fmaxf(m2, fminf(m1, fmaxf(p, u))), fmaxf(fminf(p, u), fmaxf(s, w)));
         m1 = fmaxf(m1, fmaxf(p, u));
@@ -636,6 +674,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
         m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
         m1 = fmaxf(m1, o1);
       }
+      const float x1 = m1, x2 = m2;  // (logits without a bias)
       if (!two) m2 = 0.0f;
       else if (!BIASED) m1 = score(m1), m2 = score(m2);
       // the groups before this one in the order, counted by its lanes
@@ -653,11 +692,14 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
         const float last = -warp_largest(in ? -rank : NAN), next = warp_largest(in || g >= a.G ? NAN : rank);
         const float room = 2.0f * unsure + 0x1p-21f * warp_largest(big);
         doubt = !ranks_apart(last, next, room);
-        if constexpr (BIASED && !SOFT) {
-          // Groups next to the border: their ranks in doubles, from their two largest values
-          // (unless a third is next to the second) or their largest, wherever they lie.
-          if (doubt) {
-            const bool near = g < a.G && (room == INFINITY || (in ? rank - next <= room : last - rank <= room));
+        // Groups next to the border: their ranks in doubles, from their two largest values
+        // (unless a third is next to the second) or their largest, wherever they lie.
+        if (doubt && !(SOFT && isinf(top))) {
+          const double sum = SOFT ? softmax_total64<32>(a.logits + static_cast<size_t>(t) * a.E, a.E, lane, top) : 0.0;
+          const bool near = g < a.G && (room == INFINITY || (in ? rank - next <= room : last - rank <= room));
+          bool told = near;
+          double exact;
+          if constexpr (BIASED) {
             const float least = (two ? m2 : m1) - room;
             int count = 0, e = 0, f = 0;
             if (near) {
@@ -667,26 +709,29 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
                   if (mine[j] < least) continue;
                   ++count;
                   f = e;
-                  e = g * a.n + j;
+                  e = g * a.np + j;
                 }
               }
             }
             int all = count;
             for (int o = a.lpg >> 1; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-            const bool told = near && all == (two ? 2 : 1);
-            const double2 d = biased_sigmoids64(raw[e], bias[e], raw[f], bias[f]);
-            double exact = (count > 0 ? d.x : 0.0) + (count > 1 ? d.y : 0.0);
+            told = near && all == (two ? 2 : 1);
+            const double2 d = biased_scores64<SOFT>(raw[e], bias[e], raw[f], bias[f], top, sum);
+            exact = (count > 0 ? d.x : 0.0) + (count > 1 ? d.y : 0.0);
             for (int o = a.lpg >> 1; o > 0; o >>= 1) exact += __shfl_xor_sync(0xFFFFFFFFu, exact, o);
-            exact = told ? fmax(exact, static_cast<double>(-INFINITY)) : rank;
-            int ahead = 0;
-            for (int o = 0; o < a.G; ++o) {
-              const double other = __shfl_sync(0xFFFFFFFFu, exact, o << a.log_lpg);
-              ahead += other > exact || (other == exact && o < g);
-            }
-            if (!__any_sync(0xFFFFFFFFu, near && !told)) {
-              in = g < a.G && ahead < a.kept;
-              doubt = false;
-            }
+          } else {
+            const double2 d = biased_scores64<SOFT>(x1, 0.0f, x2, 0.0f, top, sum);
+            exact = d.x + d.y;
+          }
+          exact = told ? fmax(exact, static_cast<double>(-INFINITY)) : rank;
+          int ahead = 0;
+          for (int o = 0; o < a.G; ++o) {
+            const double other = __shfl_sync(0xFFFFFFFFu, exact, o << a.log_lpg);
+            ahead += other > exact || (other == exact && o < g);
+          }
+          if (!__any_sync(0xFFFFFFFFu, near && !told)) {
+            in = g < a.G && ahead < a.kept;
+            doubt = false;
           }
         }
       }
@@ -696,7 +741,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
     }
     // lists of four, largest first, equal ones in order; their numbers in the bytes of a
     // word, and a NaN at their end
-    const int count = a.kept * a.n;
+    const int count = a.kept * a.np;
     float h[LISTS];  // the heads
     int at[LISTS];   // and their places
 #pragma unroll
@@ -705,18 +750,23 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
       float4 x = make_float4(NAN, NAN, NAN, NAN);
       if constexpr (GROUPED) {
         if (p < count) {
-          const int g = group_of(a, p);
-          x = *reinterpret_cast<const float4*>(val + kept[g] * (a.n + a.pad) + (p - g * a.n));
+          const int g = group_of(p);
+          x = *reinterpret_cast<const float4*>(val + kept[g] * (a.np + a.pad) + (p - g * a.np));
         }
       } else if (q < vecs) {
         const float4 y = values(p);
         if (p < count) x = y;
       }
       float v[4] = {x.x, x.y, x.z, x.w};
+      if (shift != 0) {
+        const int left = a.n - (p - group_of(p) * a.np);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < left ? v[i] : NAN;
+      }
       uint32_t id[4] = {0, 1, 2, 3};
       auto sort2 = [&](int i) {  // neighbours, if out of order: equal ones stay in theirs
         const bool swap = v[i] < v[i + 1];
-        const float hi = fmaxf(v[i], v[i + 1]), lo = fminf(v[i], v[i + 1]);
+        const float hi = swap ? v[i + 1] : v[i], lo = swap ? v[i] : v[i + 1];
         const uint32_t first = swap ? id[i + 1] : id[i], second = swap ? id[i] : id[i + 1];
         v[i] = hi, v[i + 1] = lo, id[i] = first, id[i + 1] = second;
       };
@@ -783,7 +833,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
     }
     __syncwarp();
     const bool few = a.topk <= 32;
-    auto expert = [&](int p) { return GROUPED ? expert_at(a, kept, p) : p; };
+    auto expert = [&](int p) { return GROUPED ? kept_place(p) : p; };  // (its place)
     int own = few && lane < a.topk ? candidate(pick[lane]) : 0;
     if (!few) {
       for (int j = lane; j < a.topk; j += 32) pick[j] = candidate(pick[j]);
@@ -792,7 +842,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
     own = expert(own);
     if constexpr (BIASED) {
       const float next = warp_largest(head());  // the best one left, NaN if none is
-      auto value = [&](int e) { return GROUPED ? val[place(a, e)] : score(fmaxf(raw[e], -INFINITY)) + bias[e]; };
+      auto value = [&](int e) { return GROUPED ? val[spot(e)] : score(fmaxf(raw[e], -INFINITY)) + bias[e]; };
       auto apart = [&](float hi, float lo) { return hi - lo > unsure + 0x1p-23f * (fabsf(hi) + fabsf(lo)); };
       bool close = false;
       if (few) {
@@ -834,10 +884,12 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
         out = __reduce_min_sync(0xFFFFFFFFu, out);
         equal = __reduce_add_sync(0xFFFFFFFFu, equal);
         unsorted = __any_sync(0xFFFFFFFFu, unsorted) || others > 0u;
-        if (unsorted && !SOFT && few && others <= 1u && equal == 0u) {
+        if (unsorted && !(SOFT && isinf(top)) && few && others <= 1u && equal == 0u) {
           // two neighbours, or the last one in and the first one out: by their doubles alone
           const int f = others == 1u ? static_cast<int>(out) : -1;
-          const int2 place = order64<32>(a.logits + static_cast<size_t>(t) * a.E, a.bias, own, f, lane, a.topk);
+          const float* row = a.logits + static_cast<size_t>(t) * a.E;
+          const double sum = SOFT ? softmax_total64<32>(row, a.E, lane, top) : 0.0;
+          const int2 place = order64<32, SOFT>(row, a.bias, id_of(own), f < 0 ? f : id_of(f), lane, a.topk, top, sum);
           __syncwarp();
           if (lane < a.topk && place.x < a.topk) pick[place.x] = own;
           if (lane == 0 && f >= 0 && place.y < a.topk) pick[place.y] = f;
@@ -850,7 +902,13 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
     }
     if ((BIASED || GROUPED) && __any_sync(0xFFFFFFFFu, doubt)) {
       choose64<32>(a, a.logits + static_cast<size_t>(t) * a.E, kept, pick, lane, 0xFFFFFFFFu);
-      if (few && lane < a.topk) own = expert(pick[lane]);
+      auto chosen = [&](int j) { return place_of(expert_at(a, kept, pick[j])); };
+      if (few) {
+        if (lane < a.topk) own = chosen(lane);
+      } else {  // as places among the kept groups' again
+        for (int j = lane; j < a.topk; j += 32) pick[j] = place_of(pick[j]);
+        __syncwarp();
+      }
     }
     // The weights, with the rules of group_gate_kernel.  rcp: to one unit in the last
     // place, where a rounded quotient costs eight times as much.
@@ -875,8 +933,8 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
       float w = weight(x);
       w = here ? w : 0.0f;
       const float sum = a.renorm ? warp_sum(w) : total;
-      if (here && token) {
-        ids[lane] = own;
+      if (here) {
+        ids[lane] = id_of(own);
         weights[lane] = a.scale * w * rcp(sum);
       }
     } else {
@@ -889,9 +947,9 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
         for (int j = lane; j < a.topk; j += 32) sum += weight(logit(expert(pick[j])));
         sum = warp_sum(sum);
       }
-      for (int j = lane; token && j < a.topk; j += 32) {
+      for (int j = lane; j < a.topk; j += 32) {
         const int e = expert(pick[j]);
-        ids[j] = e;
+        ids[j] = id_of(e);
         weights[j] = a.scale * weight(logit(e)) * rcp(sum);
       }
     }
@@ -1017,6 +1075,7 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
         m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
         m1 = fmaxf(m1, o1);
       }
+      const float x1 = m1, x2 = m2;  // (logits without a bias)
       if (!two) m2 = 0.0f;
       else if (!BIASED) m1 = score(m1), m2 = score(m2);
       // lanes of groups before this one in the order
@@ -1034,33 +1093,44 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
         const float last = -O::maxf(in ? -rank : -INFINITY), next = O::maxf(in ? -INFINITY : rank);
         const float room = 2.0f * unsure + 0x1p-21f * O::maxf(big);
         doubt = !ranks_apart(last, next, room);
-        if constexpr (BIASED && !SOFT) {
-          // Groups next to the border, where a group is one lane: their ranks in doubles, from
-          // their two largest values (unless a third is next to the second) or their largest.
-          if (lpg == 1 && __any_sync(0xFFFFFFFFu, doubt)) {
-            const bool near = doubt && (room == INFINITY || (in ? rank - next <= room : last - rank <= room));
+        // Groups next to the border: as in group_gate_wide_kernel.
+        const bool here = doubt && !(SOFT && isinf(top));
+        if (__any_sync(0xFFFFFFFFu, here)) {
+          const double sum = SOFT ? softmax_total64<8>(row, a.E, l, top) : 0.0;
+          const bool near = here && (room == INFINITY || (in ? rank - next <= room : last - rank <= room));
+          bool told = near;
+          double exact;
+          if constexpr (BIASED) {
             const float least = (two ? m2 : m1) - room;
             int count = 0, places = 0;
 #pragma unroll
             for (int k = 0; k < P; ++k) {
-              const bool one = (full || k < mine) && c[k] >= least;
+              const bool one = near && (full || k < mine) && c[k] >= least;
               count += one;
               places = one ? places << 8 | k : places;
             }
-            const bool told = near && count == (two ? 2 : 1);
-            const int e = told ? l * a.per + (places & 255) : 0, f = told && two ? l * a.per + (places >> 8 & 255) : 0;
-            const double2 d = biased_sigmoids64(load_global(row + e), load_global(a.bias + e), load_global(row + f), load_global(a.bias + f));
-            const double exact = !told ? rank : two ? fmax(d.x + d.y, static_cast<double>(-INFINITY)) : d.x;
-            int ahead = 0;
+            int all = count;
+            for (int o = lpg >> 1; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+            told = near && all == (two ? 2 : 1);
+            const int e = count > 0 ? l * a.per + (places & 255) : 0, f = count > 1 ? l * a.per + (places >> 8 & 255) : 0;
+            const double2 d = biased_scores64<SOFT>(load_global(row + e), load_global(a.bias + e), load_global(row + f), load_global(a.bias + f), top, sum);
+            exact = (count > 0 ? d.x : 0.0) + (count > 1 ? d.y : 0.0);
+            for (int o = lpg >> 1; o > 0; o >>= 1) exact += __shfl_xor_sync(0xFFFFFFFFu, exact, o);
+          } else {
+            const double2 d = biased_scores64<SOFT>(x1, 0.0f, x2, 0.0f, top, sum);
+            exact = d.x + d.y;
+          }
+          exact = told ? fmax(exact, static_cast<double>(-INFINITY)) : rank;
+          int ahead = 0;  // lanes of groups
 #pragma unroll
-            for (int k = 1; k < 8; ++k) {
-              const double other = __shfl_xor_sync(0xFFFFFFFFu, exact, k);
-              ahead += other > exact || (other == exact && (l ^ k) < l);
-            }
-            if (O::any(near && !told) == 0u && doubt) {
-              in = ahead < a.kept;
-              doubt = false;
-            }
+          for (int k = 1; k < 8; ++k) {
+            const double other = __shfl_xor_sync(0xFFFFFFFFu, exact, k);
+            const int g = (l ^ k) >> a.log_lpg;
+            ahead += g != group && (other > exact || (other == exact && g < group));
+          }
+          if (O::any(near && !told) == 0u && here) {
+            in = ahead < a.kept * lpg;
+            doubt = false;
           }
         }
       }
@@ -1186,13 +1256,15 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
         out = O::min(out);
         equal = O::any(equal);
         unsorted = O::any(unsorted || others > 0u) != 0u;
-        if (SOFT || others > 1u || equal != 0u) doubt |= unsorted;
+        const bool full_choice = (SOFT && isinf(top)) || others > 1u || equal != 0u;
+        if (full_choice) doubt |= unsorted;
         // Mostly it is two neighbours, or the last one in and the first one out: their order
         // is told by the doubles of these nine alone.
-        const bool nine = unsorted && !SOFT && others <= 1u && equal == 0u;
+        const bool nine = unsorted && !full_choice;
         if (__any_sync(0xFFFFFFFFu, nine)) {
           const int f = others == 1u ? static_cast<int>(out) : -1;
-          const int2 place = order64<8>(row, a.bias, e, f, l, a.topk);
+          const double sum = SOFT ? softmax_total64<8>(row, a.E, l, top) : 0.0;
+          const int2 place = order64<8, SOFT>(row, a.bias, e, f, l, a.topk, top, sum);
           __syncwarp();
           if (nine && here && place.x < a.topk) pick[place.x] = e;
           if (nine && l == 0 && f >= 0 && place.y < a.topk) pick[place.y] = f;
@@ -1424,17 +1496,17 @@ flux_status_t check_gate(int T, int E, int topk, int score, float scale, const f
   return aligned16(logits) ? FLUX_OK : FLUX_ERR_UNSUPPORTED;
 }
 
-template <int LPT, int NC>
+template <int NC>
 flux_status_t launch_gate(const GroupGateArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  constexpr int TPC = GG_WARPS * (32 / LPT);
-  constexpr auto kernel = group_gate_kernel<LPT, NC>;
+  constexpr int TPC = GG_WARPS * 4;
+  constexpr auto kernel = group_gate_kernel<NC>;
   const size_t smem = TPC * gate_token_bytes(a.row, a.topk);
   static OncePerDevice once;
   const cudaError_t attr = once(dev.device, [&dev] {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dev.max_smem_optin));
   });
   if (attr != cudaSuccess) return cuda_fail(attr);
-  const int per_sm = static_cast<int>(std::max<size_t>(1, std::min<size_t>(NC <= 8 ? 5 : 2, (227u << 10) / (smem + 1024))));
+  const int per_sm = static_cast<int>(std::max<size_t>(1, std::min<size_t>(5, (227u << 10) / (smem + 1024))));
   const int grid = std::min(ceil_div(a.T, TPC), GG_SMS * per_sm);
   const cudaError_t e = launch_behind(kernel, dim3(grid), GG_THREADS, smem, s, a);
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e);
@@ -1464,7 +1536,7 @@ flux_status_t launch_wide(const GroupGateArgs& a, const DeviceInfo& dev, cudaStr
 // Rows of up to 256 experts have their loops unrolled.
 template <bool GROUPED>
 flux_status_t launch_wide(const GroupGateArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-  const int lists = ceil_div(a.kept * a.n, 128);
+  const int lists = ceil_div(a.kept * a.np, 128);
   if (a.vecs == 1) return launch_wide<1, 1, GROUPED>(a, dev, s);
   if (a.vecs == 2 && lists == 2) return launch_wide<2, 2, GROUPED>(a, dev, s);
   if constexpr (GROUPED) {
@@ -1473,7 +1545,8 @@ flux_status_t launch_wide(const GroupGateArgs& a, const DeviceInfo& dev, cudaStr
     if (lists == 2) return launch_wide<0, 2, true>(a, dev, s);
   }
   if (lists <= 4) return launch_wide<0, 4, GROUPED>(a, dev, s);
-  return launch_wide<0, 8, GROUPED>(a, dev, s);
+  if (lists <= 8) return launch_wide<0, 8, GROUPED>(a, dev, s);
+  return launch_wide<0, 9, GROUPED>(a, dev, s);  // more than 1024 places
 }
 
 template <int P, bool SOFT, bool BIASED>
@@ -1552,10 +1625,10 @@ extern "C" flux_status_t flux_moe_group_gate(int T, int E, int topk, int score, 
   a.T = T;
   a.E = E;
   a.topk = topk;
-  a.G = groups;
-  a.kept = topk_groups;
+  a.G = topk_groups < groups ? groups : 1;  // where all are kept there might as well be one
+  a.kept = topk_groups < groups ? topk_groups : 1;
   a.top = group_top;
-  a.n = E / groups;
+  a.n = E / a.G;
   a.div_n = ((1u << 20) + a.n - 1) / a.n;
   a.softmax = score == FLUX_SCORE_SOFTMAX;
   a.renorm = renorm != 0;
@@ -1565,46 +1638,42 @@ extern "C" flux_status_t flux_moe_group_gate(int T, int E, int topk, int score, 
   const int lanes = !grouped ? 8 : groups <= 8 && 8 % groups == 0 ? 8 / groups : 0;  // of a group
   // A warp a token is faster while a warp has at most two or three of them (256 experts, 8
   // groups, us with cold caches, a warp a token and eight lanes: 13 tokens 4.1 and 6.2,
-  // 4864 10 and 14, 9728 13 and 16, 19456 20 and 20, 131072 120 and 80).  Groups that are
-  // not of whole vectors would have the general form instead, which is slower (255
-  // experts, 4864 tokens 30, eight lanes 16).
-  const bool lone = T <= 64 * GG_SMS && E > 64 && a.n % 4 == 0;
+  // 4864 10 and 14, 9728 13 and 16, 19456 20 and 20, 131072 120 and 80).
+  const bool lone = T <= 64 * GG_SMS && E > 64;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (topk <= 8 && E <= 256 && !lone && lanes > 0 && (!grouped || a.n % lanes == 0)) {
     a.per = grouped ? a.n / lanes : ceil_div(E, 8);
     a.div_per = ((1u << 20) + a.per - 1) / a.per;
     while (grouped && 1 << a.log_lpg < lanes) ++a.log_lpg;
     a.vecs = a.per % 4 == 0 && E % 4 == 0;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.per <= 4) return launch_octet<4>(a, dev, s);
     if (a.per <= 8) return launch_octet<8>(a, dev, s);
     if (a.per <= 16) return launch_octet<16>(a, dev, s);
     return launch_octet<32>(a, dev, s);
   }
-  const int lpt = E <= 64 ? 8 : 32;
+  const bool wide = E > 64 || T <= 64 * GG_SMS;
+  const int lpt = wide ? 32 : 8;
   a.lpg = lpt;  // lanes of a group: as many as let all groups be ranked at once, at least one
-  while (a.lpg > 1 && a.lpg * groups > lpt) a.lpg /= 2;
+  while (a.lpg > 1 && a.lpg * a.G > lpt) a.lpg /= 2;
   while (1 << a.log_lpg < a.lpg) ++a.log_lpg;
-  const bool wide = lpt == 32 && a.n % 4 == 0;
-  // words between the groups' rows: lanes of neighbouring groups read other banks
-  a.pad = !grouped ? 0 : !wide ? a.lpg : a.lpg >= 8 ? 0 : (4 * a.lpg - a.n % 32 + 32) % 32;
-  a.vecs = ceil_div(E, 128);
-  a.trips = ceil_div(a.n, 4 * a.lpg);
-  a.rivals = ceil_div(groups, a.lpg);
-  // (the wide form has values past the last expert too)
-  a.row = !wide ? E + groups * a.pad : !grouped ? 0 : 128 * a.vecs + (128 * a.vecs - 4) / a.n * a.pad;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (wide) return grouped ? launch_wide<true>(a, dev, s) : launch_wide<false>(a, dev, s);
-  const int each = ceil_div(topk_groups * a.n, lpt);  // candidates of a lane
-  if (lpt == 8) {
-    if (each <= 1) return launch_gate<8, 1>(a, dev, s);
-    if (each <= 2) return launch_gate<8, 2>(a, dev, s);
-    if (each <= 4) return launch_gate<8, 4>(a, dev, s);
-    return launch_gate<8, 8>(a, dev, s);
+  if (!wide) {
+    // (pad: words between the groups' rows, so that lanes of neighbouring groups read other banks)
+    a.pad = grouped ? a.lpg : 0;
+    a.row = E + a.G * a.pad;
+    const int each = ceil_div(a.kept * a.n, lpt);  // candidates of a lane
+    if (each <= 1) return launch_gate<1>(a, dev, s);
+    if (each <= 2) return launch_gate<2>(a, dev, s);
+    if (each <= 4) return launch_gate<4>(a, dev, s);
+    return launch_gate<8>(a, dev, s);
   }
-  if (each <= 4) return launch_gate<32, 4>(a, dev, s);
-  if (each <= 8) return launch_gate<32, 8>(a, dev, s);
-  if (each <= 16) return launch_gate<32, 16>(a, dev, s);
-  return launch_gate<32, 32>(a, dev, s);
+  a.np = (a.n + 3) / 4 * 4;
+  a.div_np = ((1u << 20) + a.np - 1) / a.np;
+  a.pad = !grouped || a.lpg >= 8 ? 0 : (4 * a.lpg - a.np % 32 + 32) % 32;
+  a.vecs = ceil_div(a.G * a.np, 128);
+  a.trips = ceil_div(a.np, 4 * a.lpg);
+  a.rivals = ceil_div(a.G, a.lpg);
+  a.row = !grouped ? 0 : 128 * a.vecs + (128 * a.vecs - 4) / a.np * a.pad;  // values of every place
+  return grouped ? launch_wide<true>(a, dev, s) : launch_wide<false>(a, dev, s);
 }
 
 extern "C" flux_status_t flux_moe_group_gate_bwd(int T, int E, int topk, int score, int renorm, float scale,

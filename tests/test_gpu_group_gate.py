@@ -50,7 +50,7 @@ class Gate:
 
     def check_many(self, want_ids, want_w, depth):
         """The same tokens over and over: past 9728 of them a warp takes four at once."""
-        if self.E <= 64 or self.T > 9728:
+        if self.T > 9728:
             return
         times = 9800 // self.T + 1
         ids = torch.full((times * self.T * self.k,), -7, dtype=torch.int32, device="cuda")
@@ -77,6 +77,16 @@ CASES = [
     (41, 96, 4, "sigmoid", 32, 7, 2, True, 1.0, True),      # more groups than lanes of a token... of 64 experts
     (19, 64, 4, "sigmoid", 32, 9, 2, True, 1.0, True),
     (29, 1024, 16, "sigmoid", 16, 16, 1, True, 1.0, True),
+    (29, 1020, 9, "sigmoid", 30, 29, 2, True, 1.0, True),   # groups of 34: more than 1024 places
+    (29, 1023, 40, "softmax", 31, 31, 1, False, 1.0, True),
+    (29, 1023, 33, "softmax", 31, 30, 2, True, 1.0, False),
+    (29, 999, 12, "sigmoid", 27, 5, 2, True, 1.0, True),
+    (9800, 48, 4, "sigmoid", 16, 6, 2, True, 1.0, True),    # long batches of few experts
+    (9800, 60, 5, "softmax", 5, 2, 2, True, 1.0, True),
+    (9800, 16, 10, "softmax", 1, 1, 1, False, 1.0, False),
+    (9800, 64, 33, "sigmoid", 32, 21, 1, True, 1.0, True),
+    (9800, 7, 3, "sigmoid", 7, 5, 2, True, 1.0, True),
+    (9800, 24, 4, "softmax", 8, 3, 2, False, 1.0, True),
     (29, 1024, 40, "softmax", 32, 11, 2, False, 1.0, True),
     (64, 1021, 33, "softmax", 1, 1, 1, True, 1.0, True),    # prime
     (300, 384, 8, "sigmoid", 1, 1, 1, True, 2.5, True),
