@@ -25,7 +25,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 CHECKED_LIB_PATH = os.path.join(HERE, "libflux_gb300_checked.so")
 
 SOURCES = ["flux_core.cu", "flux_dense.cu", "flux_moe.cu", "flux_noalloc.cu", "flux_tune.cu", "flux_block.cu",
-           "flux_router.cu", "flux_w4.cu", "flux_layer.cu", "flux_gate.cu", "flux_q8.cu", "flux_q8_gemm.cu"]
+           "flux_router.cu", "flux_w4.cu", "flux_layer.cu", "flux_gate.cu", "flux_gate_wide.cu", "flux_q8.cu", "flux_q8_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
           "-diag-suppress", "550", "-Xptxas", "-v"]
