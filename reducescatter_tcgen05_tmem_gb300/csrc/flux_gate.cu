@@ -232,6 +232,29 @@ __host__ __device__ constexpr int octet_pitch() {
 }
 __host__ __device__ inline int octet_words(int pitch) { return 32 * pitch + 4 * 8 + 8 + 32; }
 
+// A group's rank in doubles, from its values from `least` on (x), of which there are y;
+// the lanes of the group, lpg, have `mine` logits and biases each.  (Not inline: few
+// tokens come here, and the others need not step over it.)
+template <bool SOFT>
+__device__ __noinline__ double2 group_rank64(const float* logit, const float* bias, int mine, float least, int lpg, float top, float inv, double sum) {
+  int count = 0, e = 0, f = 0;
+  for (int k = 0; k < mine; ++k) {
+    const float x = fmaxf(logit[k], -INFINITY);
+    const float c = (SOFT ? ex2((x - top) * G_LOG2E) * inv : rcp(1.0f + ex2(-x * G_LOG2E))) + bias[k];
+    if (c < least) continue;
+    ++count;
+    f = e;
+    e = k;
+  }
+  const double2 d = biased_scores64<SOFT>(logit[e], bias[e], logit[f], bias[f], top, sum);
+  double exact = (count > 0 ? d.x : 0.0) + (count > 1 ? d.y : 0.0);
+  for (int o = lpg >> 1; o > 0; o >>= 1) {
+    count += __shfl_xor_sync(0xFFFFFFFFu, count, o);
+    exact += __shfl_xor_sync(0xFFFFFFFFu, exact, o);
+  }
+  return make_double2(exact, count);
+}
+
 // Four tokens to a warp: a token's scores lie in neighbouring order in eight lanes, P
 // at most in each, so that a group is one lane (or 2, 4 or 8) and most of the work is
 // in the lanes' own registers.  Lists and rounds as in group_gate_wide_kernel.
@@ -367,21 +390,10 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
           bool told = near;
           double exact;
           if constexpr (BIASED) {
-            const float least = (two ? m2 : m1) - room;
-            int count = 0, places = 0;
-#pragma unroll
-            for (int k = 0; k < P; ++k) {
-              const bool one = near && (full || k < mine) && c[k] >= least;
-              count += one;
-              places = one ? places << 8 | k : places;
-            }
-            int all = count;
-            for (int o = lpg >> 1; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-            told = near && all == (two ? 2 : 1);
-            const int e = count > 0 ? l * a.per + (places & 255) : 0, f = count > 1 ? l * a.per + (places >> 8 & 255) : 0;
-            const double2 d = biased_scores64<SOFT>(load_global(row + e), load_global(a.bias + e), load_global(row + f), load_global(a.bias + f), top, sum);
-            exact = (count > 0 ? d.x : 0.0) + (count > 1 ? d.y : 0.0);
-            for (int o = lpg >> 1; o > 0; o >>= 1) exact += __shfl_xor_sync(0xFFFFFFFFu, exact, o);
+            const int need = two ? 2 : 1;
+            const double2 d = group_rank64<SOFT>(own, bias + l * (P + 4), near ? mine : 0, (two ? m2 : m1) - room, lpg, top, inv, sum);
+            told = near && d.y == need;
+            exact = d.x;
           } else {
             const double2 d = biased_scores64<SOFT>(x1, 0.0f, x2, 0.0f, top, sum);
             exact = d.x + d.y;
