@@ -449,10 +449,11 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
       return of * a.per + q * 4 + static_cast<int>(order >> (in_lane - q * 6) * 8 & 3u);
     };
     float value = NAN;  // of the choice that this lane stands for
+    float best = NAN;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (j >= a.topk) break;
-      const float best = head();
+      best = head();
       value = l == j ? best : value;
 #pragma unroll
       for (int q = 0; q < LISTS; ++q) {
@@ -468,7 +469,9 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
     taken += __shfl_xor_sync(0xFFFFFFFFu, taken, 1);
     taken += __shfl_xor_sync(0xFFFFFFFFu, taken, 2);
     taken += __shfl_xor_sync(0xFFFFFFFFu, taken, 4);
-    if (__any_sync(0xFFFFFFFFu, taken != a.topk)) {
+    // (as many taken as rounds, and none left for the last one: several in one round, where
+    // every candidate is chosen)
+    if (__any_sync(0xFFFFFFFFu, taken != a.topk || best != best)) {
       // several lists had the largest: the rounds again, the first expert takes it
       __syncwarp();
 #pragma unroll
@@ -477,7 +480,7 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
         h[q] = in ? own[q * 6] : NAN;
       }
       for (int j = 0; j < a.topk; ++j) {
-        const float best = head();
+        best = head();
         value = l == j ? best : value;
         uint32_t of = 0xFFFFFFFFu;
 #pragma unroll

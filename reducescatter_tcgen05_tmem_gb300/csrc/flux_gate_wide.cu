@@ -261,12 +261,14 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
     };
     // One round after the other.  Where the largest is in several lists, the one with the
     // first expert has it.  To see that costs half a round, so all of them take it; more
-    // taken than rounds tell, and the rounds are gone through again with care.
+    // taken than rounds tell, or (where every candidate is chosen) a last round that found
+    // none, and the rounds are gone through again with care.
+    float best = NAN;
     for (int j0 = 0; j0 < a.topk; j0 += 8) {
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         if (j0 + u >= a.topk) break;
-        const float best = warp_largest(head());
+        best = warp_largest(head());
 #pragma unroll
         for (int q = 0; q < LISTS; ++q) {
           if (h[q] == best) {
@@ -279,7 +281,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
     int taken = 0;
 #pragma unroll
     for (int q = 0; q < LISTS; ++q) taken += at[q] - (q * 32 + lane) * 5;
-    if (__reduce_add_sync(0xFFFFFFFFu, taken) != a.topk) {
+    if (__reduce_add_sync(0xFFFFFFFFu, taken) != a.topk || best != best) {
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < LISTS; ++q) {
@@ -287,7 +289,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
         h[q] = list[at[q]];
       }
       for (int j = 0; j < a.topk; ++j) {
-        const float best = warp_largest(head());
+        best = warp_largest(head());
         uint32_t first = 0xFFFFFFFFu;
 #pragma unroll
         for (int q = LISTS - 1; q >= 0; --q)
