@@ -96,7 +96,7 @@ def group_gate(logits, bias, topk, score, groups, kept, top, renorm, scale):
     n = E // groups
     z = np.where(np.isnan(logits), -np.inf, logits).astype(np.float64)
     s = gate_scores(logits, score)
-    c = z if bias is None else s + bias[None, :]
+    c = z if bias is None else s + np.where(np.isnan(bias), -np.inf, bias)[None, :]
     ids = np.empty((T, topk), np.int32)
     weights = np.empty((T, topk))
     for t in range(T):

@@ -75,7 +75,7 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
       if (biased) {
         auto third = [&](int e) {
           const int at = place(a, e);
-          r.val[at] = fmaxf(r.val[at] * inv + load_global(a.bias + e), -INFINITY);
+          r.val[at] = r.val[at] * inv + bias_of(a.bias, e);
         };
         if (a.E % 4 == 0) {
           for (int e = l * 4; e < a.E; e += LPT * 4) third(e), third(e + 1), third(e + 2), third(e + 3);
@@ -85,7 +85,7 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
       }
     } else {
       each_logit<LPT>(row, a.E, l, [&](int e, float x) {
-        r.val[place(a, e)] = biased ? fmaxf(score(x) + load_global(a.bias + e), -INFINITY) : x;
+        r.val[place(a, e)] = biased ? score(x) + bias_of(a.bias, e) : x;
       });
     }
     __syncwarp();
@@ -174,7 +174,7 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
     auto expert = [&](int j) { return expert_at(a, r.kept, r.pick[j]); };
     if (biased) {
       auto apart = [&](float hi, float lo) { return hi - lo > unsure + 0x1p-23f * (fabsf(hi) + fabsf(lo)); };
-      auto same = [&](int e, int f) { return load_global(row + e) == load_global(row + f) && load_global(a.bias + e) == load_global(a.bias + f); };
+      auto same = [&](int e, int f) { return load_global(row + e) == load_global(row + f) && bias_of(a.bias, e) == bias_of(a.bias, f); };
       const float last = r.val[place(a, expert(a.topk - 1))];
       uint32_t close = m != 0u && !apart(last, value_of(m));
       for (int j = l; j + 1 < a.topk; j += LPT) close |= !apart(r.val[place(a, expert(j))], r.val[place(a, expert(j + 1))]);
@@ -283,7 +283,7 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
   if constexpr (BIASED) {
     for (int i = threadIdx.x; i < 8 * (P + 4); i += GG_THREADS) {
       const int b = i / (P + 4), k = i - b * (P + 4), e = b * a.per + k;
-      bias[i] = k < a.per && e < a.E ? load_global(a.bias + e) : -INFINITY;
+      bias[i] = k < a.per && e < a.E ? bias_of(a.bias, e) : -INFINITY;
     }
     __syncthreads();
   }
@@ -508,7 +508,7 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
       next = O::maxf(next);  // the best one left, NaN if none is
       auto apart = [&](float hi, float lo) { return hi - lo > unsure + 0x1p-23f * (fabsf(hi) + fabsf(lo)); };
       auto same = [&](int f, int g) {
-        return load_global(row + f) == load_global(row + g) && load_global(a.bias + f) == load_global(a.bias + g);
+        return load_global(row + f) == load_global(row + g) && bias_of(a.bias, f) == bias_of(a.bias, g);
       };
       const float after = __shfl_down_sync(0xFFFFFFFFu, value, 1, 8), lo = l + 1 < a.topk ? after : next;
       const bool close = here && lo == lo && !apart(value, lo);

@@ -176,6 +176,10 @@ __device__ __noinline__ double softmax_total64(const float* row, int E, int l, f
   return total;
 }
 
+// An expert's bias, a NaN as -inf: no value of the choice is a NaN, which would stand at
+// the head of a list and hide what is behind it.
+__device__ __forceinline__ float bias_of(const float* bias, int e) { return fmaxf(load_global(bias + e), -INFINITY); }
+
 // Two values in doubles, side by side: a dependent double operation takes some 100
 // cycles on this GPU.  (top and total: of a softmax)
 template <bool SOFT>
@@ -194,7 +198,7 @@ template <int LANES, bool SOFT>
 __device__ __noinline__ int2 order64(const float* row, const float* bias, int e, int out, int l, int topk, float top, double total) {
   const bool here = l < topk;
   const int mine = here ? e : 0, f = out >= 0 ? out : 0;
-  const double2 d = biased_scores64<SOFT>(load_global(row + mine), load_global(bias + mine), load_global(row + f), load_global(bias + f), top, total);
+  const double2 d = biased_scores64<SOFT>(load_global(row + mine), bias_of(bias, mine), load_global(row + f), bias_of(bias, f), top, total);
   auto first = [](double u, int i, double v, int k) { return u > v || (u == v && i < k); };
   int2 place = make_int2(out >= 0 && first(d.y, out, d.x, e), 0);
   for (int j = 0; j < topk; ++j) {
@@ -235,8 +239,8 @@ __device__ __noinline__ void choose64(const GroupGateArgs& a, const float* row, 
   unsigned long long c[MINE];  // experts l, l + LPT, ...
 #pragma unroll 4
   for (int e = l, i = 0; e < a.E; e += LPT, ++i) {
-    const double x = logit(e), v = a.bias != nullptr ? score(x) + static_cast<double>(load_global(a.bias + e)) : x;
-    c[i] = v != v ? LEAST : order_of(v);
+    const double x = logit(e);
+    c[i] = order_of(a.bias != nullptr ? score(x) + static_cast<double>(bias_of(a.bias, e)) : x);
   }
   uint32_t in = 0xFFFFFFFFu;
   if (a.kept < a.G) {

@@ -56,7 +56,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
   wait_for_previous();
   if constexpr (BIASED) {
     for (int p = threadIdx.x; p < wide; p += GG_THREADS)
-      bias[p] = p < places && p - group_of(p) * a.np < a.n ? load_global(a.bias + id_of(p)) : -INFINITY;
+      bias[p] = p < places && p - group_of(p) * a.np < a.n ? bias_of(a.bias, id_of(p)) : -INFINITY;
     __syncthreads();
   }
   auto fetch = [&](long long at, float* dst) {
