@@ -202,11 +202,10 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
       for (int j = l; j < a.topk; j += LPT) peak = fmaxf(peak, chosen(j));
       peak = O::maxf(peak);
     }
-    // renormalised sigmoids are scaled by e^-min(peak, 0): very low scores still have shares
     auto weight = [&](float x) {
       if (a.renorm && (a.softmax ? isinf(peak) : peak == -INFINITY)) return x == peak ? 1.0f : 0.0f;
       if (a.softmax) return a.renorm ? expf(x - peak) : isinf(top) ? soft(x) : expf(x - top);
-      return expf(fminf(x, 0.0f) - (a.renorm ? fminf(peak, 0.0f) : 0.0f)) / (1.0f + expf(-fabsf(x)));
+      return sigmoid_share(x, a.renorm ? peak : 0.0f);
     };
     float sum = a.softmax ? total : 1.0f;
     if (a.renorm) {
@@ -572,7 +571,7 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
       const float from = a.renorm ? peak : top;
       w = isinf(from) ? (x == from ? 1.0f : 0.0f) : expf(x - from);
     } else {
-      w = !a.renorm || peak > -64.0f ? rcp(1.0f + expf(-x)) : peak == -INFINITY ? 1.0f : expf(x - peak);
+      w = peak == -INFINITY ? 1.0f : sigmoid_share(x, peak);
     }
     w = here ? w : 0.0f;
     const float sum = a.renorm ? O::sum(w) : total;

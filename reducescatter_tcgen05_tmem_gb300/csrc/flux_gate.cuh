@@ -58,6 +58,14 @@ __device__ __forceinline__ float rcp(float x) {
   return r;
 }
 
+// sigmoid(x) e^-min(peak, 0), what a chosen score brings to renormalised weights whose
+// largest logit is peak; sigmoid(x) with a peak of 0.  1 + e^-|x| is at most 2: rcp of 1 +
+// e^-x would be 0 for logits below -87, whose shares fp32 still holds.  (rcp: to one unit
+// in the last place, where a rounded quotient costs eight times as much)
+__device__ __forceinline__ float sigmoid_share(float x, float peak) {
+  return expf(fminf(x, 0.0f) - fminf(peak, 0.0f)) * rcp(1.0f + expf(-fabsf(x)));
+}
+
 // Unsigned numbers in the order of the floats (no NaN; 0 is below all of them).
 __device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);  // -0 becomes 0

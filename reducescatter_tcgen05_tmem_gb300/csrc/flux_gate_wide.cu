@@ -383,8 +383,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
         __syncwarp();
       }
     }
-    // The weights, with the rules of group_gate_kernel.  rcp: to one unit in the last
-    // place, where a rounded quotient costs eight times as much.
+    // The weights, with the rules of group_gate_kernel.
     auto logit = [&](int e) { return fmaxf(raw[e], -INFINITY); };
     float peak = 0.0f;
     auto weight = [&](float x) {
@@ -392,9 +391,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
         if (a.renorm) return isinf(peak) ? (x == peak ? 1.0f : 0.0f) : expf(x - peak);
         return isinf(top) ? (x == top ? 1.0f : 0.0f) : expf(x - top);
       } else {
-        if (!a.renorm || peak > -64.0f) return rcp(1.0f + expf(-x));
-        if (peak == -INFINITY) return 1.0f;
-        return expf(x - peak);  // so low that 1 + e^x is 1
+        return peak == -INFINITY ? 1.0f : sigmoid_share(x, peak);
       }
     };
     int32_t* ids = a.ids + static_cast<size_t>(t) * a.topk;
