@@ -612,8 +612,11 @@ group_gate_bwd_chosen_kernel(const __grid_constant__ GroupGateArgs a) {
     if (t < a.T && l < a.topk) {
       id = load_global(a.ids_in + t * a.topk + l);
       if (id >= a.E) id = -1;
-      g = a.scale * load_global(a.dweights + t * a.topk + l);
-      if (id >= 0) x = fmaxf(load_global(a.logits + t * a.E + id), -INFINITY);
+      const float up = a.scale * load_global(a.dweights + t * a.topk + l);
+      if (id >= 0) {  // (what lies beside another id may be anything)
+        g = up;
+        x = fmaxf(load_global(a.logits + t * a.E + id), -INFINITY);
+      }
     }
     if (!a.accumulate) {
       float* rows = a.dlogits + t0 * a.E;
@@ -675,7 +678,8 @@ group_gate_bwd_kernel(const __grid_constant__ GroupGateArgs a) {
     auto load = [&](int j) {
       const int e = load_global(a.ids_in + t * a.topk + j);
       const float g = a.scale * load_global(a.dweights + t * a.topk + j);
-      return Slot{e < a.E ? e : -1, g, e >= 0 && e < a.E ? fmaxf(load_global(row + e), -INFINITY) : -INFINITY};
+      // (what lies beside an id outside the experts may be anything)
+      return e >= 0 && e < a.E ? Slot{e, g, fmaxf(load_global(row + e), -INFINITY)} : Slot{-1, 0.0f, -INFINITY};
     };
     // a lane's first slot is on its way before the row is worked on
     const Slot first = l < a.topk ? load(l) : Slot{-1, 0.0f, -INFINITY};
