@@ -384,6 +384,7 @@ layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a) {
         unpack8<DT>(slot(stage, X, v), x);
         unpack8<DT>(slot(stage, DU, v), du);
         unpack8<DT>(weight(v), w);
+        if (column(v) >= a.H) continue;  // (there (0 - m) r may be infinite where no column's n is)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const f32x2 xn = mul2(add2(x[i], minus), r2), g = mul2(du[i], w[i]);
