@@ -778,9 +778,9 @@ flux_status_t flux_layer_norm_bwd(int R, int T, int H, flux_dtype_t dtype, float
  * (experts g E/groups ..), as flux_moe_topk_gate but with
  *     s = sigmoid(logits) or softmax(logits) over all E          (score)
  *     c = s + bias, or the logits themselves without a bias: what the choice goes by
- * A group's rank is the sum of its group_top (1 or 2) largest c (of the scores
- * without a bias and with group_top 2; all of them where a group has fewer
- * experts).  The topk_groups groups of highest rank are kept, then the topk
+ * A group's rank is the sum of its group_top (1 or 2) largest c; without a bias and
+ * with group_top 2 it is the sum of its two largest scores.  A group of one expert
+ * has a sum of one.  The topk_groups groups of highest rank are kept, then the topk
  * largest c of their experts are chosen, largest first; ties go to the lowest
  * index, of groups and of experts.  The weights are
  *     scale s[id_j], or scale s[id_j] / (sum of the chosen s) with renorm

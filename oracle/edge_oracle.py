@@ -104,7 +104,7 @@ def group_gate(logits, bias, topk, score, groups, kept, top, renorm, scale):
             rank = []
             for g in range(groups):
                 mine = slice(g * n, (g + 1) * n)
-                if top == 1 or n == 1:
+                if top == 1:
                     rank.append(c[t, mine].max())
                 else:
                     v = s[t, mine] if bias is None else c[t, mine]

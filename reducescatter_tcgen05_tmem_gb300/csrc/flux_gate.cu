@@ -40,8 +40,8 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPT, sub = lane / LPT;
   using O = Over<LPT>;
   const Rows r(reinterpret_cast<char*>(smem) + (warp * TPW + sub) * gate_token_bytes(a.row, a.topk), a.row, a.topk);
-  const bool grouped = a.kept < a.G, biased = a.bias != nullptr;
-  const bool soft_row = a.softmax && (biased || !a.renorm || (grouped && a.top == 2));
+  const bool grouped = a.kept < a.G, biased = a.bias != nullptr, two = ranked_by_two(a, biased);
+  const bool soft_row = a.softmax && (biased || !a.renorm || (grouped && two));
   wait_for_previous();
   for (long long t0 = static_cast<long long>(blockIdx.x * GG_WARPS + warp) * TPW; t0 < a.T; t0 += static_cast<long long>(gridDim.x) * GG_WARPS * TPW) {
     const bool here = t0 + sub < a.T;
@@ -114,7 +114,7 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
           m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
           m1 = fmaxf(m1, o1);
         }
-        if (a.top == 2 && a.n > 1) {
+        if (two) {
           if (!biased) m1 = score(m1), m2 = score(m2);
           if (g < a.G) big = fmaxf(big, (isinf(m1) ? 0.0f : fabsf(m1)) + (isinf(m2) ? 0.0f : fabsf(m2)));
           m1 = fmaxf(m1 + m2, -INFINITY);
@@ -141,7 +141,7 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
       big = O::maxf(big);
       __syncwarp();
       // (ranks that are logits are exact)
-      if (biased || (a.top == 2 && a.n > 1))
+      if (biased || two)
         doubt = !ranks_apart(r.sorted[a.kept - 1], r.sorted[a.kept], 2.0f * unsure + 0x1p-21f * big);
     }
     const int count = a.kept * a.n;
@@ -273,7 +273,7 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
   int32_t* pick64 = reinterpret_cast<int32_t*>(mem + 32 * S) + 4 * 8;
   int32_t* kept64 = pick64 + 8;
   using O = Over<8>;
-  const bool grouped = a.kept < a.G, two = a.top == 2 && a.n > 1;
+  const bool grouped = a.kept < a.G, two = ranked_by_two(a, BIASED);
   const bool soft_row = SOFT && (BIASED || !a.renorm || (grouped && two));
   const int mine = min(a.per, max(a.E - l * a.per, 0));  // scores of this lane
   const bool full = a.per == P && a.E == 8 * P;

@@ -148,6 +148,10 @@ struct Rows {
   }
 };
 
+// Whether a group's rank is made of its two largest values.  Of a group of one there is
+// one; without a bias it goes through the same sum, as its score and not as its logit
+// (m2 is -inf, whose score is 0): logits may differ where scores are equal.
+__device__ __forceinline__ bool ranked_by_two(const GroupGateArgs& a, bool biased) { return a.top == 2 && (a.n > 1 || !biased); }
 __device__ __forceinline__ int group_of(const GroupGateArgs& a, int e) { return static_cast<int>((e * a.div_n) >> 20); }
 __device__ __forceinline__ int place(const GroupGateArgs& a, int e) { return a.pad == 0 ? e : e + group_of(a, e) * a.pad; }
 // The expert at place p of the kept groups' experts in order.
@@ -272,6 +276,8 @@ __device__ __noinline__ void choose64(const GroupGateArgs& a, const float* row, 
         const int owner = (__ffs(all) - 1) % LPT;
         const double second = value_of(largest_of(mask, l == owner ? m2 : m1));
         r = a.bias != nullptr ? r + second : score(r) + score(second);
+      } else if (ranked_by_two(a, a.bias != nullptr)) {
+        r = score(r);
       }
       if (g % LPT == l) mine[g / LPT] = r != r ? LEAST : order_of(r);
     }

@@ -35,7 +35,7 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
   int32_t* kept = pick + ((a.topk + 3) & ~3);
   float* list = reinterpret_cast<float*>(kept + 32);
   uint32_t* order = reinterpret_cast<uint32_t*>(list + LISTS * 32 * 5);
-  const bool two = a.top == 2 && a.n > 1;
+  const bool two = ranked_by_two(a, BIASED);
   const bool soft_row = SOFT && (BIASED || !a.renorm || (GROUPED && two));
   // experts and their places; a place that holds none is -inf everywhere
   const int shift = a.np - a.n, places = a.G * a.np;
