@@ -789,7 +789,7 @@ flux_status_t flux_layer_norm_bwd(int R, int T, int H, flux_dtype_t dtype, float
 
 /*   logits       device float32[T x E]
  *   bias         device float32[E], or NULL: moves the choice, not the weights; a NaN
- *                counts as -inf
+ *                counts as -inf, and so does a group's sum of +inf and -inf
  *   topk_ids     device int32[T x topk]     topk_weights  device float32[T x topk]
  * Odd rows: a NaN logit counts as -inf; softmax where the largest logit is infinite:
  * the logits equal to it share equally.  Renormalised softmax weights go by the

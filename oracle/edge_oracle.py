@@ -109,7 +109,9 @@ def group_gate(logits, bias, topk, score, groups, kept, top, renorm, scale):
                 else:
                     v = s[t, mine] if bias is None else c[t, mine]
                     rank.append(np.sort(v)[::-1][:2].sum())
-            best = np.argsort(-np.array(rank), kind="stable")[:kept]
+            rank = np.array(rank)
+            rank[np.isnan(rank)] = -np.inf  # a bias of +inf beside one of -inf
+            best = np.argsort(-rank, kind="stable")[:kept]
             pool = np.concatenate([np.arange(g * n, (g + 1) * n) for g in sorted(best)])
         else:
             pool = np.arange(E)
