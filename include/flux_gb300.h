@@ -846,8 +846,13 @@ size_t flux_q8_workspace_size(int M, int N, int K);
 /*   x  device int8[M x K]   x_scales  device float[M]
  *   w  device int8[N x K]   w_scales  device float[N]   bias  device [N] in dtype, or NULL
  *   out  device [M x N] in dtype
- * The integer sums are exact for M <= 8; for more rows as long as they stay below
- * 2^24, past that to 24 bits.  K = 0 writes the bias, or zeros. */
+ * The integer sums are exact for M <= 8.  For more rows they are fp32 sums in steps of
+ * 16 inputs: exact while sum_k |x w| stays below 2^24, beyond that every step rounds, so
+ * that a sum is off by at most some K 2^-23 of sum_k |x w| (relative to the sum itself
+ * that is more where large terms cancel; measured with large codes of one sign: 4e-5
+ * at K = 131056).  A row's bits may therefore differ between calls of 8 and of 9 rows.
+ * The sum is multiplied by the row's scale and then by the channel's, in fp32.
+ * K = 0 writes the bias, or zeros. */
 flux_status_t flux_q8_gemm(int M, int N, int K, flux_dtype_t dtype, const int8_t* x,
                            const float* x_scales, const int8_t* w, const float* w_scales,
                            const void* bias, void* out, void* workspace, size_t workspace_bytes,

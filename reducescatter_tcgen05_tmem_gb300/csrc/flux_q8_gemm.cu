@@ -1,7 +1,8 @@
 // 8-bit products of more than a few rows, on the 16-bit tensor cores: fp16 holds the
 // codes and their products exactly, and so does the fp32 sum while it stays below
 // 2^24 (always up to K = 1024; with codes of ordinary spread at every K), beyond that
-// each step of 16 rounds to 24 bits.
+// each step of 16 rounds to 24 bits, so that the error grows with K (large codes of one
+// sign: 4e-5 of the sum at K = 131056).
 //
 // out^T = w x^T: the channels are the rows of the tensor core's product and the tokens
 // its columns, of which there may be any multiple of 16, so that few tokens cost
