@@ -59,9 +59,9 @@
  *   - Workspaces must be 256-byte aligned, at least flux_*workspace_size()
  *     bytes, and zero-filled once before first use (flux_workspace_init).
  *     Every successful call leaves its workspace zero again (the MoE layers leave
- *     their routing and staged rows in it, flux_q8_gemm of more than 8 rows its
- *     widened tokens and partial sums: before a dense or MoE layer the workspace
- *     has to be zero-filled again, or that layer has one of its own).  The
+ *     their routing and staged rows in it), but for flux_q8_gemm, which leaves
+ *     widened tokens and partial sums: a dense or MoE layer has another workspace
+ *     than it, or one that was zero-filled again in between.  The
  *     block-norm, layer-norm, router, 4-bit and 8-bit calls need zeros in the
  *     first 256 bytes only.  Calls that share
  *     one workspace must be ordered on the GPU (same stream or events); calls
@@ -840,7 +840,9 @@ flux_status_t flux_q8_quantize(int rows, int K, flux_dtype_t dtype, const void* 
                                float* scales, void* stream);
 
 /* Bytes of workspace that are enough for flux_q8_gemm of up to M rows; 0 for invalid
- * sizes. */
+ * sizes.  Whatever M is, a dense or MoE layer must not be given this workspace unless it
+ * has been zero-filled again: flux_q8_gemm does not clear it, and such a layer would add
+ * onto what it finds there without an error.  The other operators may share it. */
 size_t flux_q8_workspace_size(int M, int N, int K);
 
 /*   x  device int8[M x K]   x_scales  device float[M]
