@@ -193,7 +193,7 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
       }
     }
     doubt = O::any(doubt);
-    if (doubt) choose64<LPT>(a, row, r.kept, r.pick, l, LPT == 32 ? 0xFFFFFFFFu : ((1u << LPT % 32) - 1u) << (sub * LPT));
+    if (doubt) choose64<LPT>(a, row, r.kept, r.pick, l, ((1u << LPT) - 1u) << (sub * LPT));
     __syncwarp();
     // the weights
     auto chosen = [&](int j) { return fmaxf(load_global(row + expert(j)), -INFINITY); };
