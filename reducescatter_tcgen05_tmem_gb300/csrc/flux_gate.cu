@@ -98,7 +98,6 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
     uint32_t doubt = 0;  // the groups' choice is not sure
     if (grouped) {
       const int per = LPT / a.lpg;
-      float big = 0.0f;
       for (int g0 = 0; g0 < a.G; g0 += per) {
         const int g = g0 + l / a.lpg;
         float m1 = -INFINITY, m2 = -INFINITY;
@@ -114,17 +113,19 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
           m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
           m1 = fmaxf(m1, o1);
         }
-        if (two) {
-          if (!biased) m1 = score(m1), m2 = score(m2);
-          if (g < a.G) big = fmaxf(big, (isinf(m1) ? 0.0f : fabsf(m1)) + (isinf(m2) ? 0.0f : fabsf(m2)));
-          m1 = fmaxf(m1 + m2, -INFINITY);
-        } else if (g < a.G && !isinf(m1)) {
-          big = fmaxf(big, fabsf(m1));
+        if (!two) m2 = 0.0f;
+        else if (!biased) m1 = score(m1), m2 = score(m2);
+        if (g < a.G && l % a.lpg == 0) {
+          const float rank = fmaxf(m1 + m2, -INFINITY);
+          const RankRange range(rank, m1, m2, unsure);
+          r.rank[g] = rank;
+          r.low[g] = range.low;
+          r.high[g] = range.high;
         }
-        if (g < a.G && l % a.lpg == 0) r.rank[g] = m1;
       }
       __syncwarp();
       uint32_t in = 0;
+      float low = INFINITY, high = -INFINITY;
       for (int g = l; g < a.G; g += LPT) {
         const float mine = r.rank[g];
         int pos = 0;
@@ -132,17 +133,21 @@ group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
           const float other = r.rank[o];
           pos += other > mine || (other == mine && o < g);
         }
-        r.sorted[pos] = mine;
-        if (pos < a.kept) in |= 1u << g;
+        if (pos < a.kept) {
+          in |= 1u << g;
+          low = fminf(low, r.low[g]);
+        } else {
+          high = fmaxf(high, r.high[g]);
+        }
       }
       in = O::any(in);
       for (int g = l; g < a.G; g += LPT)
         if (in >> g & 1u) r.kept[__popc(in & ((1u << g) - 1u))] = g;
-      big = O::maxf(big);
+      low = -O::maxf(-low);
+      high = O::maxf(high);
       __syncwarp();
       // (ranks that are logits are exact)
-      if (biased || two)
-        doubt = !ranks_apart(r.sorted[a.kept - 1], r.sorted[a.kept], 2.0f * unsure + 0x1p-21f * big);
+      if (biased || two) doubt = !ranks_apart(low, high);
     }
     const int count = a.kept * a.n;
     uint32_t key[NC];
@@ -377,20 +382,19 @@ group_gate_octet_kernel(const __grid_constant__ GroupGateArgs a) {
       }
       in = before < a.kept * lpg;
       if (BIASED || two) {
-        const float big = (isinf(m1) ? 0.0f : fabsf(m1)) + (isinf(m2) ? 0.0f : fabsf(m2));
-        const float last = -O::maxf(in ? -rank : -INFINITY), next = O::maxf(in ? -INFINITY : rank);
-        const float room = 2.0f * unsure + 0x1p-21f * O::maxf(big);
-        doubt = !ranks_apart(last, next, room);
+        const RankRange range(rank, m1, m2, unsure);
+        const float low = -O::maxf(in ? -range.low : -INFINITY), high = O::maxf(in ? -INFINITY : range.high);
+        doubt = !ranks_apart(low, high);
         // Groups next to the border: as in group_gate_wide_kernel.
         const bool here = doubt && !(SOFT && isinf(top));
         if (__any_sync(0xFFFFFFFFu, here)) {
           const double sum = SOFT ? softmax_total64<8>(row, a.E, l, top) : 0.0;
-          const bool near = here && (room == INFINITY || (in ? rank - next <= room : last - rank <= room));
+          const bool near = here && (in ? range.low <= high : range.high >= low);
           bool told = near;
           double exact;
           if constexpr (BIASED) {
             const int need = two ? 2 : 1;
-            const double2 d = group_rank64<SOFT>(own, bias + l * (P + 4), near ? mine : 0, (two ? m2 : m1) - room, lpg, top, inv, sum);
+            const double2 d = group_rank64<SOFT>(own, bias + l * (P + 4), near ? mine : 0, (two ? m2 : m1) - 2.0f * range.error, lpg, top, inv, sum);
             told = near && d.y == need;
             exact = d.x;
           } else {

@@ -43,9 +43,9 @@ constexpr int GG_WARPS = 8, GG_THREADS = GG_WARPS * 32;
 constexpr int GG_SMS = 152;
 constexpr float G_LOG2E = 1.4426950408889634f;
 
-// What a token needs in shared memory: its values, the picked experts, the groups'
-// ranks, the ranks in order, the kept groups.
-__host__ __device__ inline size_t gate_token_bytes(int row, int topk) { return static_cast<size_t>(row + topk + 3 * 32) * 4; }
+// What a token needs in shared memory: its values, the picked experts, the groups' ranks
+// and the ends of their ranges, the kept groups.
+__host__ __device__ inline size_t gate_token_bytes(int row, int topk) { return static_cast<size_t>(row + topk + 4 * 32) * 4; }
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -108,12 +108,24 @@ struct Over {
   }
 };
 
-// Whether the last kept group and the first one left out are told apart by their fp32
-// ranks: by more than their errors, or equal and infinite where nothing finite is so
-// large that its sum may have become so (then `room` is infinite too).
-__device__ __forceinline__ bool ranks_apart(float last, float next, float room) {
-  return last - next > room || (last == next && isinf(last) && room < INFINITY);
-}
+// Where a group's rank in doubles may lie, from its fp32 rank and the largest values
+// that make it (m2 0 where there is one): both values' errors, and their own and the
+// sum's rounding.  By the group's own values: a group that is masked with the type's
+// lowest value must not widen the others' ranges (131072 tokens with two such groups
+// of eight took 2.1 ms that way, every one of them by its choice in doubles; 87 us).  A sum
+// that passes fp32 lies past 3.4e38; an infinite value is one in doubles too.
+struct RankRange {
+  float error, low, high;
+  __device__ __forceinline__ RankRange(float rank, float m1, float m2, float unsure) {
+    error = fmaf(0x1p-22f, isinf(m1) ? 0.0f : fabsf(m1), fmaf(0x1p-22f, isinf(m2) ? 0.0f : fabsf(m2), unsure));
+    const bool past = isinf(rank) && !isinf(m1) && !isinf(m2);
+    low = past && rank > 0.0f ? 3.4e38f : rank - error;
+    high = past && rank < 0.0f ? -3.4e38f : rank + error;
+  }
+};
+// Whether the kept groups, of which `low` is the least end of a range, and those left out,
+// of which `high` is the greatest, are told apart: equal infinite ones are by index.
+__device__ __forceinline__ bool ranks_apart(float low, float high) { return low > high || (low == high && isinf(low)); }
 
 // f(e, logit) for the lane's experts of a row, a NaN as -inf.
 template <int LPT, typename F>
@@ -137,14 +149,15 @@ __device__ __forceinline__ void each_logit(const float* row, int E, int l, F&& f
 struct Rows {
   float* val;
   int32_t* pick;
-  float *rank, *sorted;
+  float *rank, *low, *high;
   int32_t* kept;
   __device__ __forceinline__ Rows(char* base, int row, int topk) {
     val = reinterpret_cast<float*>(base);
     pick = reinterpret_cast<int32_t*>(val + row);
     rank = reinterpret_cast<float*>(pick + topk);
-    sorted = rank + 32;
-    kept = reinterpret_cast<int32_t*>(sorted + 32);
+    low = rank + 32;
+    high = low + 32;
+    kept = reinterpret_cast<int32_t*>(high + 32);
   }
 };
 

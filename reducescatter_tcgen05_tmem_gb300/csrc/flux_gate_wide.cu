@@ -159,19 +159,18 @@ group_gate_wide_kernel(const __grid_constant__ GroupGateArgs a) {
       for (int o = a.lpg >> 1; o > 0; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
       bool in = g < a.G && before < a.kept;
       if (BIASED || two) {
-        const float big = g < a.G ? (isinf(m1) ? 0.0f : fabsf(m1)) + (isinf(m2) ? 0.0f : fabsf(m2)) : 0.0f;
-        const float last = -warp_largest(in ? -rank : NAN), next = warp_largest(in || g >= a.G ? NAN : rank);
-        const float room = 2.0f * unsure + 0x1p-21f * warp_largest(big);
-        doubt = !ranks_apart(last, next, room);
+        const RankRange range(rank, m1, m2, unsure);
+        const float low = -warp_largest(in ? -range.low : NAN), high = warp_largest(in || g >= a.G ? NAN : range.high);
+        doubt = !ranks_apart(low, high);
         // Groups next to the border: their ranks in doubles, from their two largest values
         // (unless a third is next to the second) or their largest, wherever they lie.
         if (doubt && !(SOFT && isinf(top))) {
           const double sum = SOFT ? softmax_total64<32>(a.logits + static_cast<size_t>(t) * a.E, a.E, lane, top) : 0.0;
-          const bool near = g < a.G && (room == INFINITY || (in ? rank - next <= room : last - rank <= room));
+          const bool near = g < a.G && (in ? range.low <= high : range.high >= low);
           bool told = near;
           double exact;
           if constexpr (BIASED) {
-            const float least = (two ? m2 : m1) - room;
+            const float least = (two ? m2 : m1) - 2.0f * range.error;
             int count = 0, e = 0, f = 0;
             if (near) {
               for (int k = 0; k < a.trips; ++k) {
