@@ -19,8 +19,9 @@
 // chooses in fp32, whose error it bounds; where two neighbours in the order, or the
 // last one in and the first one out, are closer than the bounds it takes these two,
 // or where there are more of them that token's whole choice, again in doubles.  Values
-// made from equal scores and equal biases are equal in both, so that ties cost nothing
-// extra.
+// made from equal scores and equal biases are equal in both, so that experts that tie cost
+// nothing extra.  Groups whose ranks tie do: their two largest values in doubles, or where
+// more than two are equal the whole choice (131072 x 256 of zero logits and biases 2.3 ms).
 #include "flux_gate.cuh"
 
 namespace flux {
@@ -31,7 +32,7 @@ namespace {
 // values into a row of shared memory, rank the groups from there, and take their
 // candidates (those of the kept groups, in order) into registers for topk rounds of a
 // maximum.  For long batches of what the octet form does not take: 131072 tokens, 4 of 48
-// experts in 6 of 16 groups 82 us, a warp a token 108; 10 of 16 experts 31 and 55.
+// experts in 6 of 16 groups 85 us, a warp a token 108; 10 of 16 experts 31 and 55.
 template <int NC>
 __global__ void __launch_bounds__(GG_THREADS, 5)
 group_gate_kernel(const __grid_constant__ GroupGateArgs a) {
@@ -262,7 +263,7 @@ __device__ __noinline__ double2 group_rank64(const float* logit, const float* bi
 // Four tokens to a warp: a token's scores lie in neighbouring order in eight lanes, P
 // at most in each, so that a group is one lane (or 2, 4 or 8) and most of the work is
 // in the lanes' own registers.  Lists and rounds as in group_gate_wide_kernel.
-// 131072 x 256 (8 of 256 in 4 of 8 groups) 80 us, of which the logits' bytes need 20:
+// 131072 x 256 (8 of 256 in 4 of 8 groups) 83 us, of which the logits' bytes need 20:
 // bound by issue slots (62 % busy with the 24 warps an SM that 80 registers leave) and
 // by tokens that need doubles.
 template <int P, bool SOFT, bool BIASED>

@@ -264,12 +264,12 @@ layer_norm_kernel(const __grid_constant__ LayerNormArgs a) {
 
 // Backward.  A CTA takes a stretch of consecutive rows, its teams one row each in
 // turn, with the same slots of shared memory; both sums over a row are taken at
-// once.  32768 x 4096 bf16 with a tenth dropped 227 us with the joining kernel, 5.9 TB/s
+// once.  32768 x 4096 bf16 with a tenth dropped 226 us with the joining kernel, 5.9 TB/s
 // (DRAM 75 % busy, issue slots 68 %): the weights and the column sums leave registers
 // for 24 warps an SM, which wait for one another once a row.  (Rows of more than 6144 columns leave room for one CTA an SM, whose warps all
 // wait for one another; more warps with fewer vectors make that worse: 16384 x 8192 with
 // 32 warps of one vector 308 us, with 16 of two 249, 4061 x 12288 with 24 of two 80, with
-// 16 of three 76.)  The sums of a thread's own columns over the rows (dw, db) stay in its
+// 16 of three 75.)  The sums of a thread's own columns over the rows (dw, db) stay in its
 // registers; the teams' are joined in shared memory and the CTAs' by
 // layer_norm_sums_kernel, both in a fixed order, so repeat calls give the same
 // bits.
